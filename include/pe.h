@@ -12,7 +12,8 @@
  *     host out-parameters and the host grids of pe_upload_packed and
  *     pe_download_padded. The library allocates nothing; between calls it
  *     keeps only per-device attribute caches, the process-wide wait limit
- *     (pe_set_wait_limit_ns) and the allocation-free forward's static array.
+ *     (pe_set_wait_limit_ns), the allocation-free forward's static array and
+ *     the 8-bit matrix product's status word.
  *   - Every call is asynchronous on `stream` (NULL = the legacy default
  *     stream), except pe_pack_sequences, pe_pack_document_ids and
  *     pe_flatten_packed_metadata, which perform one host read each, and the
@@ -56,6 +57,10 @@ typedef enum pe_status {
 
 typedef enum pe_dtype { PE_BF16 = 0, PE_FP32 = 1 } pe_dtype;
 
+/* 8-bit floating-point types of the 8-bit layer calls: e4m3 (largest finite
+ * value F = 448, no infinities) and e5m2 (F = 57344). */
+typedef enum pe_fp8_type { PE_E4M3 = 0, PE_E5M2 = 1 } pe_fp8_type;
+
 /* Text for a status code; never NULL. */
 const char* pe_status_string(int status);
 
@@ -66,7 +71,9 @@ const char* pe_status_string(int status);
  * later additions within 2: pe_download_padded; 3 added the device-side
  * layout check of the attention calls, pe_set_wait_limit_ns and
  * pe_read_noalloc_status; later additions within 3:
- * pe_attention_kernel_local). */
+ * pe_attention_kernel_local, pe_rmsnorm, pe_rmsnorm_fp8, pe_rmsnorm_bwd and its
+ * workspace size, pe_quantize_fp8, pe_matmul_fp8 and its workspace size,
+ * pe_read_matmul_status). */
 int pe_abi_version(void);
 
 /* ------------------------------------------------------------------------
@@ -374,6 +381,112 @@ pe_status pe_layernorm(pe_dtype dtype, const void* x, const void* residual, cons
                        void* residual_out, pe_stream_t stream);
 pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t features, void* y,
                    pe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The linear steps of a packed encoder layer in 8-bit floating point: a
+ * root-mean-square norm that writes its output in 8 bits, its backward, the
+ * quantisation of matrices, and the matrix product of quantised operands. The
+ * calls stand next to pe_layernorm and pe_geglu: asynchronous on `stream`,
+ * nothing allocated, nothing read back, capturable in a CUDA graph; I/O tensors
+ * are contiguous device memory in bf16 or fp32; arithmetic is fp32.
+ *
+ * An 8-bit matrix [R, C] is row-major with a leading dimension `ld` in bytes: a
+ * multiple of 16, >= C; its base address is a multiple of 16. Bytes C .. ld-1
+ * of a row are neither read nor written. It stands for value * scale with one
+ * fp32 scale for each block of block_rows x 128 elements (block_rows is 1 or
+ * 128; the last block of a row or column may be short). Scales are stored
+ * block column first: scales[c * RB + b] belongs to rows
+ * b * block_rows .. and columns c * 128 .., RB = ceil(R / block_rows).
+ * Quantisation of a block with largest magnitude amax (in fp32):
+ *     A = max(amax, 2^-117),  scale = A / F,
+ *     value = x * (F / A) rounded to the nearest 8-bit number, ties to even.
+ * The floor 2^-117 keeps scale and F / A normal fp32 numbers; an all-zero block
+ * holds zeros. A NaN in a block makes the whole block NaN; an infinity makes
+ * its scale infinite, so the whole block stands for NaN.
+ * ------------------------------------------------------------------------ */
+
+/* RMSNorm of num_tokens rows of `channels`: with h = x, or h = x + residual
+ * rounded to the I/O dtype (written to residual_out when that is non-NULL),
+ *     y = h / sqrt(mean(h^2) + eps) * weight.
+ * y and residual_out may be the buffers x or residual themselves.
+ * pe_rmsnorm writes y in the I/O dtype. pe_rmsnorm_fp8 writes y, unrounded, in
+ * 8 bits with 1 x 128 blocks into y8 (leading dimension y8_ld) and y8_scales
+ * [ceil(channels / 128)][num_tokens], and, when y is non-NULL, also y in the
+ * I/O dtype.
+ * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
+ * finite and > 0, NULL required pointers, residual_out without residual;
+ * PE_ERR_UNSUPPORTED for other dtypes or devices and for an 8-bit output whose
+ * address or leading dimension is not as above. */
+pe_status pe_rmsnorm(pe_dtype dtype, const void* x, const void* residual, const void* weight,
+                     int64_t num_tokens, int32_t channels, float eps, void* y, void* residual_out,
+                     pe_stream_t stream);
+pe_status pe_rmsnorm_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x,
+                         const void* residual, const void* weight, int64_t num_tokens,
+                         int32_t channels, float eps, void* y8, int64_t y8_ld, float* y8_scales,
+                         void* y, void* residual_out, pe_stream_t stream);
+
+/* RMSNorm backward. h is the normalised input as the forward stored it (x, or
+ * residual_out), dy the gradient of y, dresidual (nullable) the gradient that
+ * reaches residual_out by other ways. With n = h / sqrt(mean(h^2) + eps):
+ *     dx = (w dy - n mean(w dy n)) / sqrt(mean(h^2) + eps) (+ dresidual),
+ *     dweight[c] = sum over tokens of dy n.
+ * dx is the gradient of x and of residual alike, in the I/O dtype; it may be
+ * the buffer dy or dresidual. dweight is fp32 [channels], written (zeros when
+ * num_tokens is 0) and bitwise the same in every run. channels <= 16384, else
+ * PE_ERR_UNSUPPORTED. workspace: device, 16-byte aligned, >=
+ * pe_rmsnorm_bwd_workspace_size(channels) bytes, else PE_ERR_WORKSPACE. */
+size_t pe_rmsnorm_bwd_workspace_size(int32_t channels);
+pe_status pe_rmsnorm_bwd(pe_dtype dtype, const void* dy, const void* h, const void* weight,
+                         const void* dresidual, int64_t num_tokens, int32_t channels, float eps,
+                         void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                         pe_stream_t stream);
+
+/* Quantises x [rows, cols] (contiguous, bf16 or fp32) with blocks of
+ * block_rows x 128 (block_rows 1 or 128), as it is into y [rows, cols] with
+ * scales (skipped when y is NULL), and its transpose into yt [cols, rows] with
+ * scales_t (skipped when yt is NULL); x is read once for both. The transpose
+ * is quantised as a matrix of its own: with block_rows 1 its blocks are 128
+ * rows of x by one column; with 128 it holds y's values.
+ * Operands of pe_matmul_fp8 made this way, for Y = X W^T with X [N, K],
+ * W [M, K] and a gradient dY [N, M]:
+ *     forward          a = X (block_rows 1), b = W (128)
+ *     dX = dY W        a = dY (1), b = transposed W (128)
+ *     dW = dY^T X      a = transposed dY (1), b = transposed X (128)
+ * Errors: PE_ERR_INVALID_ARG for negative sizes, another block_rows, NULL x,
+ * NULL scales of a wanted output, or neither output wanted; PE_ERR_UNSUPPORTED
+ * for other dtypes or devices and for an output's address or leading
+ * dimension; PE_ERR_OVERFLOW for 2^31 rows or columns or more, or as many
+ * 128 x 128 tiles. */
+pe_status pe_quantize_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x, int64_t rows,
+                          int64_t cols, int32_t block_rows, void* y, int64_t y_ld, float* scales,
+                          void* yt, int64_t yt_ld, float* scales_t, pe_stream_t stream);
+
+/* Matrix product of 8-bit operands with a scale for each block of 128:
+ *     out[i, j] = sum over c of a_scales[c, i] b_scales[c, j / 128]
+ *                 (sum over l in block c of a[i, l] b[j, l]),
+ * a [m, k] with 1 x 128 blocks, b [n, k] with 128 x 128 blocks, out [m, n]
+ * contiguous in bf16 or fp32. a and b may have different 8-bit types. Products
+ * of a block are summed by the tensor cores in fp32, blocks in fp32, always in
+ * the same order: the result is bitwise the same in every run on a device. k = 0 writes
+ * zeros. out must not overlap the operands.
+ * workspace: device, 16-byte aligned, >= pe_matmul_fp8_workspace_size(m, n, k)
+ * bytes; may be NULL when that is 0. Calls that may run at the same time need
+ * one each.
+ * A pipeline wait that gives up (pe_set_wait_limit_ns) leaves out incomplete
+ * and records PE_ERR_DEVICE_TIMEOUT in the device's matrix-product status word:
+ * pe_read_matmul_status synchronizes `stream`, returns that word of the current
+ * device and sets it back to PE_OK. One word serves all calls on a device, so
+ * it tells that some product since the last read was incomplete.
+ * Errors: PE_ERR_INVALID_ARG for negative sizes or NULL pointers;
+ * PE_ERR_OVERFLOW for sizes of 2^31 or more, or as many tiles;
+ * PE_ERR_UNSUPPORTED for other types or devices, operand addresses or leading
+ * dimensions; PE_ERR_WORKSPACE. */
+size_t pe_matmul_fp8_workspace_size(int64_t m, int64_t n, int64_t k);
+pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_ld, const float* a_scales,
+                        pe_fp8_type b_type, const void* b, int64_t b_ld, const float* b_scales,
+                        int64_t m, int64_t n, int64_t k, pe_dtype out_dtype, void* out,
+                        void* workspace, size_t workspace_bytes, pe_stream_t stream);
+pe_status pe_read_matmul_status(pe_stream_t stream);
 
 /* Name of the kernel family that pe_packed_attention_fwd (backward = 0) or
  * pe_packed_attention_bwd (backward = 1) runs for these arguments (full

@@ -16,6 +16,7 @@ from .binding import (  # noqa: F401
     pe_flatten_packed_metadata,
     pe_geglu,
     pe_layernorm,
+    pe_matmul_fp8,
     pe_pack_document_ids,
     pe_pack_sequences,
     pe_packed_positions,
@@ -24,8 +25,13 @@ from .binding import (  # noqa: F401
     pe_packed_attention_fwd,
     pe_packed_attention_fwd_local,
     pe_packed_attention_fwd_noalloc,
+    pe_quantize_fp8,
     pe_read_device_status,
+    pe_read_matmul_status,
     pe_read_noalloc_status,
+    pe_rmsnorm,
+    pe_rmsnorm_bwd,
+    pe_rmsnorm_fp8,
     pe_rope_packed,
     pe_scatter_padded,
     pe_set_wait_limit_ns,

@@ -29,7 +29,9 @@ EXPORTED = (
     "pe_rows_workspace_size", "pe_pack_document_ids", "pe_flatten_packed_metadata",
     "pe_packed_positions", "pe_rope_packed", "pe_layernorm", "pe_geglu", "pe_upload_packed",
     "pe_download_padded", "pe_packed_attention_fwd_noalloc", "pe_read_noalloc_status",
-    "pe_set_wait_limit_ns", "pe_attention_kernel_local",
+    "pe_set_wait_limit_ns", "pe_attention_kernel_local", "pe_rmsnorm", "pe_rmsnorm_fp8",
+    "pe_rmsnorm_bwd_workspace_size", "pe_rmsnorm_bwd", "pe_quantize_fp8",
+    "pe_matmul_fp8_workspace_size", "pe_matmul_fp8", "pe_read_matmul_status",
 )
 
 _lib = None
@@ -115,6 +117,26 @@ def load_library(path: str = LIB_PATH):
     lib.pe_packed_attention_fwd_noalloc.argtypes = [c.c_int, i32, i64, i32, i32, i32, vp, vp, vp,
                                                     vp, c.c_float, c.c_int, vp, vp, vp]
     lib.pe_packed_attention_fwd_noalloc.restype = c.c_int
+    lib.pe_rmsnorm.argtypes = [c.c_int, vp, vp, vp, i64, i32, c.c_float, vp, vp, vp]
+    lib.pe_rmsnorm.restype = c.c_int
+    lib.pe_rmsnorm_fp8.argtypes = [c.c_int, c.c_int, vp, vp, vp, i64, i32, c.c_float, vp, i64, vp,
+                                   vp, vp, vp]
+    lib.pe_rmsnorm_fp8.restype = c.c_int
+    lib.pe_rmsnorm_bwd_workspace_size.argtypes = [i32]
+    lib.pe_rmsnorm_bwd_workspace_size.restype = sz
+    lib.pe_rmsnorm_bwd.argtypes = [c.c_int, vp, vp, vp, vp, i64, i32, c.c_float, vp, vp, vp, sz,
+                                   vp]
+    lib.pe_rmsnorm_bwd.restype = c.c_int
+    lib.pe_quantize_fp8.argtypes = [c.c_int, c.c_int, vp, i64, i64, i32, vp, i64, vp, vp, i64, vp,
+                                    vp]
+    lib.pe_quantize_fp8.restype = c.c_int
+    lib.pe_matmul_fp8_workspace_size.argtypes = [i64, i64, i64]
+    lib.pe_matmul_fp8_workspace_size.restype = sz
+    lib.pe_matmul_fp8.argtypes = [c.c_int, vp, i64, vp, c.c_int, vp, i64, vp, i64, i64, i64,
+                                  c.c_int, vp, vp, sz, vp]
+    lib.pe_matmul_fp8.restype = c.c_int
+    lib.pe_read_matmul_status.argtypes = [vp]
+    lib.pe_read_matmul_status.restype = c.c_int
     _lib = lib
     return lib
 
@@ -520,3 +542,234 @@ def pe_geglu(x: torch.Tensor, out=None) -> torch.Tensor:
     _check("pe_geglu", lib.pe_geglu(_dtype_code(x.dtype), _ptr(x), n, f2 // 2, _ptr(y),
                                     _stream(x.device)))
     return y
+
+
+# --------------------------------------------------------------------------- 8-bit layer
+
+_FP8_CODES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _fp8_code(dtype: torch.dtype) -> int:
+    code = _FP8_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: float8_e4m3fn or float8_e5m2 only")
+    return code
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """Runs one entry point on `device` and its current stream."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    if status:
+        _check(name, status)
+
+
+def _input(t: torch.Tensor, name: str, like: torch.Tensor | None = None,
+           shape=None) -> torch.Tensor:
+    """A contiguous CUDA tensor on the device and in the dtype of `like`."""
+    t = _cuda(t, name)
+    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _output(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Tensor:
+    """The caller's contiguous output tensor after a check, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not (
+            t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}")
+    return t
+
+
+def _two_dims(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _round16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def _fp8_rows_ok(t: torch.Tensor) -> bool:
+    """Rows of adjacent bytes that start at multiples of 16."""
+    rows, cols = t.shape
+    return (t.data_ptr() % 16 == 0 and (cols <= 1 or t.stride(1) == 1)
+            and (rows <= 1 or (t.stride(0) % 16 == 0 and t.stride(0) >= cols)))
+
+
+def _fp8_ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else _round16(t.shape[1])
+
+
+def _fp8_empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """An 8-bit matrix whose rows start at multiples of 16 bytes."""
+    ld = _round16(cols)
+    t = torch.empty((rows, ld), dtype=dtype, device=device)
+    return t if ld == cols else t[:, :cols]
+
+
+def _fp8_output(t: torch.Tensor | None, name: str, rows: int, cols: int, dtype, device):
+    if t is None:
+        return _fp8_empty(rows, cols, dtype, device)
+    if t.shape != (rows, cols) or t.dtype != dtype or t.device != device or not _fp8_rows_ok(t):
+        raise ValueError(f"{name} must be a {dtype} matrix of shape {(rows, cols)} on {device} "
+                         "whose rows start at multiples of 16 bytes")
+    return t
+
+
+def _fp8_operand(t: torch.Tensor, name: str) -> torch.Tensor:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    _two_dims(t, name)
+    if _fp8_rows_ok(t):
+        return t
+    return _fp8_empty(t.shape[0], t.shape[1], t.dtype, t.device).copy_(t)
+
+
+def _norm_inputs(x, weight, residual):
+    x = _input(x, "x")
+    _, c = _two_dims(x, "x")
+    weight = _cuda(weight, "weight").to(x.dtype)
+    weight = _input(weight, "weight", x, (c,))
+    if residual is not None:
+        residual = _input(residual, "residual", x, x.shape)
+    return x, weight, residual
+
+
+def pe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+               residual: torch.Tensor | None = None, out=None, residual_out=None):
+    """RMSNorm over the last dim of x [N, C]; with a residual, of h = x + residual
+    (rounded to x's dtype), returning (y, h). Otherwise returns y."""
+    x, weight, residual = _norm_inputs(x, weight, residual)
+    n, c = x.shape
+    y = _output(out, "out", x.shape, x.dtype, x.device)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    h = None if residual is None else _output(residual_out, "residual_out", x.shape, x.dtype,
+                                              x.device)
+    _call("pe_rmsnorm", x.device, _dtype_code(x.dtype), x.data_ptr(), _ptr(residual),
+          weight.data_ptr(), n, c, float(eps), y.data_ptr(), _ptr(h))
+    return y if residual is None else (y, h)
+
+
+def pe_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                   residual: torch.Tensor | None = None, dtype=torch.float8_e4m3fn, out=None,
+                   y=None, residual_out=None):
+    """RMSNorm with an 8-bit output: returns (q [N, C], scales fp32
+    [ceil(C / 128), N]), and also h = x + residual with a residual. q's rows
+    start at multiples of 16 bytes (a view of a wider matrix when C is not a
+    multiple of 16). With `y` (a tensor like x) the norm is also written there
+    in x's dtype."""
+    x, weight, residual = _norm_inputs(x, weight, residual)
+    n, c = x.shape
+    code = _fp8_code(dtype)
+    q = _fp8_output(out, "out", n, c, dtype, x.device)
+    scales = torch.empty(((c + 127) // 128, n), dtype=torch.float32, device=x.device)
+    if y is not None:
+        y = _output(y, "y", x.shape, x.dtype, x.device)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    h = None if residual is None else _output(residual_out, "residual_out", x.shape, x.dtype,
+                                              x.device)
+    _call("pe_rmsnorm_fp8", x.device, _dtype_code(x.dtype), code, x.data_ptr(), _ptr(residual),
+          weight.data_ptr(), n, c, float(eps), q.data_ptr(), _fp8_ld(q), scales.data_ptr(),
+          _ptr(y), _ptr(h))
+    return (q, scales) if residual is None else (q, scales, h)
+
+
+def pe_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                   dresidual: torch.Tensor | None = None, out=None, workspace=None):
+    """RMSNorm backward for the stored norm input h [N, C]; dresidual is the
+    gradient that reaches h by other ways. Returns (dx, dweight): dx (of x and of
+    residual alike) in h's dtype, dweight fp32 [C]."""
+    lib = load_library()
+    h = _input(h, "h")
+    n, c = _two_dims(h, "h")
+    dy = _input(dy, "dy", h, h.shape)
+    weight = _input(_cuda(weight, "weight").to(h.dtype), "weight", h, (c,))
+    if dresidual is not None:
+        dresidual = _input(dresidual, "dresidual", h, h.shape)
+    dx = _output(out, "out", h.shape, h.dtype, h.device)
+    dweight = torch.empty(c, dtype=torch.float32, device=h.device)
+    if workspace is None:
+        workspace = _workspace(lib.pe_rmsnorm_bwd_workspace_size(c), h.device)
+    _call("pe_rmsnorm_bwd", h.device, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
+          weight.data_ptr(), _ptr(dresidual), n, c, float(eps), dx.data_ptr(),
+          dweight.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return dx, dweight
+
+
+def pe_quantize_fp8(x: torch.Tensor, block_rows: int = 1, dtype=torch.float8_e4m3fn,
+                    plain: bool = True, transposed: bool = False):
+    """x [R, C] in 8 bits with one fp32 scale for each block of block_rows (1 or
+    128) x 128: (q [R, C], scales [ceil(C / 128), ceil(R / block_rows)]) when
+    `plain`, and the same of x's transpose when `transposed` (both: four
+    tensors). Rows of q start at multiples of 16 bytes."""
+    x = _input(x, "x")
+    r, c = _two_dims(x, "x")
+    code = _fp8_code(dtype)
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    if not (plain or transposed):
+        raise ValueError("neither the matrix nor its transpose is wanted")
+
+    def outputs(rows, cols):
+        return (_fp8_empty(rows, cols, dtype, x.device),
+                torch.empty(((cols + 127) // 128, -(-rows // block_rows)), dtype=torch.float32,
+                            device=x.device))
+
+    q, s = outputs(r, c) if plain else (None, None)
+    qt, st = outputs(c, r) if transposed else (None, None)
+    _call("pe_quantize_fp8", x.device, _dtype_code(x.dtype), code, x.data_ptr(), r, c,
+          block_rows, _ptr(q), _fp8_ld(q) if plain else 0, _ptr(s), _ptr(qt),
+          _fp8_ld(qt) if transposed else 0, _ptr(st))
+    return ((q, s) if plain else ()) + ((qt, st) if transposed else ())
+
+
+def pe_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                  b_scales: torch.Tensor, dtype=torch.bfloat16, out=None, workspace=None):
+    """a [M, K] times the transpose of b [N, K], both in 8 bits: a with scales of
+    1 x 128 blocks [ceil(K / 128), M], b with scales of 128 x 128 blocks
+    [ceil(K / 128), ceil(N / 128)]. Returns [M, N] in `dtype` (bfloat16 or
+    float32), or in out and its dtype."""
+    lib = load_library()
+    a, b = _fp8_operand(a, "a"), _fp8_operand(b, "b")
+    a_code, b_code = _fp8_code(a.dtype), _fp8_code(b.dtype)
+    m, k = a.shape
+    n = b.shape[0]
+    dev = a.device
+    if b.shape[1] != k or b.device != dev:
+        raise ValueError(f"a is {tuple(a.shape)} on {dev}, b is {tuple(b.shape)} on {b.device}")
+    kb = (k + 127) // 128
+    for name, s, shape in (("a_scales", a_scales, (kb, m)),
+                           ("b_scales", b_scales, (kb, (n + 127) // 128))):
+        if s.shape != shape or s.dtype != torch.float32 or s.device != dev:
+            raise ValueError(f"{name} must be float32 of shape {shape} on {dev}")
+    a_scales, b_scales = a_scales.contiguous(), b_scales.contiguous()
+    out = _output(out, "out", (m, n), dtype if out is None else out.dtype, dev)
+    if workspace is None:
+        need = lib.pe_matmul_fp8_workspace_size(m, n, k)
+        workspace = _workspace(need, dev) if need else None
+    _call("pe_matmul_fp8", dev, a_code, a.data_ptr(), _fp8_ld(a), a_scales.data_ptr(), b_code,
+          b.data_ptr(), _fp8_ld(b), b_scales.data_ptr(), m, n, k, _dtype_code(out.dtype),
+          out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out
+
+
+def pe_read_matmul_status(device=None) -> int:
+    """Status of the 8-bit matrix products on the device since the last read (0:
+    every pipeline wait completed); waits for the current stream and clears it."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else (
+        torch.device(device))
+    with torch.cuda.device(dev):
+        return int(load_library().pe_read_matmul_status(_stream(dev)))

@@ -1,0 +1,56 @@
+// 8-bit floating-point helpers of the 8-bit layer kernels (internal header).
+#pragma once
+
+#include "pe_common.cuh"
+
+namespace pe {
+
+constexpr int kFp8Block = 128;             // elements along a row that share a scale
+
+// Largest finite value of each 8-bit type.
+__host__ __device__ constexpr float fp8_largest(bool e5m2) { return e5m2 ? 57344.f : 448.f; }
+
+// Smallest block magnitude that quantisation works with: F / 2^-117 and
+// 2^-117 / F are normal fp32 numbers for both types.
+constexpr float kFp8SmallestAmax = 6.018531076210112e-36f;
+
+// max that returns NaN when either operand is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Two fp32 values rounded to 8 bits (nearest, ties to even), lo in the low byte.
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t fp8x2(float lo, float hi) {
+  uint16_t r;
+  if constexpr (kE5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
+  return fp8x2<kE5M2>(a, b) | (fp8x2<kE5M2>(c, d) << 16);
+}
+
+// The scale of a block with largest magnitude amax, and the factor that takes
+// its elements to the 8-bit range.
+template <bool kE5M2>
+__device__ __forceinline__ float fp8_scale(float amax, float& factor) {
+  const float a = max_nan(amax, kFp8SmallestAmax);
+  factor = __fdiv_rn(fp8_largest(kE5M2), a);
+  return __fdiv_rn(a, fp8_largest(kE5M2));
+}
+
+inline bool fp8_type_ok(pe_fp8_type t) { return t == PE_E4M3 || t == PE_E5M2; }
+
+// The layout every 8-bit matrix has: 16-byte aligned rows.
+inline bool fp8_layout_ok(const void* p, int64_t ld, int64_t cols) {
+  return aligned(p, 16) && ld % 16 == 0 && ld >= cols;
+}
+
+}  // namespace pe

@@ -1,0 +1,556 @@
+// RMSNorm of packed token rows, with the residual's addition and an 8-bit
+// output, and its backward.
+//   forward:  h = x, or x + residual rounded to the I/O type (stored, and
+//             normalised as stored); y = h rstd w, rstd = 1 / sqrt(mean(h^2) + eps);
+//             in 8 bits: one scale for each 128 channels of a row.
+//   backward: with n = h rstd, dx = rstd (w dy - n mean(w dy n)) (+ dresidual);
+//             dw = sum over rows of dy n.
+// All are bandwidth kernels: a row is read once, held in registers, and every
+// output written once. Statistics, products and sums are fp32.
+#include <math.h>
+
+#include "pe_fp8.cuh"
+
+namespace pe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xffffffffu;
+
+// 8-bit output of a forward: none, e4m3 or e5m2.
+enum Mode { kNoFp8 = 0, kE4M3 = 1, kE5M2 = 2 };
+
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Vec {
+  T e[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
+  return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
+  *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
+  return x;
+}
+
+template <typename T>
+struct FwdArgs {
+  const T* x;          // may be res_out or y: not read through the read-only path
+  const T* res;
+  const T* w;
+  int64_t N;
+  int32_t C;
+  float eps;
+  T* y;
+  T* res_out;
+  uint8_t* y8;
+  int64_t y8_ld;
+  float* scales;
+};
+
+// Channels of one step of a warp: U vectors of V per lane, lane-major inside a
+// vector group, so a step covers 32 V U channels and always whole blocks of
+// 128: one block for V U = 4 (32 lanes share it), two for V = 8 (16 lanes each).
+template <int V, int U>
+__device__ __forceinline__ int32_t channel(int32_t step, int u, int lane) {
+  return (step * U + u) * 32 * V + lane * V;
+}
+
+// Output of one step from its h: y in T when wanted, and the 8-bit block.
+template <typename T, int V, int U, int kMode>
+__device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t step, int lane,
+                                     const float (&h)[U * V], const Vec<T, V> (&w)[U],
+                                     float rstd) {
+  float y[U * V];
+  float amax = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      y[u * V + v] = h[u * V + v] * rstd * to_f32(w[u].e[v]);
+      amax = max_nan(amax, fabsf(y[u * V + v]));
+    }
+  }
+  if (a.y) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t c = channel<V, U>(step, u, lane);
+      if (c < a.C) {
+        Vec<T, V> o;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o.e[v] = from_f32<T>(y[u * V + v]);
+        store_vec<T, V>(a.y + t * a.C + c, o);
+      }
+    }
+  }
+  if constexpr (kMode != kNoFp8) {
+    constexpr bool e5 = kMode == kE5M2;
+    constexpr int lanes = kFp8Block / (U * V);   // lanes that share a block
+#pragma unroll
+    for (int off = lanes / 2; off > 0; off >>= 1)
+      amax = max_nan(amax, __shfl_xor_sync(kFull, amax, off));
+    float factor;
+    const float scale = fp8_scale<e5>(amax, factor);
+    const int32_t c0 = channel<V, U>(step, 0, lane);
+    if (lane % lanes == 0 && c0 < a.C)
+      a.scales[(int64_t)(c0 / kFp8Block) * a.N + t] = scale;
+    uint8_t* row = a.y8 + t * a.y8_ld;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t c = channel<V, U>(step, u, lane);
+      if (c < a.C) {
+        const float* q = y + u * V;
+        if constexpr (V == 8) {
+          uint2 o;
+          o.x = fp8x4<e5>(q[0] * factor, q[1] * factor, q[2] * factor, q[3] * factor);
+          o.y = fp8x4<e5>(q[4] * factor, q[5] * factor, q[6] * factor, q[7] * factor);
+          *reinterpret_cast<uint2*>(row + c) = o;
+        } else if constexpr (V == 4) {
+          *reinterpret_cast<uint32_t*>(row + c) =
+              fp8x4<e5>(q[0] * factor, q[1] * factor, q[2] * factor, q[3] * factor);
+        } else {
+          row[c] = (uint8_t)fp8x2<e5>(q[0] * factor, 0.f);
+        }
+      }
+    }
+  }
+}
+
+// One warp per row of up to 32 V kIter channels, held in registers: all loads
+// of a row are issued before any arithmetic.
+template <typename T, int V, int kIter, int kMode>
+__global__ void __launch_bounds__(kThreads)
+rmsnorm_row_kernel(const FwdArgs<T> a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < a.N;
+       t += warps) {
+    Vec<T, V> hv[kIter], rv[kIter], w[kIter];
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = channel<V, 1>(it, 0, lane);
+#pragma unroll
+      for (int v = 0; v < V; ++v) hv[it].e[v] = w[it].e[v] = from_f32<T>(0.f);
+      if (c < a.C) hv[it] = load_vec<T, V>(a.x + t * a.C + c);
+    }
+    if (a.res) {
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int32_t c = channel<V, 1>(it, 0, lane);
+        if (c < a.C) rv[it] = load_vec<T, V>(a.res + t * a.C + c);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = channel<V, 1>(it, 0, lane);
+      if (c < a.C) w[it] = load_vec<T, V>(a.w + c);
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = channel<V, 1>(it, 0, lane);
+      if (a.res && c < a.C) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          hv[it].e[v] = from_f32<T>(to_f32(hv[it].e[v]) + to_f32(rv[it].e[v]));
+        if (a.res_out) store_vec<T, V>(a.res_out + t * a.C + c, hv[it]);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) sq = fmaf(to_f32(hv[it].e[v]), to_f32(hv[it].e[v]), sq);
+    }
+    const float rstd = rsqrtf(warp_sum(sq) / (float)a.C + a.eps);
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      float h[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = to_f32(hv[it].e[v]);
+      const Vec<T, V> wu[1] = {w[it]};
+      emit<T, V, 1, kMode>(a, t, it, lane, h, wu, rstd);
+    }
+  }
+}
+
+// One warp per row of any width: the sum of squares, then the output, in two
+// passes over the row of which the second finds it in the caches. A lane
+// touches the same channels in both passes, so x, residual, residual_out and y
+// may share buffers (h is read back from residual_out when it is stored).
+template <typename T, int V, int kMode>
+__global__ void __launch_bounds__(kThreads)
+rmsnorm_any_kernel(const FwdArgs<T> a) {
+  constexpr int U = V == 1 ? 4 : 1;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  const int32_t steps = (a.C + 32 * V * U - 1) / (32 * V * U);
+  for (int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < a.N;
+       t += warps) {
+    const T* xr = a.x + t * a.C;
+    const T* rr = a.res ? a.res + t * a.C : nullptr;
+    T* hr = a.res_out ? a.res_out + t * a.C : nullptr;
+    float sq = 0.f;
+    for (int32_t step = 0; step < steps; ++step) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t c = channel<V, U>(step, u, lane);
+        if (c < a.C) {
+          Vec<T, V> hv = load_vec<T, V>(xr + c);
+          if (rr) {
+            const Vec<T, V> rv = load_vec<T, V>(rr + c);
+#pragma unroll
+            for (int v = 0; v < V; ++v) hv.e[v] = from_f32<T>(to_f32(hv.e[v]) + to_f32(rv.e[v]));
+            if (hr) store_vec<T, V>(hr + c, hv);
+          }
+#pragma unroll
+          for (int v = 0; v < V; ++v) sq = fmaf(to_f32(hv.e[v]), to_f32(hv.e[v]), sq);
+        }
+      }
+    }
+    const float rstd = rsqrtf(warp_sum(sq) / (float)a.C + a.eps);
+    for (int32_t step = 0; step < steps; ++step) {
+      float h[U * V];
+      Vec<T, V> w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t c = channel<V, U>(step, u, lane);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[u * V + v] = 0.f;
+          w[u].e[v] = from_f32<T>(0.f);
+        }
+        if (c < a.C) {
+          w[u] = load_vec<T, V>(a.w + c);
+          const Vec<T, V> hv = load_vec<T, V>((hr ? hr : xr) + c);
+          Vec<T, V> rv;
+          if (rr && !hr) rv = load_vec<T, V>(rr + c);
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            h[u * V + v] = rr && !hr ? to_f32(from_f32<T>(to_f32(hv.e[v]) + to_f32(rv.e[v])))
+                                     : to_f32(hv.e[v]);
+        }
+      }
+      emit<T, V, U, kMode>(a, t, step, lane, h, w, rstd);
+    }
+  }
+}
+
+unsigned row_grid(int64_t rows, int rows_per_block, int blocks_per_sm) {
+  const int64_t blocks = ceil_div(rows, rows_per_block);
+  const int64_t cap = (int64_t)device_sm_count() * blocks_per_sm;
+  return (unsigned)(blocks < cap ? blocks : cap);
+}
+
+template <typename T, int kMode>
+pe_status launch_fwd(const FwdArgs<T>& a, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.w, 16) &&
+                   (!a.y || aligned(a.y, 16)) && (!a.res || aligned(a.res, 16)) &&
+                   (!a.res_out || aligned(a.res_out, 16));
+  const unsigned grid = row_grid(a.N, kThreads / 32, 16);
+  const int64_t steps = ceil_div(a.C, 32 * V);
+  if (!vec)
+    rmsnorm_any_kernel<T, 1, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else if (steps <= 1)
+    rmsnorm_row_kernel<T, V, 1, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else if (steps <= 2)
+    rmsnorm_row_kernel<T, V, 2, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else if (steps <= 3)
+    rmsnorm_row_kernel<T, V, 3, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else if (steps <= 4)
+    rmsnorm_row_kernel<T, V, 4, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else if (steps <= 6)
+    rmsnorm_row_kernel<T, V, 6, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else if (steps <= 9)
+    rmsnorm_row_kernel<T, V, 9, kMode><<<grid, kThreads, 0, stream>>>(a);
+  else
+    rmsnorm_any_kernel<T, V, kMode><<<grid, kThreads, 0, stream>>>(a);
+  PE_CUDA_TRY(cudaGetLastError());
+  return PE_OK;
+}
+
+template <typename T>
+pe_status run_fwd(int mode, const void* x, const void* res, const void* w, int64_t N, int32_t C,
+                  float eps, void* y8, int64_t y8_ld, float* scales, void* y, void* res_out,
+                  cudaStream_t stream) {
+  const FwdArgs<T> a = {static_cast<const T*>(x),
+                        static_cast<const T*>(res),
+                        static_cast<const T*>(w),
+                        N,
+                        C,
+                        eps,
+                        static_cast<T*>(y),
+                        static_cast<T*>(res_out),
+                        static_cast<uint8_t*>(y8),
+                        y8_ld,
+                        scales};
+  if (mode == kE4M3) return launch_fwd<T, kE4M3>(a, stream);
+  if (mode == kE5M2) return launch_fwd<T, kE5M2>(a, stream);
+  return launch_fwd<T, kNoFp8>(a, stream);
+}
+
+// ---------------------------------------------------------------- backward
+constexpr int32_t kBwdMaxChannels = 16384;
+constexpr int kBwdMaxBlocks = 320;
+
+template <typename T>
+struct BwdArgs {
+  const T* dy;         // may be dx: not read through the read-only path
+  const T* h;
+  const T* w;
+  const T* dres;
+  int64_t N;
+  int32_t C;
+  float eps;
+  T* dx;
+  float* part;         // [gridDim.x][C] sums of this block's rows
+};
+
+// kGroup threads per row (a warp, or the whole block), each with kIter vectors
+// of V channels, the same for all of its rows: the weight's gradient stays in
+// fp32 registers until the block's last row. Blocks of warps add their warps'
+// sums in warp order.
+template <typename T, int V, int kIter, int kGroup>
+__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads)
+rmsnorm_bwd_kernel(const BwdArgs<T> a) {
+  constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
+  constexpr int kGroups = kBlock / kGroup;
+  extern __shared__ float sums[];            // kGroup == 32: [C]
+  __shared__ float2 red[2][kBlock / 32];
+  const int g = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
+  float dw[kIter * V];
+#pragma unroll
+  for (int i = 0; i < kIter * V; ++i) dw[i] = 0.f;
+  int phase = 0;
+  for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < a.N;
+       t += (int64_t)gridDim.x * kGroups) {
+    Vec<T, V> dyv[kIter], hv[kIter], rv[kIter], wv[kIter];
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) dyv[it].e[v] = hv[it].e[v] = wv[it].e[v] = from_f32<T>(0.f);
+      if (c < a.C) {
+        dyv[it] = load_vec<T, V>(a.dy + t * a.C + c);
+        hv[it] = load_vec<T, V>(a.h + t * a.C + c);
+        if (a.dres) rv[it] = load_vec<T, V>(a.dres + t * a.C + c);
+        wv[it] = load_vec<T, V>(a.w + c);
+      }
+    }
+    float sq = 0.f, dot = 0.f;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float h = to_f32(hv[it].e[v]);
+        sq = fmaf(h, h, sq);
+        dot = fmaf(to_f32(dyv[it].e[v]) * to_f32(wv[it].e[v]), h, dot);
+      }
+    sq = warp_sum(sq);
+    dot = warp_sum(dot);
+    if constexpr (kGroup > 32) {             // kGroups == 1: the loop is uniform in the block
+      if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = make_float2(sq, dot);
+      __syncthreads();
+      sq = dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < kBlock / 32; ++i) {
+        sq += red[phase][i].x;
+        dot += red[phase][i].y;
+      }
+      phase ^= 1;
+    }
+    const float rstd = rsqrtf(sq / (float)a.C + a.eps);
+    const float along = rstd * (dot / (float)a.C) * rstd;   // mean(w dy n) rstd
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      if (c < a.C) {
+        Vec<T, V> o;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float dy = to_f32(dyv[it].e[v]), n = to_f32(hv[it].e[v]) * rstd;
+          float dx = rstd * (dy * to_f32(wv[it].e[v])) - n * along;
+          if (a.dres) dx += to_f32(rv[it].e[v]);
+          o.e[v] = from_f32<T>(dx);
+          dw[it * V + v] = fmaf(dy, n, dw[it * V + v]);
+        }
+        store_vec<T, V>(a.dx + t * a.C + c, o);
+      }
+    }
+  }
+  float* part = a.part + (int64_t)blockIdx.x * a.C;
+  if constexpr (kGroup > 32) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int32_t c = (it * kGroup + g) * V + v;
+        if (c < a.C) part[c] = dw[it * V + v];
+      }
+  } else {
+    for (int turn = 0; turn < kGroups; ++turn) {
+      if (group == turn) {
+#pragma unroll
+        for (int it = 0; it < kIter; ++it)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int32_t c = (it * kGroup + g) * V + v;
+            if (c < a.C) sums[c] = (turn ? sums[c] : 0.f) + dw[it * V + v];
+          }
+      }
+      __syncthreads();
+    }
+    for (int32_t c = threadIdx.x; c < a.C; c += kBlock) part[c] = sums[c];
+  }
+}
+
+// dweight[c] = the blocks' sums, added in a fixed order: 32 columns per block,
+// 32 rows of threads, each adding every 32nd block's sum.
+__global__ void __launch_bounds__(1024)
+rmsnorm_dweight_kernel(const float* __restrict__ part, int32_t blocks, int32_t C,
+                       float* __restrict__ dweight) {
+  __shared__ float sum[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int32_t c = blockIdx.x * 32 + x;
+  griddep_wait();
+  float s = 0.f;
+  if (c < C)
+    for (int32_t b = y; b < blocks; b += 32) s += part[(int64_t)b * C + c];
+  sum[y][x] = s;
+  __syncthreads();
+  s = warp_sum(sum[x][y]);
+  if (x == 0 && blockIdx.x * 32 + y < C) dweight[blockIdx.x * 32 + y] = s;
+}
+
+template <typename T, int V, int kIter, int kGroup>
+pe_status launch_bwd_kernel(const BwdArgs<T>& a, float* dweight, cudaStream_t stream) {
+  constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
+  unsigned grid = row_grid(a.N, kBlock / kGroup, kGroup > kThreads ? 1 : 2);
+  if (grid > kBwdMaxBlocks) grid = kBwdMaxBlocks;
+  const size_t smem = kGroup == 32 ? (size_t)a.C * sizeof(float) : 0;
+  rmsnorm_bwd_kernel<T, V, kIter, kGroup><<<grid, kBlock, smem, stream>>>(a);
+  PE_CUDA_TRY(cudaGetLastError());
+  return launch_after_previous(rmsnorm_dweight_kernel, dim3((unsigned)ceil_div(a.C, 32)),
+                               dim3(1024), 0, stream, (const float*)a.part, (int32_t)grid, a.C,
+                               dweight);
+}
+
+template <typename T>
+pe_status run_bwd(const void* dy, const void* h, const void* w, const void* dres, int64_t N,
+                  int32_t C, float eps, void* dx, float* dweight, void* ws,
+                  cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(T);
+  const BwdArgs<T> a = {static_cast<const T*>(dy),
+                        static_cast<const T*>(h),
+                        static_cast<const T*>(w),
+                        static_cast<const T*>(dres),
+                        N,
+                        C,
+                        eps,
+                        static_cast<T*>(dx),
+                        static_cast<float*>(ws)};
+  const bool vec = C % V == 0 && aligned(dy, 16) && aligned(h, 16) && aligned(w, 16) &&
+                   aligned(dx, 16) && (!dres || aligned(dres, 16));
+  if (vec) {
+    const int64_t warp_steps = ceil_div(C, 32 * V), block_steps = ceil_div(C, 256 * V);
+    if (warp_steps <= 1) return launch_bwd_kernel<T, V, 1, 32>(a, dweight, stream);
+    if (warp_steps <= 2) return launch_bwd_kernel<T, V, 2, 32>(a, dweight, stream);
+    if (warp_steps <= 3) return launch_bwd_kernel<T, V, 3, 32>(a, dweight, stream);
+    if (warp_steps <= 4) return launch_bwd_kernel<T, V, 4, 32>(a, dweight, stream);
+    if (block_steps <= 1) return launch_bwd_kernel<T, V, 1, 256>(a, dweight, stream);
+    if (block_steps <= 2) return launch_bwd_kernel<T, V, 2, 256>(a, dweight, stream);
+    return launch_bwd_kernel<T, V, 16 / V * 1, 1024>(a, dweight, stream);
+  }
+  const int64_t steps = ceil_div(C, 256);
+  if (steps <= 1) return launch_bwd_kernel<T, 1, 1, 256>(a, dweight, stream);
+  if (steps <= 2) return launch_bwd_kernel<T, 1, 2, 256>(a, dweight, stream);
+  if (steps <= 4) return launch_bwd_kernel<T, 1, 4, 256>(a, dweight, stream);
+  if (steps <= 9) return launch_bwd_kernel<T, 1, 9, 256>(a, dweight, stream);
+  return launch_bwd_kernel<T, 1, 16, 1024>(a, dweight, stream);
+}
+
+bool dtype_ok(pe_dtype d) { return d == PE_BF16 || d == PE_FP32; }
+
+pe_status check_fwd(pe_dtype dtype, const void* x, const void* residual, const void* weight,
+                    int64_t N, int32_t C, float eps, const void* residual_out) {
+  if (!dtype_ok(dtype)) return PE_ERR_UNSUPPORTED;
+  if (N < 0 || C < 1 || !(eps > 0.f) || !isfinite(eps)) return PE_ERR_INVALID_ARG;
+  if (N > 0 && (!x || !weight || (residual_out && !residual))) return PE_ERR_INVALID_ARG;
+  return PE_OK;
+}
+
+}  // namespace
+
+}  // namespace pe
+
+using namespace pe;
+
+extern "C" pe_status pe_rmsnorm(pe_dtype dtype, const void* x, const void* residual,
+                                const void* weight, int64_t N, int32_t C, float eps, void* y,
+                                void* residual_out, pe_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  PE_TRY(check_fwd(dtype, x, residual, weight, N, C, eps, residual_out));
+  if (N == 0) return PE_OK;
+  if (!y) return PE_ERR_INVALID_ARG;
+  if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
+  if (dtype == PE_FP32)
+    return run_fwd<float>(kNoFp8, x, residual, weight, N, C, eps, nullptr, 0, nullptr, y,
+                          residual_out, stream);
+  return run_fwd<__nv_bfloat16>(kNoFp8, x, residual, weight, N, C, eps, nullptr, 0, nullptr, y,
+                                residual_out, stream);
+}
+
+extern "C" pe_status pe_rmsnorm_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x,
+                                    const void* residual, const void* weight, int64_t N,
+                                    int32_t C, float eps, void* y8, int64_t y8_ld,
+                                    float* y8_scales, void* y, void* residual_out,
+                                    pe_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!fp8_type_ok(fp8_type)) return PE_ERR_UNSUPPORTED;
+  PE_TRY(check_fwd(dtype, x, residual, weight, N, C, eps, residual_out));
+  if (N == 0) return PE_OK;
+  if (!y8 || !y8_scales) return PE_ERR_INVALID_ARG;
+  if (!fp8_layout_ok(y8, y8_ld, C)) return PE_ERR_UNSUPPORTED;
+  if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
+  const int mode = fp8_type == PE_E5M2 ? kE5M2 : kE4M3;
+  if (dtype == PE_FP32)
+    return run_fwd<float>(mode, x, residual, weight, N, C, eps, y8, y8_ld, y8_scales, y,
+                          residual_out, stream);
+  return run_fwd<__nv_bfloat16>(mode, x, residual, weight, N, C, eps, y8, y8_ld, y8_scales, y,
+                                residual_out, stream);
+}
+
+extern "C" size_t pe_rmsnorm_bwd_workspace_size(int32_t C) {
+  return C < 1 ? 0 : (size_t)kBwdMaxBlocks * (size_t)C * sizeof(float);
+}
+
+extern "C" pe_status pe_rmsnorm_bwd(pe_dtype dtype, const void* dy, const void* h,
+                                    const void* weight, const void* dresidual, int64_t N,
+                                    int32_t C, float eps, void* dx, float* dweight,
+                                    void* workspace, size_t workspace_bytes,
+                                    pe_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!dtype_ok(dtype)) return PE_ERR_UNSUPPORTED;
+  if (N < 0 || C < 1 || !(eps > 0.f) || !isfinite(eps) || !dweight) return PE_ERR_INVALID_ARG;
+  if (C > kBwdMaxChannels) return PE_ERR_UNSUPPORTED;
+  if (N > 0) {
+    if (!dy || !h || !weight || !dx) return PE_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < pe_rmsnorm_bwd_workspace_size(C))
+      return PE_ERR_WORKSPACE;
+  }
+  if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
+  if (N == 0) {
+    PE_CUDA_TRY(cudaMemsetAsync(dweight, 0, (size_t)C * sizeof(float), stream));
+    return PE_OK;
+  }
+  if (dtype == PE_FP32)
+    return run_bwd<float>(dy, h, weight, dresidual, N, C, eps, dx, dweight, workspace, stream);
+  return run_bwd<__nv_bfloat16>(dy, h, weight, dresidual, N, C, eps, dx, dweight, workspace,
+                                stream);
+}
