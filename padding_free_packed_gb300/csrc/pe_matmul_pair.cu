@@ -13,6 +13,7 @@
 //
 //   warp 0       TMA producer (both CTAs), a ring of kStages blocks
 //   warp 1       MMA issue (first CTA of the pair)
+//   warp 2       the blocks' scales, copied ahead into a ring in shared memory
 //   warps 4-11   scaling and sums; warps 4-7 columns 0-127, 8-11 128-255
 //
 // Work: whole tiles in turn, or, where few tiles have long sums, equal runs of
@@ -32,7 +33,8 @@ using namespace sm103;
 
 constexpr int kTile = 256;
 constexpr int kRows = 128;                               // rows of a (and of b) per CTA
-constexpr int kStages = 5;
+constexpr int kStages = 4;
+constexpr int kScaleSlots = 8;                           // blocks of k whose scales are in flight
 constexpr int kThreads = 384;
 constexpr uint32_t kOperandBytes = kRows * kFp8Block;    // 16 KiB
 constexpr uint32_t kPairBytes = 4 * kOperandBytes;       // both CTAs' a and b of one block
@@ -49,8 +51,11 @@ struct alignas(1024) Smem {
   uint8_t a[kStages][kOperandBytes];
   uint8_t b[kStages][kOperandBytes];
   alignas(1024) uint8_t out[8][2 * kBoxBytes];
+  float a_scale[kScaleSlots][kRows];
+  float b_scale[kScaleSlots][2];
   uint64_t full[kStages], empty[kStages];    // full: the first CTA's serve the pair
   uint64_t acc_full[2], acc_empty[2];        // acc_empty: likewise
+  uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
   uint64_t drain;
   int32_t issued[2];                         // blocks each CTA's producer loaded (first CTA)
   int32_t aborted[2];
@@ -76,7 +81,7 @@ struct Params {
   uint64_t wait_limit_ns;
 };
 
-enum WaitSite { kSiteProducer = 71, kSiteMma = 72, kSiteEpilogue = 73 };
+enum WaitSite { kSiteProducer = 71, kSiteMma = 72, kSiteEpilogue = 73, kSiteScales = 74 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -97,7 +102,7 @@ __device__ __forceinline__ void store_cluster_i32(uint32_t addr, int32_t v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
 }
 __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
@@ -128,6 +133,20 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       " [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
+}
+
+// Four bytes to shared memory without a register on the way (zero unless `in`),
+// and an arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // kind::f8f6f4, fp32 accumulator, both operands K-major.
@@ -203,6 +222,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       mbar_init(smem_u32(&s.acc_full[i]), 1);
       mbar_init(smem_u32(&s.acc_empty[i]), 16);
     }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(smem_u32(&s.scale_full[i]), 32);
+      mbar_init(smem_u32(&s.scale_empty[i]), 8);
+    }
     mbar_init(smem_u32(&s.drain), 1);
     s.guard.abort = 0;
     s.guard.limit_ns = p.wait_limit_ns;
@@ -270,6 +293,35 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         commit_pair(smem_u32(&s.drain));
         mbar_drain_wait(smem_u32(&s.drain), 0);
       }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- scales
+      const int32_t col_blocks = (p.n + kFp8Block - 1) / kFp8Block;
+      int32_t done = 0;
+      Walk w;
+      for (bool more = w.start(p, pair, pairs); more; more = w.next(p)) {
+        const int slot = done % kScaleSlots;
+        if (!warp_wait(smem_u32(&s.scale_empty[slot]), ((done / kScaleSlots) & 1) ^ 1, guard,
+                       p.status, kSiteScales))
+          break;
+        const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
+        const int32_t row0 = rt * kTile + (int32_t)rank * kRows;
+        const float* src = p.a_scales + (int64_t)w.block * p.m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t row = row0 + i * 32 + lane;
+          copy_async4(smem_u32(&s.a_scale[slot][i * 32 + lane]), src + (row < p.m ? row : 0),
+                      row < p.m);
+        }
+        if (lane < 2) {
+          const int32_t cb = ct * 2 + lane;
+          copy_async4(smem_u32(&s.b_scale[slot][lane]),
+                      p.b_scales + (int64_t)w.block * col_blocks + (cb < col_blocks ? cb : 0),
+                      cb < col_blocks);
+        }
+        copy_async_arrive(smem_u32(&s.scale_full[slot]));
+        ++done;
+      }
+      copy_async_wait_all();
     }
     __syncwarp();
   } else {
@@ -277,28 +329,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     // ------------------------------------------------------------ scaling and sums
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
-    const int32_t col_blocks = (p.n + kFp8Block - 1) / kFp8Block;
     const int32_t row_in = (int32_t)rank * kRows + quad * 32;   // this warp's rows in the tile
     uint8_t* stage_out = s.out[warp - 4];
     const uint32_t empty0 = peer_address(smem_u32(&s.acc_empty[0]), 0);
     const uint32_t empty1 = peer_address(smem_u32(&s.acc_empty[1]), 0);
-
-    // Scales are fetched two blocks ahead, across tiles.
-    Walk ahead;
-    bool ahead_more = ahead.start(p, pair, pairs);
-    auto fetch = [&]() {
-      float v = 0.f;
-      if (ahead_more) {
-        const int32_t rt = ahead.tile / p.col_tiles, ct = ahead.tile - rt * p.col_tiles;
-        const int32_t row = rt * kTile + row_in + lane, cb = ct * 2 + half;
-        if (row < p.m && cb < col_blocks)
-          v = __ldg(p.a_scales + (int64_t)ahead.block * p.m + row) *
-              __ldg(p.b_scales + (int64_t)ahead.block * col_blocks + cb);
-        ahead_more = ahead.next(p);
-      }
-      return v;
-    };
-    float scale0 = fetch(), scale1 = fetch();
 
     uint64_t acc[64];
 #pragma unroll
@@ -311,12 +345,15 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     if (more) first_block = w.block;
     while (more) {
       const int buf = done & 1;
-      const float scale = scale0;
-      scale0 = scale1;
-      scale1 = fetch();
-      const bool ok = mbar_wait(smem_u32(&s.acc_full[buf]), (done >> 1) & 1, guard, p.status,
-                                kSiteEpilogue);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      const int slot = done % kScaleSlots;
+      if (!warp_wait(smem_u32(&s.scale_full[slot]), (done / kScaleSlots) & 1, guard, p.status,
+                     kSiteEpilogue))
+        break;
+      const float scale = s.a_scale[slot][quad * 32 + lane] * s.b_scale[slot][half];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[slot]));
+      if (!warp_wait(smem_u32(&s.acc_full[buf]), (done >> 1) & 1, guard, p.status, kSiteEpilogue))
+        break;
       tc_fence_after();
       const uint64_t scale2 = f2(scale, scale);
       uint32_t d[2][32];
