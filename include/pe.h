@@ -478,7 +478,8 @@ pe_status pe_quantize_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x, i
  * device and sets it back to PE_OK. One word serves all calls on a device, so
  * it tells that some product since the last read was incomplete.
  * Errors: PE_ERR_INVALID_ARG for negative sizes or NULL pointers;
- * PE_ERR_OVERFLOW for sizes of 2^31 - 1024 or more, or 2^27 tiles of 256 x 256;
+ * PE_ERR_OVERFLOW for sizes of 2^31 - 1024 or more, or 2^30 blocks of
+ * 256 x 256 x 128;
  * PE_ERR_UNSUPPORTED for other types or devices, operand addresses or leading
  * dimensions; PE_ERR_WORKSPACE. */
 size_t pe_matmul_fp8_workspace_size(int64_t m, int64_t n, int64_t k);

@@ -4,17 +4,22 @@
 //
 // A pair of CTAs (tcgen05 cta_group::2) works on a 256 x 256 tile: each CTA
 // loads 128 rows of a and 128 rows of b, one 128-byte block of k at a time, and
-// the pair's MMAs (M = 256, N = 256, K = 32) leave a 128 x 256 half of the
-// block's product in each CTA's tensor memory. The scales change with every
-// block of k, so a block's product cannot stay in the accumulator: eight
-// epilogue warps read it from tensor memory and add it, scaled, to fp32 sums in
-// registers (one thread: one row, 128 columns, so one scale a thread and block)
-// while the MMAs of the next block fill the other half of tensor memory.
+// the pair's MMAs (M = 256, N = 128, K = 32) leave two 128 x 128 products of the
+// block in each CTA's tensor memory, one for each 128 columns. The scales change
+// with every block of k, so a block's product cannot stay in the accumulator:
+// eight epilogue warps read it from tensor memory and add it, scaled, to fp32
+// sums in registers (one thread: one row, 128 columns, so one scale a thread and
+// block) while the MMAs of the next block fill the other half of tensor memory.
 //
 //   warp 0       TMA producer (both CTAs), a ring of kStages blocks
-//   warp 1       MMA issue (first CTA of the pair)
-//   warp 2       the blocks' scales, copied ahead into a ring in shared memory
+//   warps 1, 2   MMA issue for columns 0-127 and 128-255 (first CTA of the pair)
+//   warp 3       the blocks' scales, copied ahead into a ring in shared memory
 //   warps 4-11   scaling and sums; warps 4-7 columns 0-127, 8-11 128-255
+//
+// The two column halves are separate pipelines (accumulators, barriers, issuing
+// warp) so that a half's tensor memory is handed back as soon as its four warps
+// in both CTAs have read it: the way back through the other CTA is long, and four
+// small accumulators in flight cover it better than two large ones.
 //
 // Work: whole tiles in turn, or, where few tiles have long sums, equal runs of
 // consecutive blocks of k (a run may start and end inside a tile); a tile that
@@ -34,16 +39,18 @@ using namespace sm103;
 constexpr int kTile = 256;
 constexpr int kRows = 128;                               // rows of a (and of b) per CTA
 constexpr int kStages = 4;
-constexpr int kScaleSlots = 8;                           // blocks of k whose scales are in flight
+constexpr int kIssueWarps = 2;
+constexpr int kScaleAhead = 8;                           // blocks of k that scales are copied ahead
+constexpr int kScaleSlots = 16;
 constexpr int kThreads = 384;
 constexpr uint32_t kOperandBytes = kRows * kFp8Block;    // 16 KiB
 constexpr uint32_t kPairBytes = 4 * kOperandBytes;       // both CTAs' a and b of one block
 constexpr uint32_t kRegsLaunch = 168;
-constexpr uint32_t kRegsLow = 56, kRegsHigh = 224;
+constexpr uint32_t kRegsLow = 40, kRegsHigh = 232;
 static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kBoxBytes = 32 * 128;                 // 32 rows of 128 bytes, swizzled
+constexpr uint32_t kBoxBytes = 32 * 128;                 // 32 rows of 128 bytes
 constexpr int kMaxPairs = 80;
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 
@@ -54,14 +61,15 @@ struct alignas(1024) Smem {
   float a_scale[kScaleSlots][kRows];
   float b_scale[kScaleSlots][2];
   uint64_t full[kStages], empty[kStages];    // full: the first CTA's serve the pair
-  uint64_t acc_full[2], acc_empty[2];        // acc_empty: likewise
-  uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
-  uint64_t drain;
+  uint64_t acc_full[2][2], acc_empty[2][2];  // [column half][buffer]; acc_empty: likewise.
+                                             // acc_full counts the MMAs and the scales
+  uint64_t drain[kIssueWarps];
   int32_t issued[2];                         // blocks each CTA's producer loaded (first CTA)
   int32_t aborted[2];
   uint32_t tmem_base;
   WaitGuard guard;
 };
+static_assert(kScaleSlots >= kScaleAhead + 4, "a slot is reused only after its last reader");
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory exceeds the per-CTA limit");
 
 struct Params {
@@ -118,35 +126,38 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+// Both are executed by a whole warp with the same operands; one lane issues.
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrives once on this barrier in both CTAs when the MMAs issued so far complete.
 __device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
 }
 
-// Four bytes to shared memory without a register on the way (zero unless `in`),
-// and an arrival on `bar` when this thread's copies so far have landed.
-__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+// Four bytes to shared memory without a register on the way (zero unless `in`).
+__device__ __forceinline__ void copy_async4(void* dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(in ? 4 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void copy_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+template <int kPending>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 // kind::f8f6f4, fp32 accumulator, both operands K-major.
@@ -160,11 +171,11 @@ __host__ __device__ __forceinline__ int64_t run_start(int64_t total, int32_t pai
   return total / pairs * p + (total % pairs) * p / pairs;
 }
 
-// The blocks a pair works on, in order: (tile, block of k) pairs.
+// The work of a pair as segments (a tile and a run of its blocks of k), in order.
 struct Walk {
-  int32_t tile, block, last;      // last: one past the segment's last block
+  int32_t tile, first, last;      // last: one past the segment's last block
   int32_t stride;
-  int64_t left;                   // blocks after this segment (runs), or tiles
+  int64_t left;                   // blocks after this segment (shared tiles)
 
   // The pair's first segment; false when it has none.
   __device__ bool start(const Params& p, int32_t pair, int32_t pairs) {
@@ -173,42 +184,92 @@ struct Walk {
       const int64_t lo = run_start(total, pairs, pair), hi = run_start(total, pairs, pair + 1);
       if (lo >= hi) return false;
       tile = (int32_t)(lo / p.blocks);
-      block = (int32_t)(lo - (int64_t)tile * p.blocks);
+      first = (int32_t)(lo - (int64_t)tile * p.blocks);
       const int64_t room = hi - lo;
-      last = room < p.blocks - block ? block + (int32_t)room : p.blocks;
-      left = room - (last - block);
+      last = room < p.blocks - first ? first + (int32_t)room : p.blocks;
+      left = room - (last - first);
       return true;
     }
     stride = pairs;
     tile = pair;
-    block = 0;
+    first = 0;
     last = p.blocks;
     return tile < p.tiles;
   }
-  // Moves to the next block; false at the end of the work.
   __device__ bool next(const Params& p) {
-    if (++block < last) return true;
+    first = 0;
     if (p.shared_tiles) {
       if (left <= 0) return false;
       ++tile;
-      block = 0;
       last = left < p.blocks ? (int32_t)left : p.blocks;
       left -= last;
       return true;
     }
     tile += stride;
-    block = 0;
     return tile < p.tiles;
   }
 };
+
+// Blocks of all of the pair's segments.
+__device__ __forceinline__ int32_t pair_blocks(const Params& p, int32_t pair, int32_t pairs) {
+  if (p.shared_tiles) {
+    const int64_t total = (int64_t)p.tiles * p.blocks;
+    return (int32_t)(run_start(total, pairs, pair + 1) - run_start(total, pairs, pair));
+  }
+  return pair < p.tiles ? ((p.tiles - 1 - pair) / pairs + 1) * p.blocks : 0;
+}
+
+// The 64 registers that tensor-memory loads of the epilogue write, declared once
+// by name: a load may then be in flight across the loop's back edge, where a C++
+// variable could be copied before its data has come.
+#define PE_DECLARE_D() asm volatile(".reg .b32 pe_d<64>;")
+#define PE_D8(a, b, c, d, e, f, g, h) \
+  "pe_d" #a ", pe_d" #b ", pe_d" #c ", pe_d" #d ", pe_d" #e ", pe_d" #f ", pe_d" #g ", pe_d" #h
+// 32 columns of this thread's lane into registers 0-31, or 32-63.
+__device__ __forceinline__ void load_low(uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(0, 1, 2, 3, 4, 5, 6, 7) ", " PE_D8(
+                   8, 9, 10, 11, 12, 13, 14, 15) ", " PE_D8(16, 17, 18, 19, 20, 21, 22, 23)
+                   ", " PE_D8(24, 25, 26, 27, 28, 29, 30, 31) "}, [%0];" ::"r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void load_high(uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(
+                   32, 33, 34, 35, 36, 37, 38, 39) ", " PE_D8(40, 41, 42, 43, 44, 45, 46, 47)
+                   ", " PE_D8(48, 49, 50, 51, 52, 53, 54, 55) ", " PE_D8(
+                       56, 57, 58, 59, 60, 61, 62, 63) "}, [%0];" ::"r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+#define PE_ADD(sum, lo, hi)                                          \
+  asm volatile(                                                      \
+      "{\n\t.reg .b64 t;\n\tmov.b64 t, {pe_d" #lo ", pe_d" #hi "};\n\t" \
+      "fma.rn.f32x2 %0, t, %1, %0;\n\t}"                             \
+      : "+l"(sum)                                                    \
+      : "l"(scale2))
+// 16 pairs of sums += scale * registers 0-31, or 32-63.
+__device__ __forceinline__ void add_low(uint64_t* s, uint64_t scale2) {
+  PE_ADD(s[0], 0, 1); PE_ADD(s[1], 2, 3); PE_ADD(s[2], 4, 5); PE_ADD(s[3], 6, 7);
+  PE_ADD(s[4], 8, 9); PE_ADD(s[5], 10, 11); PE_ADD(s[6], 12, 13); PE_ADD(s[7], 14, 15);
+  PE_ADD(s[8], 16, 17); PE_ADD(s[9], 18, 19); PE_ADD(s[10], 20, 21); PE_ADD(s[11], 22, 23);
+  PE_ADD(s[12], 24, 25); PE_ADD(s[13], 26, 27); PE_ADD(s[14], 28, 29); PE_ADD(s[15], 30, 31);
+}
+__device__ __forceinline__ void add_high(uint64_t* s, uint64_t scale2) {
+  PE_ADD(s[0], 32, 33); PE_ADD(s[1], 34, 35); PE_ADD(s[2], 36, 37); PE_ADD(s[3], 38, 39);
+  PE_ADD(s[4], 40, 41); PE_ADD(s[5], 42, 43); PE_ADD(s[6], 44, 45); PE_ADD(s[7], 46, 47);
+  PE_ADD(s[8], 48, 49); PE_ADD(s[9], 50, 51); PE_ADD(s[10], 52, 53); PE_ADD(s[11], 54, 55);
+  PE_ADD(s[12], 56, 57); PE_ADD(s[13], 58, 59); PE_ADD(s[14], 60, 61); PE_ADD(s[15], 62, 63);
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_out, const Params p) {
+  PE_DECLARE_D();
   extern __shared__ uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile WaitGuard* guard = &s.guard;
@@ -216,17 +277,15 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s.acc_full[i]), 1);
-      mbar_init(smem_u32(&s.acc_empty[i]), 16);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(smem_u32(&s.acc_full[i][j]), 2);
+        mbar_init(smem_u32(&s.acc_empty[i][j]), 8);
+      }
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(smem_u32(&s.scale_full[i]), 32);
-      mbar_init(smem_u32(&s.scale_empty[i]), 8);
-    }
-    mbar_init(smem_u32(&s.drain), 1);
+    for (int i = 0; i < kIssueWarps; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     s.guard.abort = 0;
     s.guard.limit_ns = p.wait_limit_ns;
     fence_mbarrier_init();
@@ -251,77 +310,121 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     regs_release<kRegsLow>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
-      int32_t issued = 0;
+      const uint32_t full0 = peer_address(smem_u32(&s.full[0]), 0);
+      int32_t issued = 0, stage = 0;
+      uint32_t parity = 1;
+      bool ok = true;
       Walk w;
-      for (bool more = w.start(p, pair, pairs); more; more = w.next(p)) {
-        const int stage = issued % kStages;
-        const uint32_t turn = issued / kStages;
-        if (!mbar_wait(smem_u32(&s.empty[stage]), (turn & 1) ^ 1, guard, p.status, kSiteProducer))
-          break;
+      for (bool more = w.start(p, pair, pairs); more && ok; more = w.next(p)) {
         const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
-        const uint32_t bar = peer_address(smem_u32(&s.full[stage]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), kPairBytes);
-        tma_load_pair(smem_u32(s.a[stage]), &tm_a, bar, w.block * kFp8Block,
-                      rt * kTile + (int32_t)rank * kRows);
-        tma_load_pair(smem_u32(s.b[stage]), &tm_b, bar, w.block * kFp8Block,
-                      ct * kTile + (int32_t)rank * kRows);
-        ++issued;
+        const int32_t row = rt * kTile + (int32_t)rank * kRows;
+        const int32_t col = ct * kTile + (int32_t)rank * 64;   // 64 rows of each column half
+        for (int32_t block = w.first; block < w.last; ++block) {
+          ok = mbar_wait(smem_u32(&s.empty[stage]), parity, guard, p.status, kSiteProducer);
+          if (!ok) break;
+          const uint32_t bar = full0 + stage * 8;
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), kPairBytes);
+          tma_load_pair(smem_u32(s.a[stage]), &tm_a, bar, block * kFp8Block, row);
+          tma_load_pair(smem_u32(s.b[stage]), &tm_b, bar, block * kFp8Block, col);
+          tma_load_pair(smem_u32(s.b[stage]) + kOperandBytes / 2, &tm_b, bar, block * kFp8Block,
+                        col + 128);
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1;
+          }
+        }
       }
       store_cluster_i32(peer_address(smem_u32(&s.issued[rank]), 0), issued);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if ((warp == 1 || warp == 2) && rank == 0) {
       // ---------------------------------------------------------- MMA issue
-      int32_t done = 0;
-      Walk w;
-      for (bool more = w.start(p, pair, pairs); more; more = w.next(p)) {
-        const int stage = done % kStages, buf = done & 1;
-        if (!mbar_wait(smem_u32(&s.acc_empty[buf]), ((done >> 1) & 1) ^ 1, guard, p.status,
-                       kSiteMma))
-          break;
-        if (!mbar_wait(smem_u32(&s.full[stage]), (done / kStages) & 1, guard, p.status, kSiteMma))
-          break;
+      const int half = warp - 1;
+      const int32_t blocks = pair_blocks(p, pair, pairs);
+      const uint32_t full0 = smem_u32(&s.full[0]), empty0 = smem_u32(&s.empty[0]);
+      const uint32_t acc_full = smem_u32(&s.acc_full[half][0]);
+      const uint32_t acc_empty = smem_u32(&s.acc_empty[half][0]);
+      const uint64_t desc_a0 = smem_desc_sw128(smem_u32(s.a[0]), 16, 1024);
+      const uint64_t desc_b0 =
+          smem_desc_sw128(smem_u32(s.b[0]) + half * (kOperandBytes / 2), 16, 1024);
+      uint32_t stage = 0, parity = 0;
+      // Both barriers of a block are asked for while the one before is issued.
+      bool free = true, loaded = false;
+      for (int32_t i = 0; i < blocks; ++i) {
+        const uint32_t buf = i & 1;
+        if (!__all_sync(0xffffffffu, free && loaded)) {
+          if (!warp_wait(acc_empty + buf * 8, ((i >> 1) & 1) ^ 1, guard, p.status, kSiteMma)) break;
+          if (!warp_wait(full0 + stage * 8, parity, guard, p.status, kSiteMma)) break;
+        }
         tc_fence_after();
-        const uint64_t da = smem_desc_sw128(smem_u32(s.a[stage]), 16, 1024);
-        const uint64_t db = smem_desc_sw128(smem_u32(s.b[stage]), 16, 1024);
+        const uint64_t da = desc_a0 + stage * (kOperandBytes / 16);
+        const uint64_t db = desc_b0 + stage * (kOperandBytes / 16);
+        const uint32_t d = tmem + buf * kTile + half * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)        // 32 bytes of k each: 2 units of 16 bytes
-          mma_pair(tmem + buf * kTile, da + 2 * i, db + 2 * i, p.idesc, i > 0);
-        commit_pair(smem_u32(&s.empty[stage]));
-        commit_pair(smem_u32(&s.acc_full[buf]));
-        ++done;
+        for (int k = 0; k < 4; ++k)        // 32 bytes of k each: 2 units of 16 bytes
+          mma_pair(d, da + 2 * k, db + 2 * k, p.idesc, k > 0);
+        commit_pair(acc_full + buf * 8);
+        commit_pair(empty0 + stage * 8);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+        free = mbar_test_wait(acc_empty + (buf ^ 1) * 8, (((i + 1) >> 1) & 1) ^ 1);
+        loaded = mbar_test_wait(full0 + stage * 8, parity);
       }
-      if (s.guard.abort) {                 // let the MMAs in flight finish
-        commit_pair(smem_u32(&s.drain));
-        mbar_drain_wait(smem_u32(&s.drain), 0);
-      }
-    } else if (warp == 2) {
+      commit_pair(smem_u32(&s.drain[warp - 1]));   // no MMA is in flight past this
+      mbar_drain_wait(smem_u32(&s.drain[warp - 1]), 0);
+    } else if (warp == 3) {
       // ---------------------------------------------------------- scales
       const int32_t col_blocks = (p.n + kFp8Block - 1) / kFp8Block;
-      int32_t done = 0;
+      const int32_t blocks = pair_blocks(p, pair, pairs);
       Walk w;
-      for (bool more = w.start(p, pair, pairs); more; more = w.next(p)) {
-        const int slot = done % kScaleSlots;
-        if (!warp_wait(smem_u32(&s.scale_empty[slot]), ((done / kScaleSlots) & 1) ^ 1, guard,
-                       p.status, kSiteScales))
-          break;
-        const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
-        const int32_t row0 = rt * kTile + (int32_t)rank * kRows;
-        const float* src = p.a_scales + (int64_t)w.block * p.m;
+      bool more = w.start(p, pair, pairs);
+      const float* a_src = nullptr;
+      const float* b_src = nullptr;
+      bool a_in[4], b_in = false;
+      auto locate = [&]() {                // this lane's rows (and columns) in w's tile
+        const int32_t rt = w.tile / p.col_tiles, cb = 2 * (w.tile - rt * p.col_tiles) + (lane & 1);
+        const int32_t row = rt * kTile + (int32_t)rank * kRows + lane;
+        a_src = p.a_scales + (int64_t)w.first * p.m + (row < p.m ? row : 0);
+        b_src = p.b_scales + (int64_t)w.first * col_blocks + (cb < col_blocks ? cb : 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t row = row0 + i * 32 + lane;
-          copy_async4(smem_u32(&s.a_scale[slot][i * 32 + lane]), src + (row < p.m ? row : 0),
-                      row < p.m);
+        for (int i = 0; i < 4; ++i) a_in[i] = row + 32 * i < p.m;
+        b_in = cb < col_blocks;
+      };
+      if (more) locate();
+      for (int32_t i = -kScaleAhead; i < blocks; ++i) {
+        if (more) {
+          // The slot's last reader is done: that block is at least four before i,
+          // and the MMAs of block i - 2 waited for it to be read.
+          const int slot = (i + kScaleAhead) % kScaleSlots;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            copy_async4(&s.a_scale[slot][j * 32 + lane], a_src + (a_in[j] ? 32 * j : 0), a_in[j]);
+          if (lane < 2) copy_async4(&s.b_scale[slot][lane], b_src, b_in);
+          a_src += p.m;
+          b_src += col_blocks;
+          if (++w.first == w.last) {
+            more = w.next(p);
+            if (more) locate();
+          }
         }
-        if (lane < 2) {
-          const int32_t cb = ct * 2 + lane;
-          copy_async4(smem_u32(&s.b_scale[slot][lane]),
-                      p.b_scales + (int64_t)w.block * col_blocks + (cb < col_blocks ? cb : 0),
-                      cb < col_blocks);
+        copy_async_commit();
+        if (i < 0) continue;
+        copy_async_wait<kScaleAhead>();    // block i's scales are here
+        const uint32_t bar = smem_u32(&s.acc_full[0][i & 1]);
+        if (i >= 2) {                      // its turn of the barriers has begun
+          const uint32_t before = (uint32_t)((i >> 1) - 1) & 1;
+          if (!warp_wait(bar, before, guard, p.status, kSiteScales) ||
+              !warp_wait(bar + 16, before, guard, p.status, kSiteScales))
+            break;
         }
-        copy_async_arrive(smem_u32(&s.scale_full[slot]));
-        ++done;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar);
+          mbar_arrive(bar + 16);
+        }
       }
-      copy_async_wait_all();
+      copy_async_wait<0>();
     }
     __syncwarp();
   } else {
@@ -331,59 +434,58 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
     const int32_t row_in = (int32_t)rank * kRows + quad * 32;   // this warp's rows in the tile
     uint8_t* stage_out = s.out[warp - 4];
-    const uint32_t empty0 = peer_address(smem_u32(&s.acc_empty[0]), 0);
-    const uint32_t empty1 = peer_address(smem_u32(&s.acc_empty[1]), 0);
+    const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[half][0]), 0);
 
     uint64_t acc[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0ull;
     int32_t done = 0;
+    const int32_t blocks = pair_blocks(p, pair, pairs);
     Walk w;
-    int32_t first_block = 0;
-    bool more = w.start(p, pair, pairs);
     bool begins = true;                    // the segment is the pair's first
-    if (more) first_block = w.block;
-    while (more) {
-      const int buf = done & 1;
-      const int slot = done % kScaleSlots;
-      if (!warp_wait(smem_u32(&s.scale_full[slot]), (done / kScaleSlots) & 1, guard, p.status,
-                     kSiteEpilogue))
-        break;
-      const float scale = s.a_scale[slot][quad * 32 + lane] * s.b_scale[slot][half];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[slot]));
-      if (!warp_wait(smem_u32(&s.acc_full[buf]), (done >> 1) & 1, guard, p.status, kSiteEpilogue))
-        break;
-      tc_fence_after();
-      const uint64_t scale2 = f2(scale, scale);
-      uint32_t d[2][32];
-      tmem_ld32(lane_base + buf * kTile, d[0]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_wait_ld(d[c & 1]);
-        if (c < 3) {
-          tmem_ld32(lane_base + buf * kTile + 32 * (c + 1), d[(c + 1) & 1]);
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          acc[c * 16 + i] = ffma2(f2(__uint_as_float(d[c & 1][2 * i]),
-                                     __uint_as_float(d[c & 1][2 * i + 1])),
-                                  scale2, acc[c * 16 + i]);
+    if (w.start(p, pair, pairs)) {
+      int32_t block = w.first;
+      bool ok = warp_wait(smem_u32(&s.acc_full[half][0]), 0, guard, p.status, kSiteEpilogue);
+      if (ok) {
+        tc_fence_after();
+        load_low(lane_base);
+        load_high(lane_base + 32);
       }
-      ++done;
-      const int32_t tile = w.tile, block = w.block;
-      const bool ends = block + 1 == w.last;
-      more = w.next(p);
-      if (!ends) continue;
+      while (ok) {
+        const int buf = done & 1, slot = done % kScaleSlots;
+        const uint32_t src = lane_base + buf * kTile;
+        const float scale = s.a_scale[slot][quad * 32 + lane] * s.b_scale[slot][half];
+        const uint64_t scale2 = f2(scale, scale);
+        wait_loads();
+        add_low(acc, scale2);
+        load_low(src + 64);
+        add_high(acc + 16, scale2);
+        load_high(src + 96);
+        ++done;
+        // The next block's accumulator, asked for early.
+        const uint32_t next_bar = smem_u32(&s.acc_full[half][buf ^ 1]);
+        const uint32_t next_parity = (uint32_t)(done >> 1) & 1;
+        const bool more = done < blocks;
+        const bool ready = more && mbar_test_wait(next_bar, next_parity);
+        wait_loads();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty + buf * 8);
+        add_low(acc + 32, scale2);
+        if (more) {
+          ok = __all_sync(0xffffffffu, ready) ||
+               warp_wait(next_bar, next_parity, guard, p.status, kSiteEpilogue);
+          tc_fence_after();
+          if (ok) load_low(lane_base + (buf ^ 1) * kTile);
+        }
+        add_high(acc + 48, scale2);
+        if (more && ok) load_high(lane_base + (buf ^ 1) * kTile + 32);
+        if (++block < w.last) continue;
 
       // The segment's sums: a whole tile goes to out, a part to the workspace.
-      const int32_t rt = tile / p.col_tiles, ct = tile - rt * p.col_tiles;
+      const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
       const int32_t row0 = rt * kTile + row_in, col0 = ct * kTile + half * 128;
-      if (first_block != 0 || block + 1 != p.blocks) {
+      if (w.first != 0 || w.last != p.blocks) {
         const int32_t slot = 2 * pair + (begins ? 0 : 1);
         float4* part = reinterpret_cast<float4*>(p.parts + slot * kPartFloats) +
                        (rank * 64 + half * 32) * 128 + quad * 32 + lane;
@@ -396,69 +498,68 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         }
       } else if (row0 < p.m && col0 < p.n) {
         if (p.tma_store) {
+          // Boxes of 32 rows x 128 bytes (64 bf16 or 32 fp32 columns), written by TMA.
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {    // 64 columns: one bf16 box or two fp32 boxes
-            if (lane == 0 && (h == 0 || p.out_fp32)) bulk_wait_read();
-            __syncwarp();
+          for (int c = 0; c < 4; ++c) {                 // 32 columns
+            if (p.out_fp32 && c == 2) {                 // both boxes are in use
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
+            }
+            uint8_t* row = stage_out + (p.out_fp32 ? c & 1 : c >> 1) * kBoxBytes + lane * 128;
 #pragma unroll
-            for (int g = 0; g < 16; ++g) { // 4 columns
-              float x0, x1, x2, x3;
-              f2_split(acc[h * 32 + 2 * g], x0, x1);
-              f2_split(acc[h * 32 + 2 * g + 1], x2, x3);
+            for (int g = 0; g < 4; ++g) {               // 8 columns
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                f2_split(acc[c * 16 + g * 4 + i], x[2 * i], x[2 * i + 1]);
               if (p.out_fp32) {
-                *reinterpret_cast<float4*>(stage_out + (g >> 3) * kBoxBytes + lane * 128 +
-                                           (((g & 7) ^ (lane & 7)) << 4)) =
-                    make_float4(x0, x1, x2, x3);
+                *reinterpret_cast<float4*>(row + (((2 * g) ^ (lane & 7)) << 4)) =
+                    make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(row + (((2 * g + 1) ^ (lane & 7)) << 4)) =
+                    make_float4(x[4], x[5], x[6], x[7]);
               } else {
-                *reinterpret_cast<uint2*>(stage_out + h * kBoxBytes + lane * 128 +
-                                          (((g >> 1) ^ (lane & 7)) << 4) + (g & 1) * 8) =
-                    make_uint2(pack_bf16x2(x0, x1), pack_bf16x2(x2, x3));
+                *reinterpret_cast<uint4*>(row + (((c % 2 * 4 + g) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
               }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (p.out_fp32) {
-                for (int b = 0; b < 2; ++b)
-                  if (col0 + h * 64 + b * 32 < p.n)
-                    tma_store_2d(&tm_out, smem_u32(stage_out + b * kBoxBytes),
-                                 col0 + h * 64 + b * 32, row0);
-              } else if (col0 + h * 64 < p.n) {
-                tma_store_2d(&tm_out, smem_u32(stage_out + h * kBoxBytes), col0 + h * 64, row0);
+            if (p.out_fp32 || c % 2 == 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              const int32_t col = col0 + (p.out_fp32 ? c * 32 : c / 2 * 64);
+              if (lane == 0 && col < p.n) {
+                tma_store_2d(&tm_out, smem_u32(row - lane * 128), col, row0);
+                bulk_commit();
               }
-              bulk_commit();
             }
           }
         } else {
-          // Rows that start anywhere: 64 columns at a time through the stage, then
-          // a row at a time in runs of 32 columns.
+          // Rows that start anywhere: 32 columns at a time through this warp's
+          // stage, then row by row.
           const int32_t rows = p.m - row0 < 32 ? p.m - row0 : 32;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int c = 0; c < 4; ++c) {                 // 32 columns
             __syncwarp();
 #pragma unroll
-            for (int g = 0; g < 16; ++g) {
+            for (int g = 0; g < 8; ++g) {               // 4 columns
               float4 v;
-              f2_split(acc[h * 32 + 2 * g], v.x, v.y);
-              f2_split(acc[h * 32 + 2 * g + 1], v.z, v.w);
-              *reinterpret_cast<float4*>(stage_out + (g >> 3) * kBoxBytes + lane * 128 +
-                                         (((g & 7) ^ (lane & 7)) << 4)) = v;
+              f2_split(acc[c * 16 + g * 2], v.x, v.y);
+              f2_split(acc[c * 16 + g * 2 + 1], v.z, v.w);
+              *reinterpret_cast<float4*>(stage_out + lane * 128 + ((g ^ (lane & 7)) << 4)) = v;
             }
             __syncwarp();
-            for (int32_t r = 0; r < rows; ++r) {
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int32_t col = col0 + h * 64 + b * 32 + lane;
+            const int32_t col = col0 + c * 32 + lane;
+            if (col < p.n) {
+              for (int32_t r = 0; r < rows; ++r) {
                 const float v = *reinterpret_cast<const float*>(
-                    stage_out + b * kBoxBytes + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
-                    (lane & 3) * 4);
-                if (col < p.n) {
-                  const int64_t at = (int64_t)(row0 + r) * p.n + col;
-                  if (p.out_fp32)
-                    static_cast<float*>(p.out)[at] = v;
-                  else
-                    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-                }
+                    stage_out + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                const int64_t at = (int64_t)(row0 + r) * p.n + col;
+                if (p.out_fp32)
+                  static_cast<float*>(p.out)[at] = v;
+                else
+                  static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
               }
             }
           }
@@ -467,7 +568,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
       begins = false;
-      if (more) first_block = w.block;
+      if (!w.next(p)) break;
+      block = w.first;
+      }
+      wait_loads();
     }
     bulk_wait_all();
   }
@@ -618,7 +722,7 @@ pe_status matmul_pair(const MatmulFp8& q, void* workspace, DeviceStatus* status,
   PE_TRY(get_encoder_matmul());
   CUtensorMap ma, mb, mo;
   PE_TRY(make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.a, q.m, q.k, q.a_ld, kRows));
-  PE_TRY(make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.b, q.n, q.k, q.b_ld, kRows));
+  PE_TRY(make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.b, q.n, q.k, q.b_ld, kRows / 2));
   const int size = q.out_fp32 ? 4 : 2;
   const bool tma_store = aligned(q.out, 16) && (int64_t)q.n * size % 16 == 0;
   mo = ma;
@@ -642,14 +746,14 @@ pe_status matmul_pair(const MatmulFp8& q, void* workspace, DeviceStatus* status,
   p.blocks = (int32_t)ceil_div(q.k, kFp8Block);
   p.col_tiles = (int32_t)ceil_div(q.n, kTile);
   const int64_t tiles = ceil_div(q.m, kTile) * p.col_tiles;
-  if (tiles >= (1LL << 27)) return PE_ERR_OVERFLOW;
+  if (tiles * p.blocks >= (1LL << 30)) return PE_ERR_OVERFLOW;
   p.tiles = (int32_t)tiles;
   int32_t pairs = pair_count();
   p.shared_tiles = use_runs(tiles, p.blocks, pairs) ? 1 : 0;
   if (!p.shared_tiles && tiles < pairs) pairs = (int32_t)tiles;
   p.tma_store = tma_store ? 1 : 0;
   p.out_fp32 = q.out_fp32 ? 1 : 0;
-  p.idesc = idesc_fp8(256, kTile, q.a_e5m2, q.b_e5m2);
+  p.idesc = idesc_fp8(256, 128, q.a_e5m2, q.b_e5m2);
   p.out = q.out;
   p.parts = static_cast<float*>(workspace);
   p.status = status;
