@@ -397,11 +397,12 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  * 128; the last block of a row or column may be short). Scales are stored
  * block column first: scales[c * RB + b] belongs to rows
  * b * block_rows .. and columns c * 128 .., RB = ceil(R / block_rows).
- * Quantisation of a block with largest magnitude amax (in fp32):
- *     A = max(amax, 2^-117),  scale = A / F,
- *     value = x * (F / A) rounded to the nearest 8-bit number, ties to even.
- * The floor 2^-117 keeps scale and F / A normal fp32 numbers; an all-zero block
- * holds zeros. A NaN in a block makes the whole block NaN; an infinity makes
+ * Quantisation of a block with largest magnitude amax:
+ *     A = max(amax, 2^-117) for e4m3, max(amax, 2^-110) for e5m2,
+ *     scale = A / F, value = x * (F / A) rounded to the nearest 8-bit number,
+ *     ties to even,
+ * with the two quotients in fp32, scale within 2 and F / A within 3 roundings.
+ * The floor keeps both normal fp32 numbers; an all-zero block holds zeros. A NaN in a block makes the whole block NaN; an infinity makes
  * its scale infinite, so the whole block stands for NaN.
  * ------------------------------------------------------------------------ */
 

@@ -147,7 +147,14 @@ def _check(call: str, status: int):
         raise PackedAttentionError(call, status, text)
 
 
+# The handle of a device's current stream without a Stream object around it
+# (2 us a call on the GPU's host); the public way where torch lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -558,7 +565,7 @@ def _fp8_code(dtype: torch.dtype) -> int:
 
 def _call(name: str, device: torch.device, *args) -> None:
     """Runs one entry point on `device` and its current stream."""
-    fn = getattr(load_library(), name)
+    fn = getattr(_lib or load_library(), name)
     if device.index == torch.cuda.current_device():
         status = fn(*args, _stream(device))
     else:
@@ -583,7 +590,7 @@ def _output(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Te
     """The caller's contiguous output tensor after a check, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not (
+    if t.shape != shape or t.dtype != dtype or t.device != device or not (
             t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          f"{device}")
@@ -639,7 +646,8 @@ def _fp8_operand(t: torch.Tensor, name: str) -> torch.Tensor:
 def _norm_inputs(x, weight, residual):
     x = _input(x, "x")
     _, c = _two_dims(x, "x")
-    weight = _cuda(weight, "weight").to(x.dtype)
+    if weight.dtype != x.dtype:
+        weight = weight.to(x.dtype)
     weight = _input(weight, "weight", x, (c,))
     if residual is not None:
         residual = _input(residual, "residual", x, x.shape)
@@ -696,7 +704,9 @@ def pe_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps:
     h = _input(h, "h")
     n, c = _two_dims(h, "h")
     dy = _input(dy, "dy", h, h.shape)
-    weight = _input(_cuda(weight, "weight").to(h.dtype), "weight", h, (c,))
+    if weight.dtype != h.dtype:
+        weight = weight.to(h.dtype)
+    weight = _input(weight, "weight", h, (c,))
     if dresidual is not None:
         dresidual = _input(dresidual, "dresidual", h, h.shape)
     dx = _output(out, "out", h.shape, h.dtype, h.device)

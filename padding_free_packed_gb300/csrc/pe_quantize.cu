@@ -3,9 +3,11 @@
 //
 // One block of threads per 128 x 128 tile: a tile holds whole scale blocks of
 // both outputs, so nothing is shared between tiles. A warp takes 16 rows, a
-// lane 4 of the 128 columns, and the 64 values stay in registers. Row maxima are
-// warp shuffles, column maxima and the tile's maximum go through shared memory.
-// The transposed bytes are packed along a lane's 16 rows and exchanged through
+// lane 4 of the 128 columns, and the 64 values stay in registers as loaded. The
+// 16 row maxima of a warp are reduced together (each exchange halves the rows a
+// lane carries, 16 shuffles instead of 80), so one lane in two computes one row's
+// scale; column maxima and the tile's maximum go through shared memory. The
+// transposed bytes are packed along a lane's 16 rows and exchanged through
 // shared memory so that every output row is written in runs of 128 bytes.
 #include "pe_fp8.cuh"
 
@@ -32,122 +34,214 @@ struct QuantizeArgs {
   float* scales_t;     // [row tiles][cols], or [row tiles][col_tiles]
 };
 
+// Four elements of one row as loaded.
+template <typename T>
+struct Four;
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 v = {0u, 0u};
+  __device__ float get(int j) const {
+    const uint32_t w = j < 2 ? v.x : v.y;
+    return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+  }
+  __device__ void set(int j, __nv_bfloat16 x) {
+    uint32_t& w = j < 2 ? v.x : v.y;
+    w |= static_cast<uint32_t>(__bfloat16_as_ushort(x)) << (j & 1 ? 16 : 0);
+  }
+  __device__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+};
+template <>
+struct Four<float> {
+  float4 v = {0.f, 0.f, 0.f, 0.f};
+  __device__ float get(int j) const { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+  __device__ void set(int j, float x) { (j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w) = x; }
+  __device__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+};
+
+// Largest magnitudes of the same four columns over rows (bf16 pairs stay packed:
+// a maximum of bf16 numbers is one of them).
+template <typename T>
+struct FourMax;
+template <>
+struct FourMax<__nv_bfloat16> {
+  __nv_bfloat162 lo, hi;
+  static __device__ __nv_bfloat162 magnitude(uint32_t w) {
+    const uint32_t m = w & 0x7fff7fffu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&m);
+  }
+  __device__ void start(const Four<__nv_bfloat16>& x) {
+    lo = magnitude(x.v.x);
+    hi = magnitude(x.v.y);
+  }
+  __device__ void take(const Four<__nv_bfloat16>& x) {
+    lo = __hmax2_nan(lo, magnitude(x.v.x));
+    hi = __hmax2_nan(hi, magnitude(x.v.y));
+  }
+  __device__ float4 get() const {
+    return make_float4(__low2float(lo), __high2float(lo), __low2float(hi), __high2float(hi));
+  }
+  // Over the four columns.
+  __device__ float all() const {
+    const __nv_bfloat162 m = __hmax2_nan(lo, hi);
+    return max_nan(__low2float(m), __high2float(m));
+  }
+};
+template <>
+struct FourMax<float> {
+  float4 m;
+  __device__ void start(const Four<float>& x) {
+    m = make_float4(fabsf(x.v.x), fabsf(x.v.y), fabsf(x.v.z), fabsf(x.v.w));
+  }
+  __device__ void take(const Four<float>& x) {
+    m.x = max_nan(m.x, fabsf(x.v.x));
+    m.y = max_nan(m.y, fabsf(x.v.y));
+    m.z = max_nan(m.z, fabsf(x.v.z));
+    m.w = max_nan(m.w, fabsf(x.v.w));
+  }
+  __device__ float4 get() const { return m; }
+  __device__ float all() const { return max_nan(max_nan(m.x, m.y), max_nan(m.z, m.w)); }
+};
+
+// Maxima over the warp of 16 values per lane; lane l returns that of value l / 2.
+__device__ __forceinline__ float max_of_rows(float (&v)[kRowsPerWarp], int lane) {
+#pragma unroll
+  for (int rows = 8; rows >= 1; rows >>= 1) {
+    const bool upper = lane & (2 * rows);
+#pragma unroll
+    for (int i = 0; i < rows; ++i) {
+      const float give = upper ? v[i] : v[i + rows], keep = upper ? v[i + rows] : v[i];
+      v[i] = max_nan(keep, __shfl_xor_sync(kFull, give, 2 * rows));
+    }
+  }
+  return max_nan(v[0], __shfl_xor_sync(kFull, v[0], 1));
+}
+
 // kVec: a lane's 4 columns are adjacent (rows of x start at multiples of 4
 // elements); otherwise they are 32 apart and move one element at a time.
-template <typename T, bool kVec, bool kE5M2, bool kSquare>
-__global__ void __launch_bounds__(kThreads)
-quantize_kernel(const QuantizeArgs a) {
-  __shared__ float colmax[kWarps][kTile];
-  __shared__ uint4 exchange[kTile][kWarps];        // [column][16-row run], runs swizzled
+// kWhole: the tile lies inside the matrix.
+template <typename T, bool kVec, bool kE5M2, bool kSquare, bool kWhole>
+__device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt, int64_t ct,
+                                              float (*colmax)[kTile], uint4 (*exchange)[kWarps]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t rt = blockIdx.x / a.col_tiles, ct = blockIdx.x - rt * a.col_tiles;
   const int64_t r0 = rt * kTile, c0 = ct * kTile;
-  const int row_count = (int)(a.rows - r0 < kTile ? a.rows - r0 : kTile);
-  const int col_count = (int)(a.cols - c0 < kTile ? a.cols - c0 : kTile);
-  const int64_t row_tiles = (a.rows + kTile - 1) / kTile;
+  const int row_count = kWhole ? kTile : (int)(a.rows - r0 < kTile ? a.rows - r0 : kTile);
+  const int col_count = kWhole ? kTile : (int)(a.cols - c0 < kTile ? a.cols - c0 : kTile);
   const int wr = warp * kRowsPerWarp;              // this warp's first row in the tile
   auto col = [&](int j) { return kVec ? lane * 4 + j : j * 32 + lane; };
 
-  float x[kRowsPerWarp][4];
-  const T* src = static_cast<const T*>(a.x) + (r0 + wr) * a.cols + c0;
+  Four<T> x[kRowsPerWarp];
+  const T* src = static_cast<const T*>(a.x) + (r0 + wr) * a.cols + c0 + col(0);
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-    if (wr + i < row_count) {
+  for (int i = 0; i < kRowsPerWarp; ++i, src += a.cols) {
+    if (kWhole || wr + i < row_count) {
       if constexpr (kVec) {
-        if (col(0) < col_count) {                  // cols is a multiple of 4
-          if constexpr (sizeof(T) == 2) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + i * a.cols + col(0)));
-            x[i][0] = __uint_as_float(v.x << 16);
-            x[i][1] = __uint_as_float(v.x & 0xffff0000u);
-            x[i][2] = __uint_as_float(v.y << 16);
-            x[i][3] = __uint_as_float(v.y & 0xffff0000u);
-          } else {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(src + i * a.cols + col(0)));
-            x[i][0] = v.x;
-            x[i][1] = v.y;
-            x[i][2] = v.z;
-            x[i][3] = v.w;
-          }
-        }
+        if (kWhole || col(0) < col_count) x[i].load(src);   // cols is a multiple of 4
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (col(j) < col_count) x[i][j] = to_f32(src[i * a.cols + col(j)]);
+          if (kWhole || col(j) < col_count) x[i].set(j, src[32 * j]);
       }
     }
   }
 
-  float cmax[4] = {0.f, 0.f, 0.f, 0.f};            // over this warp's rows, then over the tile
-  if (kSquare || a.yt) {
+  FourMax<T> over_rows;
+  float row_max[kRowsPerWarp];
 #pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) cmax[j] = max_nan(cmax[j], fabsf(x[i][j]));
-    if constexpr (kSquare) {
-      float m = max_nan(max_nan(cmax[0], cmax[1]), max_nan(cmax[2], cmax[3]));
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, off));
-      if (lane == 0) colmax[0][warp] = m;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = max_nan(m, colmax[0][w]);
-      cmax[0] = m;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) colmax[warp][col(j)] = cmax[j];
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) cmax[j] = max_nan(cmax[j], colmax[w][col(j)]);
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (i == 0)
+      over_rows.start(x[i]);
+    else
+      over_rows.take(x[i]);
+    if constexpr (!kSquare) {
+      FourMax<T> one;
+      one.start(x[i]);
+      row_max[i] = one.all();
     }
   }
   float tile_factor = 0.f, tile_scale = 0.f;
-  if constexpr (kSquare) tile_scale = fp8_scale<kE5M2>(cmax[0], tile_factor);
+  float cmax[4];
+  if constexpr (kSquare) {
+    float m = over_rows.all();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, off));
+    if (lane == 0) colmax[0][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = max_nan(m, colmax[0][w]);
+    tile_scale = fp8_scale<kE5M2>(m, tile_factor);
+  } else if (a.yt) {
+    const float4 m = over_rows.get();
+    if constexpr (kVec) {
+      *reinterpret_cast<float4*>(&colmax[warp][lane * 4]) = m;
+    } else {
+      colmax[warp][col(0)] = m.x;
+      colmax[warp][col(1)] = m.y;
+      colmax[warp][col(2)] = m.z;
+      colmax[warp][col(3)] = m.w;
+    }
+    __syncthreads();
+  }
 
   if (a.y) {
-    if (kSquare && threadIdx.x == 0) a.scales[ct * row_tiles + rt] = tile_scale;
+    float factor = tile_factor;
+    if constexpr (kSquare) {
+      if (threadIdx.x == 0) a.scales[ct * ((a.rows + kTile - 1) / kTile) + rt] = tile_scale;
+    } else {
+      const float scale = fp8_scale<kE5M2>(max_of_rows(row_max, lane), factor);
+      const int r = wr + (lane >> 1);
+      if (!(lane & 1) && (kWhole || r < row_count)) a.scales[ct * a.rows + r0 + r] = scale;
+    }
+    uint8_t* dst = a.y + (r0 + wr) * a.y_ld + c0 + col(0);
 #pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-      float f = tile_factor;
-      if constexpr (!kSquare) {
-        float m = max_nan(max_nan(fabsf(x[i][0]), fabsf(x[i][1])),
-                          max_nan(fabsf(x[i][2]), fabsf(x[i][3])));
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, off));
-        const float scale = fp8_scale<kE5M2>(m, f);
-        if (lane == 0 && wr + i < row_count) a.scales[ct * a.rows + r0 + wr + i] = scale;
-      }
-      if (wr + i < row_count) {
-        uint8_t* dst = a.y + (r0 + wr + i) * a.y_ld + c0;
-        const uint32_t q = fp8x4<kE5M2>(x[i][0] * f, x[i][1] * f, x[i][2] * f, x[i][3] * f);
+    for (int i = 0; i < kRowsPerWarp; ++i, dst += a.y_ld) {
+      const float f = kSquare ? tile_factor : __shfl_sync(kFull, factor, 2 * i);
+      const uint32_t q = fp8x4<kE5M2>(x[i].get(0) * f, x[i].get(1) * f, x[i].get(2) * f,
+                                      x[i].get(3) * f);
+      if (kWhole || wr + i < row_count) {
         if constexpr (kVec) {
-          if (col(0) < col_count) *reinterpret_cast<uint32_t*>(dst + col(0)) = q;
+          if (kWhole || col(0) < col_count) *reinterpret_cast<uint32_t*>(dst) = q;
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (col(j) < col_count) dst[col(j)] = (uint8_t)(q >> (8 * j));
+            if (kWhole || col(j) < col_count) dst[32 * j] = (uint8_t)(q >> (8 * j));
         }
       }
     }
   }
 
   if (a.yt) {
-    if (kSquare && threadIdx.x == 0) a.scales_t[rt * a.col_tiles + ct] = tile_scale;
+    if constexpr (kSquare) {
+      if (threadIdx.x == 0) a.scales_t[rt * a.col_tiles + ct] = tile_scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cmax[j] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if constexpr (kVec) {
+          const float4 m = *reinterpret_cast<const float4*>(&colmax[w][lane * 4]);
+          cmax[0] = max_nan(cmax[0], m.x);
+          cmax[1] = max_nan(cmax[1], m.y);
+          cmax[2] = max_nan(cmax[2], m.z);
+          cmax[3] = max_nan(cmax[3], m.w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) cmax[j] = max_nan(cmax[j], colmax[w][col(j)]);
+        }
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float f = tile_factor;
       if constexpr (!kSquare) {
         const float scale = fp8_scale<kE5M2>(cmax[j], f);
-        if (warp == 0 && col(j) < col_count) a.scales_t[rt * a.cols + c0 + col(j)] = scale;
+        if (warp == 0 && (kWhole || col(j) < col_count))
+          a.scales_t[rt * a.cols + c0 + col(j)] = scale;
       }
       uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        q[i] = fp8x4<kE5M2>(x[4 * i][j] * f, x[4 * i + 1][j] * f, x[4 * i + 2][j] * f,
-                            x[4 * i + 3][j] * f);
+        q[i] = fp8x4<kE5M2>(x[4 * i].get(j) * f, x[4 * i + 1].get(j) * f, x[4 * i + 2].get(j) * f,
+                            x[4 * i + 3].get(j) * f);
       exchange[col(j)][warp ^ ((col(j) >> (kVec ? 2 : 0)) & 7)] =
           make_uint4(q[0], q[1], q[2], q[3]);
     }
@@ -155,13 +249,13 @@ quantize_kernel(const QuantizeArgs a) {
     // 8 threads per transposed row, 32 rows at a time.
     const int run = threadIdx.x & 7;
     const int run_rows = row_count - run * 16;     // valid bytes of this run
+    uint8_t* dst = a.yt + (c0 + (threadIdx.x >> 3)) * a.yt_ld + r0 + run * 16;
 #pragma unroll
-    for (int i = 0; i < kTile / 32; ++i) {
+    for (int i = 0; i < kTile / 32; ++i, dst += 32 * a.yt_ld) {
       const int c = i * 32 + (threadIdx.x >> 3);
-      if (c >= col_count) continue;
+      if (!kWhole && c >= col_count) continue;
       const uint4 v = exchange[c][run ^ ((c >> (kVec ? 2 : 0)) & 7)];
-      uint8_t* dst = a.yt + (c0 + c) * a.yt_ld + r0 + run * 16;
-      if (run_rows >= 16) {
+      if (kWhole || run_rows >= 16) {
         *reinterpret_cast<uint4*>(dst) = v;
       } else {
         const uint32_t q[4] = {v.x, v.y, v.z, v.w};
@@ -171,6 +265,18 @@ quantize_kernel(const QuantizeArgs a) {
       }
     }
   }
+}
+
+template <typename T, bool kVec, bool kE5M2, bool kSquare>
+__global__ void __launch_bounds__(kThreads)
+quantize_kernel(const QuantizeArgs a) {
+  __shared__ __align__(16) float colmax[kWarps][kTile];
+  __shared__ uint4 exchange[kTile][kWarps];        // [column][16-row run], runs swizzled
+  const int64_t rt = blockIdx.x / a.col_tiles, ct = blockIdx.x - rt * a.col_tiles;
+  if ((rt + 1) * kTile <= a.rows && (ct + 1) * kTile <= a.cols)
+    quantize_tile<T, kVec, kE5M2, kSquare, true>(a, rt, ct, colmax, exchange);
+  else
+    quantize_tile<T, kVec, kE5M2, kSquare, false>(a, rt, ct, colmax, exchange);
 }
 
 template <typename T, bool kVec, bool kE5M2>

@@ -21,18 +21,81 @@ constexpr unsigned kFull = 0xffffffffu;
 // 8-bit output of a forward: none, e4m3 or e5m2.
 enum Mode { kNoFp8 = 0, kE4M3 = 1, kE5M2 = 2 };
 
+// V consecutive elements of a row, kept as loaded: bf16 pairs stay in one register
+// until they are used.
 template <typename T, int V>
-struct alignas(V * sizeof(T)) Vec {
-  T e[V];
+struct Vec;
+template <>
+struct Vec<float, 1> {
+  float w;
+  __device__ float get(int) const { return w; }
+  __device__ void zero() { w = 0.f; }
+  __device__ void put(const float* x) { w = x[0]; }
+  __device__ void add(const Vec& o) { w += o.w; }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+  __nv_bfloat16 w;
+  __device__ float get(int) const { return __bfloat162float(w); }
+  __device__ void zero() { w = __float2bfloat16_rn(0.f); }
+  __device__ void put(const float* x) { w = __float2bfloat16_rn(x[0]); }
+  __device__ void add(const Vec& o) { w = __float2bfloat16_rn(get(0) + o.get(0)); }
+};
+template <>
+struct alignas(16) Vec<float, 4> {
+  float w[4];
+  __device__ float get(int v) const { return w[v]; }
+  __device__ void zero() { w[0] = w[1] = w[2] = w[3] = 0.f; }
+  __device__ void put(const float* x) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) w[v] = x[v];
+  }
+  __device__ void add(const Vec& o) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) w[v] += o.w[v];
+  }
+};
+template <>
+struct alignas(16) Vec<__nv_bfloat16, 8> {
+  uint32_t w[4];
+  __device__ float get(int v) const {
+    return __uint_as_float(v & 1 ? w[v >> 1] & 0xffff0000u : w[v >> 1] << 16);
+  }
+  __device__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ void put(const float* x) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const __nv_bfloat162 pair = __floats2bfloat162_rn(x[2 * v], x[2 * v + 1]);
+      w[v] = *reinterpret_cast<const uint32_t*>(&pair);
+    }
+  }
+  // The rounded fp32 sum, two at a time: an fp32 sum of bf16 numbers is exact
+  // unless one is below 2^-16 of the other, when rounding it first changes nothing.
+  __device__ void add(const Vec& o) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const __nv_bfloat162 sum = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&w[v]),
+                                            *reinterpret_cast<const __nv_bfloat162*>(&o.w[v]));
+      w[v] = *reinterpret_cast<const uint32_t*>(&sum);
+    }
+  }
 };
 
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
-  return *reinterpret_cast<const Vec<T, V>*>(p);
+  Vec<T, V> v;
+  if constexpr (V > 1)
+    *reinterpret_cast<uint4*>(v.w) = *reinterpret_cast<const uint4*>(p);
+  else
+    v.w = *p;
+  return v;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
-  *reinterpret_cast<Vec<T, V>*>(p) = v;
+  if constexpr (V > 1)
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v.w);
+  else
+    *p = v.w;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -48,6 +111,7 @@ struct FwdArgs {
   const T* w;
   int64_t N;
   int32_t C;
+  float inv_c;         // 1 / C
   float eps;
   T* y;
   T* res_out;
@@ -75,7 +139,7 @@ __device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t ste
   for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      y[u * V + v] = h[u * V + v] * rstd * to_f32(w[u].e[v]);
+      y[u * V + v] = h[u * V + v] * rstd * w[u].get(v);
       amax = max_nan(amax, fabsf(y[u * V + v]));
     }
   }
@@ -85,8 +149,7 @@ __device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t ste
       const int32_t c = channel<V, U>(step, u, lane);
       if (c < a.C) {
         Vec<T, V> o;
-#pragma unroll
-        for (int v = 0; v < V; ++v) o.e[v] = from_f32<T>(y[u * V + v]);
+        o.put(y + u * V);
         store_vec<T, V>(a.y + t * a.C + c, o);
       }
     }
@@ -127,18 +190,17 @@ __device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t ste
 // One warp per row of up to 32 V kIter channels, held in registers: all loads
 // of a row are issued before any arithmetic.
 template <typename T, int V, int kIter, int kMode>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kIter <= 4 ? 4 : 2)
 rmsnorm_row_kernel(const FwdArgs<T> a) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < a.N;
        t += warps) {
-    Vec<T, V> hv[kIter], rv[kIter], w[kIter];
+    Vec<T, V> hv[kIter], rv[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int32_t c = channel<V, 1>(it, 0, lane);
-#pragma unroll
-      for (int v = 0; v < V; ++v) hv[it].e[v] = w[it].e[v] = from_f32<T>(0.f);
+      hv[it].zero();
       if (c < a.C) hv[it] = load_vec<T, V>(a.x + t * a.C + c);
     }
     if (a.res) {
@@ -148,31 +210,27 @@ rmsnorm_row_kernel(const FwdArgs<T> a) {
         if (c < a.C) rv[it] = load_vec<T, V>(a.res + t * a.C + c);
       }
     }
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int32_t c = channel<V, 1>(it, 0, lane);
-      if (c < a.C) w[it] = load_vec<T, V>(a.w + c);
-    }
     float sq = 0.f;
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int32_t c = channel<V, 1>(it, 0, lane);
       if (a.res && c < a.C) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          hv[it].e[v] = from_f32<T>(to_f32(hv[it].e[v]) + to_f32(rv[it].e[v]));
+        hv[it].add(rv[it]);
         if (a.res_out) store_vec<T, V>(a.res_out + t * a.C + c, hv[it]);
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v) sq = fmaf(to_f32(hv[it].e[v]), to_f32(hv[it].e[v]), sq);
+      for (int v = 0; v < V; ++v) sq = fmaf(hv[it].get(v), hv[it].get(v), sq);
     }
-    const float rstd = rsqrtf(warp_sum(sq) / (float)a.C + a.eps);
+    const float rstd = rsqrtf(fmaf(warp_sum(sq), a.inv_c, a.eps));
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       float h[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = to_f32(hv[it].e[v]);
-      const Vec<T, V> wu[1] = {w[it]};
+      for (int v = 0; v < V; ++v) h[v] = hv[it].get(v);
+      const int32_t c = channel<V, 1>(it, 0, lane);
+      Vec<T, V> wu[1];
+      wu[0].zero();
+      if (c < a.C) wu[0] = load_vec<T, V>(a.w + c);
       emit<T, V, 1, kMode>(a, t, it, lane, h, wu, rstd);
     }
   }
@@ -202,17 +260,15 @@ rmsnorm_any_kernel(const FwdArgs<T> a) {
         if (c < a.C) {
           Vec<T, V> hv = load_vec<T, V>(xr + c);
           if (rr) {
-            const Vec<T, V> rv = load_vec<T, V>(rr + c);
-#pragma unroll
-            for (int v = 0; v < V; ++v) hv.e[v] = from_f32<T>(to_f32(hv.e[v]) + to_f32(rv.e[v]));
+            hv.add(load_vec<T, V>(rr + c));
             if (hr) store_vec<T, V>(hr + c, hv);
           }
 #pragma unroll
-          for (int v = 0; v < V; ++v) sq = fmaf(to_f32(hv.e[v]), to_f32(hv.e[v]), sq);
+          for (int v = 0; v < V; ++v) sq = fmaf(hv.get(v), hv.get(v), sq);
         }
       }
     }
-    const float rstd = rsqrtf(warp_sum(sq) / (float)a.C + a.eps);
+    const float rstd = rsqrtf(fmaf(warp_sum(sq), a.inv_c, a.eps));
     for (int32_t step = 0; step < steps; ++step) {
       float h[U * V];
       Vec<T, V> w[U];
@@ -220,19 +276,14 @@ rmsnorm_any_kernel(const FwdArgs<T> a) {
       for (int u = 0; u < U; ++u) {
         const int32_t c = channel<V, U>(step, u, lane);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[u * V + v] = 0.f;
-          w[u].e[v] = from_f32<T>(0.f);
-        }
+        for (int v = 0; v < V; ++v) h[u * V + v] = 0.f;
+        w[u].zero();
         if (c < a.C) {
           w[u] = load_vec<T, V>(a.w + c);
-          const Vec<T, V> hv = load_vec<T, V>((hr ? hr : xr) + c);
-          Vec<T, V> rv;
-          if (rr && !hr) rv = load_vec<T, V>(rr + c);
+          Vec<T, V> hv = load_vec<T, V>((hr ? hr : xr) + c);
+          if (rr && !hr) hv.add(load_vec<T, V>(rr + c));
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            h[u * V + v] = rr && !hr ? to_f32(from_f32<T>(to_f32(hv.e[v]) + to_f32(rv.e[v])))
-                                     : to_f32(hv.e[v]);
+          for (int v = 0; v < V; ++v) h[u * V + v] = hv.get(v);
         }
       }
       emit<T, V, U, kMode>(a, t, step, lane, h, w, rstd);
@@ -283,6 +334,7 @@ pe_status run_fwd(int mode, const void* x, const void* res, const void* w, int64
                         static_cast<const T*>(w),
                         N,
                         C,
+                        1.f / (float)C,
                         eps,
                         static_cast<T*>(y),
                         static_cast<T*>(res_out),
@@ -296,7 +348,7 @@ pe_status run_fwd(int mode, const void* x, const void* res, const void* w, int64
 
 // ---------------------------------------------------------------- backward
 constexpr int32_t kBwdMaxChannels = 16384;
-constexpr int kBwdMaxBlocks = 320;
+constexpr int kBwdMaxBlocks = 480;
 
 template <typename T>
 struct BwdArgs {
@@ -306,6 +358,7 @@ struct BwdArgs {
   const T* dres;
   int64_t N;
   int32_t C;
+  float inv_c;         // 1 / C
   float eps;
   T* dx;
   float* part;         // [gridDim.x][C] sums of this block's rows
@@ -316,7 +369,8 @@ struct BwdArgs {
 // fp32 registers until the block's last row. Blocks of warps add their warps'
 // sums in warp order.
 template <typename T, int V, int kIter, int kGroup>
-__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads)
+__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads,
+                                  kGroup > kThreads ? 1 : kIter * V <= 16 ? 3 : 2)
 rmsnorm_bwd_kernel(const BwdArgs<T> a) {
   constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
   constexpr int kGroups = kBlock / kGroup;
@@ -329,28 +383,31 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
   int phase = 0;
   for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < a.N;
        t += (int64_t)gridDim.x * kGroups) {
-    Vec<T, V> dyv[kIter], hv[kIter], rv[kIter], wv[kIter];
+    Vec<T, V> dyv[kIter], hv[kIter], rv[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int32_t c = (it * kGroup + g) * V;
-#pragma unroll
-      for (int v = 0; v < V; ++v) dyv[it].e[v] = hv[it].e[v] = wv[it].e[v] = from_f32<T>(0.f);
+      dyv[it].zero();
+      hv[it].zero();
       if (c < a.C) {
         dyv[it] = load_vec<T, V>(a.dy + t * a.C + c);
         hv[it] = load_vec<T, V>(a.h + t * a.C + c);
         if (a.dres) rv[it] = load_vec<T, V>(a.dres + t * a.C + c);
-        wv[it] = load_vec<T, V>(a.w + c);
       }
     }
     float sq = 0.f, dot = 0.f;
 #pragma unroll
-    for (int it = 0; it < kIter; ++it)
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      Vec<T, V> wv;                          // from the caches, here and below
+      if (c < a.C) wv = load_vec<T, V>(a.w + c);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float h = to_f32(hv[it].e[v]);
+        const float h = hv[it].get(v);
         sq = fmaf(h, h, sq);
-        dot = fmaf(to_f32(dyv[it].e[v]) * to_f32(wv[it].e[v]), h, dot);
+        if (c < a.C) dot = fmaf(dyv[it].get(v) * wv.get(v), h, dot);
       }
+    }
     sq = warp_sum(sq);
     dot = warp_sum(dot);
     if constexpr (kGroup > 32) {             // kGroups == 1: the loop is uniform in the block
@@ -364,21 +421,23 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
       }
       phase ^= 1;
     }
-    const float rstd = rsqrtf(sq / (float)a.C + a.eps);
-    const float along = rstd * (dot / (float)a.C) * rstd;   // mean(w dy n) rstd
+    const float rstd = rsqrtf(fmaf(sq, a.inv_c, a.eps));
+    const float along = rstd * (dot * a.inv_c) * rstd;   // mean(w dy n) rstd
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int32_t c = (it * kGroup + g) * V;
       if (c < a.C) {
-        Vec<T, V> o;
+        const Vec<T, V> wv = load_vec<T, V>(a.w + c);
+        float dx[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float dy = to_f32(dyv[it].e[v]), n = to_f32(hv[it].e[v]) * rstd;
-          float dx = rstd * (dy * to_f32(wv[it].e[v])) - n * along;
-          if (a.dres) dx += to_f32(rv[it].e[v]);
-          o.e[v] = from_f32<T>(dx);
+          const float dy = dyv[it].get(v), n = hv[it].get(v) * rstd;
+          dx[v] = rstd * (dy * wv.get(v)) - n * along;
+          if (a.dres) dx[v] += rv[it].get(v);
           dw[it * V + v] = fmaf(dy, n, dw[it * V + v]);
         }
+        Vec<T, V> o;
+        o.put(dx);
         store_vec<T, V>(a.dx + t * a.C + c, o);
       }
     }
@@ -451,6 +510,7 @@ pe_status run_bwd(const void* dy, const void* h, const void* w, const void* dres
                         static_cast<const T*>(dres),
                         N,
                         C,
+                        1.f / (float)C,
                         eps,
                         static_cast<T*>(dx),
                         static_cast<float*>(ws)};

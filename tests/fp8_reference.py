@@ -4,7 +4,7 @@ at most 2^-24 of its value, an output rounding by eps / 2 of its type."""
 
 import torch
 
-FLOOR = 2.0 ** -117
+FLOOR = {torch.float8_e4m3fn: 2.0 ** -117, torch.float8_e5m2: 2.0 ** -110}
 LARGEST = {torch.float8_e4m3fn: 448.0, torch.float8_e5m2: 57344.0}
 MANTISSA = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 2}
 LOWEST_EXPONENT = {torch.float8_e4m3fn: -6, torch.float8_e5m2: -14}
@@ -22,7 +22,7 @@ def scales_of(v, dtype, block_rows):
     p = torch.zeros(rb * block_rows, cb * 128, dtype=torch.float64, device=v.device)
     p[:r, :c] = v.abs()
     amax = p.view(rb, block_rows, cb, 128).amax(dim=(1, 3))
-    return (amax.clamp(min=FLOOR) / LARGEST[dtype]).t()
+    return (amax.clamp(min=FLOOR[dtype]) / LARGEST[dtype]).t()
 
 
 def spread(scales, shape, block_rows):
@@ -33,9 +33,9 @@ def spread(scales, shape, block_rows):
 
 def check_quantized(q, scales, v, dtype, block_rows, rel, what):
     """q and scales quantise the 64-bit matrix v when v itself is only known to
-    `rel` of its value: the scale within rel plus the roundings of its division,
-    and each element within half a step of the 8-bit grid plus rel (and the two
-    roundings of factor and product)."""
+    `rel` of its value: the scale within rel plus its two roundings, and each
+    element within half a step of the 8-bit grid plus rel, once through the block's
+    maximum, and the four roundings of factor (three) and product."""
     want = scales_of(v, dtype, block_rows)
     assert scales.dtype == torch.float32 and scales.shape == want.shape, what
     assert q.dtype == dtype and q.shape == v.shape, what

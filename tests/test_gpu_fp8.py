@@ -127,7 +127,7 @@ def test_rmsnorm_of_rows_with_nothing_in_them():
     w = torch.ones(300, dtype=BF16, device=DEV)
     q, s = pe.pe_rmsnorm_fp8(x, w)
     assert bool((q[1].float() == 0).all())
-    assert bool((s[:, 1] == torch.tensor(ref.FLOOR / 448, device=DEV).float()).all())
+    assert bool((s[:, 1] == torch.tensor(ref.FLOOR[E4M3] / 448, device=DEV).float()).all())
     assert bool(q[2].float().isnan().all()) and bool(s[:, 2].isnan().all())
     assert bool(q[3, 290].float().isnan()) and bool(s[2, 3].isnan())
     clean = x[[0, 4, 5]].contiguous()
@@ -247,6 +247,26 @@ def test_quantize_writes_nothing_outside(rows, cols):
     _outside_untouched(sst, rb, cols, FP32, 0x33)
 
 
+@pytest.mark.parametrize("fp8", [E4M3, E5M2])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_of_the_smallest_and_largest_blocks(block_rows, dtype, fp8):
+    """Blocks of zeros, of the smallest and of the largest numbers of the type."""
+    x = _randn(_gen(314), 384, 128).clamp(-3, 3).to(dtype)
+    x[:128] = 0
+    x[128:256] *= 2.0 ** -116                   # around both floors
+    x[256:] *= 2.0 ** 126
+    for v in (x, x.t().contiguous()):
+        q, s, qt, st = pe.pe_quantize_fp8(v, block_rows, dtype=fp8, transposed=True)
+        ref.check_quantized(q, s, v.double(), fp8, block_rows, 0.0, "as it is")
+        ref.check_quantized(qt, st, v.double().t(), fp8, block_rows, 0.0, "transposed")
+    q, s = pe.pe_quantize_fp8(x, block_rows, dtype=fp8)
+    assert bool((q[:128].float() == 0).all())
+    w = torch.ones(128, dtype=dtype, device=DEV)
+    zero, zs = pe.pe_rmsnorm_fp8(torch.zeros_like(x), w, dtype=fp8)
+    assert bool((zero.float() == 0).all()) and bool(zs.isfinite().all())
+
+
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_quantize_of_special_values(block_rows):
     x = _randn(_gen(313), 256, 256)
@@ -261,7 +281,7 @@ def test_quantize_of_special_values(block_rows):
     # 1e-38 |N(0,1)| times 448 / 2^-117 = 7.4e37 is of the order of 1: small
     # numbers of the grid, not zeros.
     ref.check_quantized(q[:, :128], s[:1], x[:, :128].double(), E4M3, block_rows, 0.0, "tiny")
-    assert bool((s[0] == torch.tensor(ref.FLOOR / 448, device=DEV).float()).all())
+    assert bool((s[0] == torch.tensor(ref.FLOOR[E4M3] / 448, device=DEV).float()).all())
     if block_rows == 128:
         assert bool(back[:, 128:].isnan().all())
     else:
