@@ -1,4 +1,6 @@
 // Matrix product of 8-bit operands with a scale for each block of 128.
+#include <cudaTypedefs.h>
+
 #include <atomic>
 
 #include "pe_matmul_fp8.cuh"
@@ -31,7 +33,72 @@ pe_status status_word(DeviceStatus** out) {
   return PE_OK;
 }
 
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
+
 }  // namespace
+
+// Estimated microseconds of every way, from times measured on a GB300 (m x n x k,
+// bf16 out; T: rows of a per CTA, S: split, whole tiles of the pair kernel last):
+//   1 x 2304 x 768     T16 4.4  T32 4.9  T64 5.9  pair 8.9
+//   1 x 1024 x 1024    T16 5.2, S8 4.4            pair 10.0
+//   320 x 2304 x 768   T16 8.9  T32 6.6  T64 6.7  pair 9.6
+//   1000 x 2304 x 768  T16 18.0 T32 11.6 T64 8.7  pair 9.9
+//   2500 x 2304 x 768                    T64 20.0 pair 14.5
+//   200 x 200 x 20000  T16,S8 11.8  T32,S8 11.0  T64,S8 13.4
+//   100 x 1000 x 8000  T32,S2 13.9  T32,S4 9.3   T64,S8 10.7
+// A narrow CTA takes kFixed and kBlock for each block of k; CTAs that share an SM
+// slow each other, and the join of a split costs kJoin. Splitting pays once a sum
+// has 8 blocks.
+MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
+  constexpr int64_t kSms = 152, kPairs = kSms / 2;
+  const int64_t blocks = ceil_div(k, kFp8Block);
+  const int64_t tiles = ceil_div(m, 256) * ceil_div(n, 256);
+  const double whole = 0.6 * (double)ceil_div(tiles, kPairs) * (blocks + 1);
+  const double parts = (double)kPairs / tiles + 1;
+  const double runs =
+      0.6 * (double)(ceil_div(tiles * blocks, kPairs) + ceil_div(tiles, kPairs)) + 4 + 0.6 * parts;
+  MatmulPlan plan = {0, 1, runs < whole};
+  double best = 5 + (runs < whole ? runs : whole);
+  constexpr int32_t kRows[3] = {16, 32, 64};
+  constexpr double kFixed[3] = {3.0, 3.4, 3.6}, kBlock[3] = {0.285, 0.30, 0.43},
+                   kJoin[3] = {0.8, 0.8, 1.5};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t ctas = ceil_div(m, kRows[i]) * ceil_div(n, 128);
+    if (ctas > 8 * kSms || ceil_div(m, kRows[i]) > 65535) continue;
+    int64_t split = blocks < 8 ? 1 : kSms / ctas;
+    split = split < 1 ? 1 : split > 8 ? 8 : split;
+    const double shared = (double)ceil_div(ctas * split, kSms) - 1;
+    const double t = kFixed[i] + kBlock[i] * (double)ceil_div(blocks, split) * (1 + 0.6 * shared) +
+                     1.2 * shared + (split > 1 ? kJoin[i] : 0);
+    if (t < best) {
+      best = t;
+      plan = {kRows[i], (int32_t)split, false};
+    }
+  }
+  return plan;
+}
+
+pe_status matmul_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base,
+                     int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = g_encode.load();
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult qres;
+    PE_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                 cudaEnableDefault, &qres));
+    if (qres != cudaDriverEntryPointSuccess || !fn) return PE_ERR_CUDA;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    g_encode.store(encode);
+  }
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  cuuint32_t box[2] = {128u / size, box_rows};
+  cuuint32_t elem_strides[2] = {1, 1};
+  CUresult r = encode(map, type, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PE_OK : PE_ERR_CUDA;
+}
 
 }  // namespace pe
 
@@ -39,7 +106,7 @@ using namespace pe;
 
 extern "C" size_t pe_matmul_fp8_workspace_size(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0) return 0;
-  return matmul_pair_workspace(m, n, k);
+  return matmul_plan(m, n, k).runs ? matmul_pair_workspace() : 0;
 }
 
 extern "C" pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_ld,
@@ -63,7 +130,8 @@ extern "C" pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_
                                 stream));
     return PE_OK;
   }
-  const size_t need = pe_matmul_fp8_workspace_size(m, n, k);
+  const MatmulPlan plan = matmul_plan(m, n, k);
+  const size_t need = plan.runs ? matmul_pair_workspace() : 0;
   if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return PE_ERR_WORKSPACE;
   DeviceStatus* status = nullptr;
@@ -81,7 +149,8 @@ extern "C" pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_
                        b_type == PE_E5M2,
                        out_dtype == PE_FP32,
                        out};
-  return matmul_pair(p, workspace, status, stream);
+  if (plan.rows) return matmul_rows(p, plan.rows, plan.split, status, stream);
+  return matmul_pair(p, plan.runs, workspace, status, stream);
 }
 
 extern "C" pe_status pe_read_matmul_status(pe_stream_t stream_) {

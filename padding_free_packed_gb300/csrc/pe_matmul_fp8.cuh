@@ -2,6 +2,7 @@
 #pragma once
 
 #include "pe_fp8.cuh"
+#include "pe_sm103.cuh"
 
 namespace pe {
 
@@ -16,9 +17,67 @@ struct MatmulFp8 {
   void* out;
 };
 
+// How a product runs. The choice depends on the sizes alone (the workspace size
+// follows it); it counts the 152 SMs of the device these kernels are built for.
+struct MatmulPlan {
+  int32_t rows;      // of a per CTA of the narrow kernel: 16, 32 or 64; 0: the pair kernel
+  int32_t split;     // narrow: CTAs of a cluster that share a tile's sum
+  bool runs;         // pair: equal runs of blocks of k, parts summed by a second kernel
+};
+MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k);
+
 // Pairs of CTAs on 256 x 256 tiles, for products with many rows.
-size_t matmul_pair_workspace(int64_t m, int64_t n, int64_t k);
-pe_status matmul_pair(const MatmulFp8& p, void* workspace, DeviceStatus* status,
+size_t matmul_pair_workspace();
+pe_status matmul_pair(const MatmulFp8& p, bool runs, void* workspace, DeviceStatus* status,
                       cudaStream_t stream);
 
+// Few rows: 128 rows of b by 16, 32 or 64 rows of a per CTA, the sum over k split
+// over a cluster.
+pe_status matmul_rows(const MatmulFp8& p, int32_t rows, int32_t split, DeviceStatus* status,
+                      cudaStream_t stream);
+
+// Tensor map of row-major [rows, cols] of `type` (elements of `size` bytes), rows
+// `pitch` bytes apart, boxes of box_rows rows of 128 bytes, 128-byte swizzle.
+pe_status matmul_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base,
+                     int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows);
+
+namespace sm103 {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Address, in the cluster's shared window, of the same variable in CTA `rank`.
+__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+// Four bytes to shared memory without a register on the way (zero unless `in`).
+__device__ __forceinline__ void copy_async4(void* dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, both operands K-major.
+constexpr uint32_t idesc_fp8(int M, int N, bool a_e5m2, bool b_e5m2) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+}  // namespace sm103
 }  // namespace pe

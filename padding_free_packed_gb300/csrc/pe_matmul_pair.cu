@@ -25,10 +25,7 @@
 // consecutive blocks of k (a run may start and end inside a tile); a tile that
 // several pairs share is then summed from their fp32 parts, in the order of k,
 // by a second kernel.
-#include <cudaTypedefs.h>
-
 #include "pe_matmul_fp8.cuh"
-#include "pe_sm103.cuh"
 
 namespace pe {
 
@@ -91,21 +88,6 @@ struct Params {
 
 enum WaitSite { kSiteProducer = 71, kSiteMma = 72, kSiteEpilogue = 73, kSiteScales = 74 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// Address, in the cluster's shared window, of the same variable in CTA `rank`.
-__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void store_cluster_i32(uint32_t addr, int32_t v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -144,26 +126,6 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       " [%0], %1;\n\t}" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
-}
-
-// Four bytes to shared memory without a register on the way (zero unless `in`).
-__device__ __forceinline__ void copy_async4(void* dst, const float* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(in ? 4 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kPending>
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
-
-// kind::f8f6f4, fp32 accumulator, both operands K-major.
-constexpr uint32_t idesc_fp8(int M, int N, bool a_e5m2, bool b_e5m2) {
-  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // First block of pair `p`'s run when `total` blocks are dealt to `pairs`.
@@ -665,69 +627,25 @@ matmul_parts_kernel(const Params p, int32_t pairs) {
 }
 
 // ---------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 g_encode_matmul = nullptr;
-
-pe_status get_encoder_matmul() {
-  if (g_encode_matmul) return PE_OK;
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult qres;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                       &qres) != cudaSuccess ||
-      qres != cudaDriverEntryPointSuccess || !fn)
-    return PE_ERR_CUDA;
-  g_encode_matmul = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  return PE_OK;
-}
-
-// Row-major [rows, cols] of `type`, rows `pitch` bytes apart, boxes of box_rows
-// rows of 128 bytes, 128-byte swizzle.
-pe_status make_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base,
-                   int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  cuuint32_t box[2] = {128u / size, box_rows};
-  cuuint32_t elem_strides[2] = {1, 1};
-  CUresult r = g_encode_matmul(map, type, 2, const_cast<void*>(base), dims, strides, box,
-                               elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? PE_OK : PE_ERR_CUDA;
-}
-
 int32_t pair_count() {
   const int32_t n = device_sm_count() / 2;
   return n < kMaxPairs ? n : kMaxPairs;
 }
 
-// Runs of blocks instead of whole tiles: when the busiest pair then saves more
-// blocks than the parts and the second kernel cost.
-bool use_runs(int64_t tiles, int64_t blocks, int64_t pairs) {
-  const int64_t whole = ceil_div(tiles, pairs) * blocks;
-  return whole - ceil_div(tiles * blocks, pairs) > 24;
-}
-
 }  // namespace
 
-size_t matmul_pair_workspace(int64_t m, int64_t n, int64_t k) {
-  // The size must not depend on the device at hand: parts for the most pairs any
-  // device runs whenever some number of pairs would use runs.
-  const int64_t tiles = ceil_div(m, kTile) * ceil_div(n, kTile), blocks = ceil_div(k, kFp8Block);
-  for (int64_t pairs = 1; pairs <= kMaxPairs; ++pairs)
-    if (use_runs(tiles, blocks, pairs)) return 2 * kMaxPairs * kPartFloats * sizeof(float);
-  return 0;
-}
+size_t matmul_pair_workspace() { return 2 * kMaxPairs * kPartFloats * sizeof(float); }
 
-pe_status matmul_pair(const MatmulFp8& q, void* workspace, DeviceStatus* status,
+pe_status matmul_pair(const MatmulFp8& q, bool runs, void* workspace, DeviceStatus* status,
                       cudaStream_t stream) {
-  PE_TRY(get_encoder_matmul());
   CUtensorMap ma, mb, mo;
-  PE_TRY(make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.a, q.m, q.k, q.a_ld, kRows));
-  PE_TRY(make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.b, q.n, q.k, q.b_ld, kRows / 2));
+  PE_TRY(matmul_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.a, q.m, q.k, q.a_ld, kRows));
+  PE_TRY(matmul_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.b, q.n, q.k, q.b_ld, kRows / 2));
   const int size = q.out_fp32 ? 4 : 2;
   const bool tma_store = aligned(q.out, 16) && (int64_t)q.n * size % 16 == 0;
   mo = ma;
   if (tma_store)
-    PE_TRY(make_map(&mo, q.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+    PE_TRY(matmul_map(&mo, q.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                     size, q.out, q.m, q.n, (int64_t)q.n * size, 32));
   const size_t smem = sizeof(Smem) + 1024;
@@ -749,7 +667,7 @@ pe_status matmul_pair(const MatmulFp8& q, void* workspace, DeviceStatus* status,
   if (tiles * p.blocks >= (1LL << 30)) return PE_ERR_OVERFLOW;
   p.tiles = (int32_t)tiles;
   int32_t pairs = pair_count();
-  p.shared_tiles = use_runs(tiles, p.blocks, pairs) ? 1 : 0;
+  p.shared_tiles = runs ? 1 : 0;
   if (!p.shared_tiles && tiles < pairs) pairs = (int32_t)tiles;
   p.tma_store = tma_store ? 1 : 0;
   p.out_fp32 = q.out_fp32 ? 1 : 0;
