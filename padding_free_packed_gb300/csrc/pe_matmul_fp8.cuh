@@ -59,6 +59,26 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) 
   return r;
 }
 
+// mbar_wait for the waits of every block of k: a few attempts (each suspends the
+// thread for a while) before the clock and the abort flag are looked at. Not with a
+// short limit, which is kept by polling.
+__device__ __forceinline__ bool eager_wait(uint32_t bar, uint32_t parity,
+                                           volatile WaitGuard* guard, DeviceStatus* status,
+                                           int where) {
+  if (mbar_test_wait(bar, parity)) return true;
+  if (guard->limit_ns >= kPollBelowNs) {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  }
+  return mbar_wait(bar, parity, guard, status, where);
+}
+// The same for a whole warp: true only if true in every lane.
+__device__ __forceinline__ bool eager_warp_wait(uint32_t bar, uint32_t parity,
+                                                volatile WaitGuard* guard, DeviceStatus* status,
+                                                int where) {
+  return __all_sync(0xffffffffu, eager_wait(bar, parity, guard, status, where));
+}
+
 // Four bytes to shared memory without a register on the way (zero unless `in`).
 __device__ __forceinline__ void copy_async4(void* dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),

@@ -77,7 +77,6 @@ struct Params {
   int32_t col_tiles;
   int32_t tiles;
   int32_t shared_tiles;      // 1: runs of blocks, partial tiles through `parts`
-  int32_t tma_store;         // out rows start at 16-byte multiples
   int32_t out_fp32;
   uint32_t idesc;
   void* out;
@@ -90,10 +89,6 @@ enum WaitSite { kSiteProducer = 71, kSiteMma = 72, kSiteEpilogue = 73, kSiteScal
 
 __device__ __forceinline__ void store_cluster_i32(uint32_t addr, int32_t v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
 }
 __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
@@ -137,7 +132,7 @@ __host__ __device__ __forceinline__ int64_t run_start(int64_t total, int32_t pai
 struct Walk {
   int32_t tile, first, last;      // last: one past the segment's last block
   int32_t stride;
-  int64_t left;                   // blocks after this segment (shared tiles)
+  int32_t left;                   // blocks after this segment (shared tiles)
 
   // The pair's first segment; false when it has none.
   __device__ bool start(const Params& p, int32_t pair, int32_t pairs) {
@@ -147,8 +142,8 @@ struct Walk {
       if (lo >= hi) return false;
       tile = (int32_t)(lo / p.blocks);
       first = (int32_t)(lo - (int64_t)tile * p.blocks);
-      const int64_t room = hi - lo;
-      last = room < p.blocks - first ? first + (int32_t)room : p.blocks;
+      const int32_t room = (int32_t)(hi - lo);
+      last = room < p.blocks - first ? first + room : p.blocks;
       left = room - (last - first);
       return true;
     }
@@ -163,7 +158,7 @@ struct Walk {
     if (p.shared_tiles) {
       if (left <= 0) return false;
       ++tile;
-      last = left < p.blocks ? (int32_t)left : p.blocks;
+      last = left < p.blocks ? left : p.blocks;
       left -= last;
       return true;
     }
@@ -181,54 +176,175 @@ __device__ __forceinline__ int32_t pair_blocks(const Params& p, int32_t pair, in
   return pair < p.tiles ? ((p.tiles - 1 - pair) / pairs + 1) * p.blocks : 0;
 }
 
-// The 64 registers that tensor-memory loads of the epilogue write, declared once
-// by name: a load may then be in flight across the loop's back edge, where a C++
-// variable could be copied before its data has come.
-#define PE_DECLARE_D() asm volatile(".reg .b32 pe_d<64>;")
-#define PE_D8(a, b, c, d, e, f, g, h) \
-  "pe_d" #a ", pe_d" #b ", pe_d" #c ", pe_d" #d ", pe_d" #e ", pe_d" #f ", pe_d" #g ", pe_d" #h
-// 32 columns of this thread's lane into registers 0-31, or 32-63.
-__device__ __forceinline__ void load_low(uint32_t taddr) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(0, 1, 2, 3, 4, 5, 6, 7) ", " PE_D8(
-                   8, 9, 10, 11, 12, 13, 14, 15) ", " PE_D8(16, 17, 18, 19, 20, 21, 22, 23)
-                   ", " PE_D8(24, 25, 26, 27, 28, 29, 30, 31) "}, [%0];" ::"r"(taddr)
+// The registers of the epilogue's inner loop have names of their own (four groups of
+// 32 sums, two of 32 loaded columns): loads of the next columns are then in flight
+// while the columns before them are added, without a copy of either. The same loop
+// on C++ variables took a move for every second column, and paired fp32 arithmetic
+// (two columns an instruction, at half the rate) one for almost every column.
+#define PE_DECLARE_SUMS()                                                                   \
+  asm volatile(                                                                             \
+      ".reg .b32 pe_s0_<32>, pe_s1_<32>, pe_s2_<32>, pe_s3_<32>, pe_d0_<32>, pe_d1_<32>;")
+#define PE_EACH32(OP, q, h)                                                                  \
+  OP(q, h, 0) OP(q, h, 1) OP(q, h, 2) OP(q, h, 3) OP(q, h, 4) OP(q, h, 5) OP(q, h, 6)        \
+  OP(q, h, 7) OP(q, h, 8) OP(q, h, 9) OP(q, h, 10) OP(q, h, 11) OP(q, h, 12) OP(q, h, 13)    \
+  OP(q, h, 14) OP(q, h, 15) OP(q, h, 16) OP(q, h, 17) OP(q, h, 18) OP(q, h, 19) OP(q, h, 20) \
+  OP(q, h, 21) OP(q, h, 22) OP(q, h, 23) OP(q, h, 24) OP(q, h, 25) OP(q, h, 26)              \
+  OP(q, h, 27) OP(q, h, 28) OP(q, h, 29) OP(q, h, 30) OP(q, h, 31)
+#define PE_FMA(q, h, i) "fma.rn.f32 pe_s" #q "_" #i ", pe_d" #h "_" #i ", %0, pe_s" #q "_" #i ";\n\t"
+#define PE_D8(h, a, b, c, d, e, f, g, i)                                                    \
+  "pe_d" #h "_" #a ", pe_d" #h "_" #b ", pe_d" #h "_" #c ", pe_d" #h "_" #d ", pe_d" #h "_" #e \
+  ", pe_d" #h "_" #f ", pe_d" #h "_" #g ", pe_d" #h "_" #i
+// 32 columns of this thread's lane, from column `off` on, into group h.
+#define PE_LOAD(h, off)                                                                   \
+  "add.u32 a, %1, " #off ";\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(            \
+      h, 0, 1, 2, 3, 4, 5, 6, 7) ", " PE_D8(h, 8, 9, 10, 11, 12, 13, 14, 15) ", " PE_D8(    \
+      h, 16, 17, 18, 19, 20, 21, 22, 23) ", " PE_D8(h, 24, 25, 26, 27, 28, 29, 30, 31)      \
+      "}, [a];\n\t"
+#define PE_WAIT_LOADS "tcgen05.wait::ld.sync.aligned;\n\t"
+// One block of k: the 128 columns at tensor-memory address `src`, scaled, added to
+// the sums. The accumulator is handed back as soon as it has been read, by the lane
+// with `first` set, on the barrier `back` of the pair's first CTA.
+__device__ __forceinline__ void add_block(float scale, uint32_t src, uint32_t back,
+                                          uint32_t first) {
+  asm volatile("{\n\t.reg .b32 a;\n\t.reg .pred q;\n\t" PE_LOAD(0, 0) PE_LOAD(1, 32)
+                   PE_WAIT_LOADS PE_EACH32(PE_FMA, 0, 0) PE_LOAD(0, 64) PE_EACH32(PE_FMA, 1, 1)
+                       PE_LOAD(1, 96) PE_WAIT_LOADS
+               "tcgen05.fence::before_thread_sync;\n\tbar.warp.sync 0xffffffff;\n\t"
+               "setp.ne.b32 q, %3, 0;\n\t@q mbarrier.arrive.shared::cluster.b64 _, [%2];\n\t"
+               PE_EACH32(PE_FMA, 2, 0) PE_EACH32(PE_FMA, 3, 1) "}" ::"f"(scale),
+               "r"(src), "r"(back), "r"(first)
                : "memory");
 }
-__device__ __forceinline__ void load_high(uint32_t taddr) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(
-                   32, 33, 34, 35, 36, 37, 38, 39) ", " PE_D8(40, 41, 42, 43, 44, 45, 46, 47)
-                   ", " PE_D8(48, 49, 50, 51, 52, 53, 54, 55) ", " PE_D8(
-                       56, 57, 58, 59, 60, 61, 62, 63) "}, [%0];" ::"r"(taddr)
-               : "memory");
+#define PE_ZERO(q, h, i) "mov.b32 pe_s" #q "_" #i ", 0;\n\t"
+__device__ __forceinline__ void clear_sums() {
+  asm volatile(PE_EACH32(PE_ZERO, 0, 0) PE_EACH32(PE_ZERO, 1, 0) PE_EACH32(PE_ZERO, 2, 0)
+                   PE_EACH32(PE_ZERO, 3, 0)::
+                       : "memory");
 }
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-#define PE_ADD(sum, lo, hi)                                          \
-  asm volatile(                                                      \
-      "{\n\t.reg .b64 t;\n\tmov.b64 t, {pe_d" #lo ", pe_d" #hi "};\n\t" \
-      "fma.rn.f32x2 %0, t, %1, %0;\n\t}"                             \
-      : "+l"(sum)                                                    \
-      : "l"(scale2))
-// 16 pairs of sums += scale * registers 0-31, or 32-63.
-__device__ __forceinline__ void add_low(uint64_t* s, uint64_t scale2) {
-  PE_ADD(s[0], 0, 1); PE_ADD(s[1], 2, 3); PE_ADD(s[2], 4, 5); PE_ADD(s[3], 6, 7);
-  PE_ADD(s[4], 8, 9); PE_ADD(s[5], 10, 11); PE_ADD(s[6], 12, 13); PE_ADD(s[7], 14, 15);
-  PE_ADD(s[8], 16, 17); PE_ADD(s[9], 18, 19); PE_ADD(s[10], 20, 21); PE_ADD(s[11], 22, 23);
-  PE_ADD(s[12], 24, 25); PE_ADD(s[13], 26, 27); PE_ADD(s[14], 28, 29); PE_ADD(s[15], 30, 31);
-}
-__device__ __forceinline__ void add_high(uint64_t* s, uint64_t scale2) {
-  PE_ADD(s[0], 32, 33); PE_ADD(s[1], 34, 35); PE_ADD(s[2], 36, 37); PE_ADD(s[3], 38, 39);
-  PE_ADD(s[4], 40, 41); PE_ADD(s[5], 42, 43); PE_ADD(s[6], 44, 45); PE_ADD(s[7], 46, 47);
-  PE_ADD(s[8], 48, 49); PE_ADD(s[9], 50, 51); PE_ADD(s[10], 52, 53); PE_ADD(s[11], 54, 55);
-  PE_ADD(s[12], 56, 57); PE_ADD(s[13], 58, 59); PE_ADD(s[14], 60, 61); PE_ADD(s[15], 62, 63);
+#define PE_GET8(q, i0, i1, i2, i3, i4, i5, i6, i7)                                         \
+  asm volatile("mov.b32 %0, pe_s" #q "_" #i0 ";\n\tmov.b32 %1, pe_s" #q "_" #i1              \
+               ";\n\tmov.b32 %2, pe_s" #q "_" #i2 ";\n\tmov.b32 %3, pe_s" #q "_" #i3          \
+               ";\n\tmov.b32 %4, pe_s" #q "_" #i4 ";\n\tmov.b32 %5, pe_s" #q "_" #i5          \
+               ";\n\tmov.b32 %6, pe_s" #q "_" #i6 ";\n\tmov.b32 %7, pe_s" #q "_" #i7 ";"      \
+               : "=f"(x[i0]), "=f"(x[i1]), "=f"(x[i2]), "=f"(x[i3]), "=f"(x[i4]),           \
+                 "=f"(x[i5]), "=f"(x[i6]), "=f"(x[i7]))
+#define PE_GET32(q)                             \
+  PE_GET8(q, 0, 1, 2, 3, 4, 5, 6, 7);           \
+  PE_GET8(q, 8, 9, 10, 11, 12, 13, 14, 15);     \
+  PE_GET8(q, 16, 17, 18, 19, 20, 21, 22, 23);   \
+  PE_GET8(q, 24, 25, 26, 27, 28, 29, 30, 31)
+// The sums of columns 32 q .. 32 q + 31.
+template <int q>
+__device__ __forceinline__ void get_sums(float (&x)[32]) {
+  if constexpr (q == 0) {
+    PE_GET32(0);
+  } else if constexpr (q == 1) {
+    PE_GET32(1);
+  } else if constexpr (q == 2) {
+    PE_GET32(2);
+  } else {
+    PE_GET32(3);
+  }
 }
 
+__device__ __forceinline__ float load_shared(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// How rows of out are written: bf16 or fp32 boxes by TMA, or, where rows start
+// anywhere, either type element by element.
+enum Out { kOutBf16 = 0, kOutFp32 = 1, kOutAnywhere = 2 };
+
+// Columns 32 q .. of a warp's 32 rows x 128 columns at (row0, col0) of out. `stage`:
+// this warp's two boxes of 32 rows x 128 bytes.
+template <int kOut, int q>
+__device__ __forceinline__ void store_quarter(const Params& p, const CUtensorMap& tm_out,
+                                              uint32_t stage, int lane, int32_t row0,
+                                              int32_t col0) {
+  float x[32];
+  get_sums<q>(x);
+  if constexpr (kOut == kOutBf16) {        // two quarters fill a box
+    const uint32_t box = stage + (q >> 1) * kBoxBytes;
+    const uint32_t row = box + lane * 128 + ((lane & 7) << 4);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row ^ ((q % 2 * 4 + g) << 4)),
+                   "r"(pack_bf16x2(x[8 * g], x[8 * g + 1])),
+                   "r"(pack_bf16x2(x[8 * g + 2], x[8 * g + 3])),
+                   "r"(pack_bf16x2(x[8 * g + 4], x[8 * g + 5])),
+                   "r"(pack_bf16x2(x[8 * g + 6], x[8 * g + 7]))
+                   : "memory");
+    if constexpr (q % 2 == 1) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && col0 + q / 2 * 64 < p.n) {
+        tma_store_2d(&tm_out, box, col0 + q / 2 * 64, row0);
+        bulk_commit();
+      }
+    }
+  } else if constexpr (kOut == kOutFp32) {
+    const uint32_t box = stage + (q & 1) * kBoxBytes;
+    const uint32_t row = box + lane * 128 + ((lane & 7) << 4);
+    if constexpr (q == 2) {                // both boxes are in use
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(row ^ (g << 4)),
+                   "f"(x[4 * g]), "f"(x[4 * g + 1]), "f"(x[4 * g + 2]), "f"(x[4 * g + 3])
+                   : "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && col0 + q * 32 < p.n) {
+      tma_store_2d(&tm_out, box, col0 + q * 32, row0);
+      bulk_commit();
+    }
+  } else {
+    // Through the stage, then row by row: a row's 32 columns are consecutive.
+    __syncwarp();
+    const uint32_t row = stage + lane * 128 + ((lane & 7) << 4);
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(row ^ (g << 4)),
+                   "f"(x[4 * g]), "f"(x[4 * g + 1]), "f"(x[4 * g + 2]), "f"(x[4 * g + 3])
+                   : "memory");
+    __syncwarp();
+    const int32_t rows = p.m - row0 < 32 ? p.m - row0 : 32;
+    const int32_t col = col0 + q * 32 + lane;
+    if (col < p.n) {
+      for (int32_t r = 0; r < rows; ++r) {
+        const float v =
+            load_shared(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        const int64_t at = (int64_t)(row0 + r) * p.n + col;
+        if (p.out_fp32)
+          static_cast<float*>(p.out)[at] = v;
+        else
+          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+      }
+    }
+  }
+}
+
+// A quarter of a part: [column group][row] float4, so that a warp's stores are
+// consecutive.
+template <int q>
+__device__ __forceinline__ void store_part(float4* part) {
+  float x[32];
+  get_sums<q>(x);
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    part[(8 * q + g) * 128] = make_float4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]);
+}
+
+template <int kOut>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_out, const Params p) {
-  PE_DECLARE_D();
+  PE_DECLARE_SUMS();
   extern __shared__ uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -282,7 +398,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         const int32_t row = rt * kTile + (int32_t)rank * kRows;
         const int32_t col = ct * kTile + (int32_t)rank * 64;   // 64 rows of each column half
         for (int32_t block = w.first; block < w.last; ++block) {
-          ok = mbar_wait(smem_u32(&s.empty[stage]), parity, guard, p.status, kSiteProducer);
+          ok = eager_wait(smem_u32(&s.empty[stage]), parity, guard, p.status, kSiteProducer);
           if (!ok) break;
           const uint32_t bar = full0 + stage * 8;
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), kPairBytes);
@@ -314,8 +430,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       for (int32_t i = 0; i < blocks; ++i) {
         const uint32_t buf = i & 1;
         if (!__all_sync(0xffffffffu, free && loaded)) {
-          if (!warp_wait(acc_empty + buf * 8, ((i >> 1) & 1) ^ 1, guard, p.status, kSiteMma)) break;
-          if (!warp_wait(full0 + stage * 8, parity, guard, p.status, kSiteMma)) break;
+          if (!eager_warp_wait(acc_empty + buf * 8, ((i >> 1) & 1) ^ 1, guard, p.status, kSiteMma)) break;
+          if (!eager_warp_wait(full0 + stage * 8, parity, guard, p.status, kSiteMma)) break;
         }
         tc_fence_after();
         const uint64_t da = desc_a0 + stage * (kOperandBytes / 16);
@@ -376,8 +492,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
         const uint32_t bar = smem_u32(&s.acc_full[0][i & 1]);
         if (i >= 2) {                      // its turn of the barriers has begun
           const uint32_t before = (uint32_t)((i >> 1) - 1) & 1;
-          if (!warp_wait(bar, before, guard, p.status, kSiteScales) ||
-              !warp_wait(bar + 16, before, guard, p.status, kSiteScales))
+          if (!eager_warp_wait(bar, before, guard, p.status, kSiteScales) ||
+              !eager_warp_wait(bar + 16, before, guard, p.status, kSiteScales))
             break;
         }
         __syncwarp();
@@ -395,145 +511,55 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
     const int32_t row_in = (int32_t)rank * kRows + quad * 32;   // this warp's rows in the tile
-    uint8_t* stage_out = s.out[warp - 4];
+    const uint32_t stage_out = smem_u32(s.out[warp - 4]);
     const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[half][0]), 0);
 
-    uint64_t acc[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-    int32_t done = 0;
-    const int32_t blocks = pair_blocks(p, pair, pairs);
-    Walk w;
-    bool begins = true;                    // the segment is the pair's first
-    if (w.start(p, pair, pairs)) {
-      int32_t block = w.first;
-      bool ok = warp_wait(smem_u32(&s.acc_full[half][0]), 0, guard, p.status, kSiteEpilogue);
-      if (ok) {
-        tc_fence_after();
-        load_low(lane_base);
-        load_high(lane_base + 32);
-      }
-      while (ok) {
-        const int buf = done & 1, slot = done % kScaleSlots;
-        const uint32_t src = lane_base + buf * kTile;
-        const float scale = s.a_scale[slot][quad * 32 + lane] * s.b_scale[slot][half];
-        const uint64_t scale2 = f2(scale, scale);
-        wait_loads();
-        add_low(acc, scale2);
-        load_low(src + 64);
-        add_high(acc + 16, scale2);
-        load_high(src + 96);
-        ++done;
-        // The next block's accumulator, asked for early.
-        const uint32_t next_bar = smem_u32(&s.acc_full[half][buf ^ 1]);
-        const uint32_t next_parity = (uint32_t)(done >> 1) & 1;
-        const bool more = done < blocks;
-        const bool ready = more && mbar_test_wait(next_bar, next_parity);
-        wait_loads();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty + buf * 8);
-        add_low(acc + 32, scale2);
-        if (more) {
-          ok = __all_sync(0xffffffffu, ready) ||
-               warp_wait(next_bar, next_parity, guard, p.status, kSiteEpilogue);
-          tc_fence_after();
-          if (ok) load_low(lane_base + (buf ^ 1) * kTile);
-        }
-        add_high(acc + 48, scale2);
-        if (more && ok) load_high(lane_base + (buf ^ 1) * kTile + 32);
-        if (++block < w.last) continue;
+    const uint32_t acc_full = smem_u32(&s.acc_full[half][0]);
+    const uint32_t first = lane == 0 ? 1u : 0u;
+    const uint32_t a_scale = smem_u32(&s.a_scale[0][quad * 32 + lane]);
+    const uint32_t b_scale = smem_u32(&s.b_scale[0][half]);
 
-      // The segment's sums: a whole tile goes to out, a part to the workspace.
-      const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
-      const int32_t row0 = rt * kTile + row_in, col0 = ct * kTile + half * 128;
-      if (w.first != 0 || w.last != p.blocks) {
-        const int32_t slot = 2 * pair + (begins ? 0 : 1);
-        float4* part = reinterpret_cast<float4*>(p.parts + slot * kPartFloats) +
-                       (rank * 64 + half * 32) * 128 + quad * 32 + lane;
-#pragma unroll
-        for (int g = 0; g < 32; ++g) {
-          float4 v;
-          f2_split(acc[2 * g], v.x, v.y);
-          f2_split(acc[2 * g + 1], v.z, v.w);
-          part[g * 128] = v;
+    uint32_t buf = 0, parity = 0, slot = 0;
+    bool ok = true;
+    Walk w;
+    if (w.start(p, pair, pairs)) {
+      for (bool begins = true;; begins = false) {       // begins: the pair's first segment
+        clear_sums();
+        for (int32_t block = w.first; block < w.last; ++block) {
+          if (!eager_warp_wait(acc_full + buf * 8, parity, guard, p.status, kSiteEpilogue)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float scale =
+              load_shared(a_scale + slot * (kRows * 4)) * load_shared(b_scale + slot * 8);
+          add_block(scale, lane_base + buf * kTile, acc_empty + buf * 8, first);
+          slot = (slot + 1) % kScaleSlots;
+          parity ^= buf;
+          buf ^= 1;
         }
-      } else if (row0 < p.m && col0 < p.n) {
-        if (p.tma_store) {
-          // Boxes of 32 rows x 128 bytes (64 bf16 or 32 fp32 columns), written by TMA.
-          if (lane == 0) bulk_wait_read();
+        if (!ok) break;
+        // The segment's sums: a whole tile goes to out, a part to the workspace.
+        const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
+        const int32_t row0 = rt * kTile + row_in, col0 = ct * kTile + half * 128;
+        if (w.first != 0 || w.last != p.blocks) {
+          float4* part =
+              reinterpret_cast<float4*>(p.parts + (2 * pair + (begins ? 0 : 1)) * kPartFloats) +
+              (rank * 64 + half * 32) * 128 + quad * 32 + lane;
+          store_part<0>(part);
+          store_part<1>(part);
+          store_part<2>(part);
+          store_part<3>(part);
+        } else if (row0 < p.m && col0 < p.n) {
+          if (lane == 0) bulk_wait_read();              // the tile before has left the stage
           __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {                 // 32 columns
-            if (p.out_fp32 && c == 2) {                 // both boxes are in use
-              if (lane == 0) bulk_wait_read();
-              __syncwarp();
-            }
-            uint8_t* row = stage_out + (p.out_fp32 ? c & 1 : c >> 1) * kBoxBytes + lane * 128;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {               // 8 columns
-              float x[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                f2_split(acc[c * 16 + g * 4 + i], x[2 * i], x[2 * i + 1]);
-              if (p.out_fp32) {
-                *reinterpret_cast<float4*>(row + (((2 * g) ^ (lane & 7)) << 4)) =
-                    make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(row + (((2 * g + 1) ^ (lane & 7)) << 4)) =
-                    make_float4(x[4], x[5], x[6], x[7]);
-              } else {
-                *reinterpret_cast<uint4*>(row + (((c % 2 * 4 + g) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-              }
-            }
-            if (p.out_fp32 || c % 2 == 1) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              const int32_t col = col0 + (p.out_fp32 ? c * 32 : c / 2 * 64);
-              if (lane == 0 && col < p.n) {
-                tma_store_2d(&tm_out, smem_u32(row - lane * 128), col, row0);
-                bulk_commit();
-              }
-            }
-          }
-        } else {
-          // Rows that start anywhere: 32 columns at a time through this warp's
-          // stage, then row by row.
-          const int32_t rows = p.m - row0 < 32 ? p.m - row0 : 32;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {                 // 32 columns
-            __syncwarp();
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {               // 4 columns
-              float4 v;
-              f2_split(acc[c * 16 + g * 2], v.x, v.y);
-              f2_split(acc[c * 16 + g * 2 + 1], v.z, v.w);
-              *reinterpret_cast<float4*>(stage_out + lane * 128 + ((g ^ (lane & 7)) << 4)) = v;
-            }
-            __syncwarp();
-            const int32_t col = col0 + c * 32 + lane;
-            if (col < p.n) {
-              for (int32_t r = 0; r < rows; ++r) {
-                const float v = *reinterpret_cast<const float*>(
-                    stage_out + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-                const int64_t at = (int64_t)(row0 + r) * p.n + col;
-                if (p.out_fp32)
-                  static_cast<float*>(p.out)[at] = v;
-                else
-                  static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-              }
-            }
-          }
+          store_quarter<kOut, 0>(p, tm_out, stage_out, lane, row0, col0);
+          store_quarter<kOut, 1>(p, tm_out, stage_out, lane, row0, col0);
+          store_quarter<kOut, 2>(p, tm_out, stage_out, lane, row0, col0);
+          store_quarter<kOut, 3>(p, tm_out, stage_out, lane, row0, col0);
         }
+        if (!w.next(p)) break;
       }
-#pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      begins = false;
-      if (!w.next(p)) break;
-      block = w.first;
-      }
-      wait_loads();
     }
     bulk_wait_all();
   }
@@ -648,12 +674,14 @@ pe_status matmul_pair(const MatmulFp8& q, bool runs, void* workspace, DeviceStat
     PE_TRY(matmul_map(&mo, q.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                     size, q.out, q.m, q.n, (int64_t)q.n * size, 32));
+  const auto kernel = !tma_store  ? matmul_pair_kernel<kOutAnywhere>
+                      : q.out_fp32 ? matmul_pair_kernel<kOutFp32>
+                                   : matmul_pair_kernel<kOutBf16>;
   const size_t smem = sizeof(Smem) + 1024;
-  PE_CUDA_TRY(cudaFuncSetAttribute(matmul_pair_kernel,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+  PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(smem)));
   cudaFuncAttributes attr;
-  PE_CUDA_TRY(cudaFuncGetAttributes(&attr, matmul_pair_kernel));
+  PE_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
   if (static_cast<uint32_t>(attr.numRegs) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
     return PE_ERR_UNSUPPORTED;
   Params p;
@@ -669,14 +697,13 @@ pe_status matmul_pair(const MatmulFp8& q, bool runs, void* workspace, DeviceStat
   int32_t pairs = pair_count();
   p.shared_tiles = runs ? 1 : 0;
   if (!p.shared_tiles && tiles < pairs) pairs = (int32_t)tiles;
-  p.tma_store = tma_store ? 1 : 0;
   p.out_fp32 = q.out_fp32 ? 1 : 0;
   p.idesc = idesc_fp8(256, 128, q.a_e5m2, q.b_e5m2);
   p.out = q.out;
   p.parts = static_cast<float*>(workspace);
   p.status = status;
   p.wait_limit_ns = wait_limit_ns();
-  matmul_pair_kernel<<<2 * pairs, kThreads, smem, stream>>>(ma, mb, mo, p);
+  kernel<<<2 * pairs, kThreads, smem, stream>>>(ma, mb, mo, p);
   PE_CUDA_TRY(cudaGetLastError());
   if (p.shared_tiles)
     return launch_after_previous(matmul_parts_kernel, dim3((unsigned)(16 * tiles)), dim3(256), 0,
