@@ -77,6 +77,8 @@ struct Params {
   int32_t col_tiles;
   int32_t tiles;
   int32_t shared_tiles;      // 1: runs of blocks, partial tiles through `parts`
+  int32_t run_blocks;        // blocks of every pair's run, and
+  int32_t run_more;          // how many pairs get one more
   int32_t out_fp32;
   uint32_t idesc;
   void* out;
@@ -123,9 +125,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// First block of pair `p`'s run when `total` blocks are dealt to `pairs`.
-__host__ __device__ __forceinline__ int64_t run_start(int64_t total, int32_t pairs, int32_t p) {
-  return total / pairs * p + (total % pairs) * p / pairs;
+// First block of pair `q`'s run: the blocks are dealt evenly, the first pairs get one
+// more each.
+__device__ __forceinline__ int32_t run_start(const Params& p, int32_t q) {
+  return p.run_blocks * q + (q < p.run_more ? q : p.run_more);
 }
 
 // The work of a pair as segments (a tile and a run of its blocks of k), in order.
@@ -137,12 +140,11 @@ struct Walk {
   // The pair's first segment; false when it has none.
   __device__ bool start(const Params& p, int32_t pair, int32_t pairs) {
     if (p.shared_tiles) {
-      const int64_t total = (int64_t)p.tiles * p.blocks;
-      const int64_t lo = run_start(total, pairs, pair), hi = run_start(total, pairs, pair + 1);
+      const int32_t lo = run_start(p, pair), hi = run_start(p, pair + 1);
       if (lo >= hi) return false;
-      tile = (int32_t)(lo / p.blocks);
-      first = (int32_t)(lo - (int64_t)tile * p.blocks);
-      const int32_t room = (int32_t)(hi - lo);
+      tile = lo / p.blocks;
+      first = lo - tile * p.blocks;
+      const int32_t room = hi - lo;
       last = room < p.blocks - first ? first + room : p.blocks;
       left = room - (last - first);
       return true;
@@ -169,10 +171,7 @@ struct Walk {
 
 // Blocks of all of the pair's segments.
 __device__ __forceinline__ int32_t pair_blocks(const Params& p, int32_t pair, int32_t pairs) {
-  if (p.shared_tiles) {
-    const int64_t total = (int64_t)p.tiles * p.blocks;
-    return (int32_t)(run_start(total, pairs, pair + 1) - run_start(total, pairs, pair));
-  }
+  if (p.shared_tiles) return run_start(p, pair + 1) - run_start(p, pair);
   return pair < p.tiles ? ((p.tiles - 1 - pair) / pairs + 1) * p.blocks : 0;
 }
 
@@ -605,31 +604,47 @@ matmul_parts_kernel(const Params p, int32_t pairs) {
   const int rank = piece >> 3, quad = (piece >> 1) & 3, half = piece & 1;
   const int32_t rt = t / p.col_tiles, ct = t - rt * p.col_tiles;
   const int32_t row0 = rt * kTile + rank * kRows + quad * 32, col0 = ct * kTile + half * 128;
-  const int64_t total = (int64_t)p.tiles * p.blocks;
-  const int64_t lo = (int64_t)t * p.blocks, hi = lo + p.blocks;
-  // The pair that holds block `lo`: run_start(q) <= lo < run_start(q + 1).
-  int32_t q = (int32_t)(lo / (total / pairs + 1));
-  while (q + 1 < pairs && run_start(total, pairs, q + 1) <= lo) ++q;
-  if (run_start(total, pairs, q + 1) >= hi) return;      // one pair wrote the whole tile
   if (row0 >= p.m || col0 >= p.n) return;
+  const int32_t lo = t * p.blocks, hi = lo + p.blocks;   // the tile's blocks
+  // Pair q holds block `lo`: run_start(q) <= lo < run_start(q + 1).
+  const int32_t long_end = p.run_more * (p.run_blocks + 1);
+  int32_t q = lo < long_end ? lo / (p.run_blocks + 1)
+                            : p.run_more + (lo - long_end) / p.run_blocks;
+  if (run_start(p, q + 1) >= hi) return;                 // one pair wrote the whole tile
   const int row = threadIdx.x & 31, g0 = threadIdx.x >> 5;
+  const float4* parts = reinterpret_cast<const float4*>(p.parts) +
+                        (rank * 64 + half * 32) * 128 + quad * 32 + row + g0 * 128;
   griddep_wait();
   float4 sum[4] = {};
-  for (; q < pairs; ++q) {
-    const int64_t start = run_start(total, pairs, q);
-    if (start >= hi) break;
-    if (start == run_start(total, pairs, q + 1)) continue;
-    const int32_t slot = 2 * q + (start >= lo ? 0 : 1);
-    const float4* part = reinterpret_cast<const float4*>(p.parts + slot * kPartFloats) +
-                         (rank * 64 + half * 32) * 128 + quad * 32 + row;
+  // Four parts in flight, added in the order of k. A pair's part of the tile is its
+  // first segment unless its run began before the tile.
+  constexpr int kAhead = 4;
+  while (q < pairs && run_start(p, q) < hi) {
+    float4 v[kAhead][4];
+    bool in[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = part[(g0 + 8 * i) * 128];
-      sum[i].x += v.x;
-      sum[i].y += v.y;
-      sum[i].z += v.z;
-      sum[i].w += v.w;
+    for (int j = 0; j < kAhead; ++j) {
+      const int32_t start = run_start(p, q + j);
+      in[j] = q + j < pairs && start < hi;
+      const int64_t slot = 2 * (q + j) + (start >= lo ? 0 : 1);
+      if (in[j]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = parts[slot * (int64_t)(kPartFloats / 4) + 8 * i * 128];
+      }
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (in[j]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i].x += v[j][i].x;
+          sum[i].y += v[j][i].y;
+          sum[i].z += v[j][i].z;
+          sum[i].w += v[j][i].w;
+        }
+      }
+    }
+    q += kAhead;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -696,6 +711,8 @@ pe_status matmul_pair(const MatmulFp8& q, bool runs, void* workspace, DeviceStat
   p.tiles = (int32_t)tiles;
   int32_t pairs = pair_count();
   p.shared_tiles = runs ? 1 : 0;
+  p.run_blocks = (int32_t)(tiles * p.blocks / pairs);
+  p.run_more = (int32_t)(tiles * p.blocks % pairs);
   if (!p.shared_tiles && tiles < pairs) pairs = (int32_t)tiles;
   p.out_fp32 = q.out_fp32 ? 1 : 0;
   p.idesc = idesc_fp8(256, 128, q.a_e5m2, q.b_e5m2);

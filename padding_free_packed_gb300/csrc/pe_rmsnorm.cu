@@ -187,6 +187,44 @@ __device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t ste
   }
 }
 
+// Block maxima of kIter steps at once, a block of each step in kLanes neighbouring
+// lanes: every exchange halves the steps a lane carries, so three steps take five
+// shuffles instead of twelve, and each lane ends with one step's maximum.
+__host__ __device__ constexpr int pow2_at_least(int n) {
+  int p = 1;
+  while (p < n) p *= 2;
+  return p;
+}
+// The lane (within its block's lanes) that ends with step `it`.
+template <int kIter, int kLanes>
+__host__ __device__ constexpr int holder(int it) {
+  int lane = 0;
+  for (int half = pow2_at_least(kIter) / 2, off = kLanes / 2; half > 0; half /= 2, off /= 2)
+    if (it & half) lane += off;
+  return lane;
+}
+template <int kIter, int kLanes>
+__device__ __forceinline__ float max_of_blocks(const float (&amax)[kIter], int lane) {
+  constexpr int P = pow2_at_least(kIter);
+  static_assert(P <= kLanes, "one lane at least for every step");
+  float m[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) m[i] = i < kIter ? amax[i < kIter ? i : 0] : 0.f;
+  int off = kLanes / 2;
+#pragma unroll
+  for (int half = P / 2; half > 0; half /= 2, off /= 2) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = upper ? m[i] : m[i + half], keep = upper ? m[i + half] : m[i];
+      m[i] = max_nan(keep, __shfl_xor_sync(kFull, give, off));
+    }
+  }
+#pragma unroll
+  for (; off > 0; off /= 2) m[0] = max_nan(m[0], __shfl_xor_sync(kFull, m[0], off));
+  return m[0];
+}
+
 // One warp per row of up to 32 V kIter channels, held in registers: all loads
 // of a row are issued before any arithmetic.
 template <typename T, int V, int kIter, int kMode>
@@ -222,16 +260,53 @@ rmsnorm_row_kernel(const FwdArgs<T> a) {
       for (int v = 0; v < V; ++v) sq = fmaf(hv[it].get(v), hv[it].get(v), sq);
     }
     const float rstd = rsqrtf(fmaf(warp_sum(sq), a.inv_c, a.eps));
+    float y[kIter][V], amax[kIter];
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-      float h[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = hv[it].get(v);
       const int32_t c = channel<V, 1>(it, 0, lane);
-      Vec<T, V> wu[1];
-      wu[0].zero();
-      if (c < a.C) wu[0] = load_vec<T, V>(a.w + c);
-      emit<T, V, 1, kMode>(a, t, it, lane, h, wu, rstd);
+      Vec<T, V> w;
+      w.zero();
+      if (c < a.C) w = load_vec<T, V>(a.w + c);
+      amax[it] = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        y[it][v] = hv[it].get(v) * rstd * w.get(v);
+        amax[it] = max_nan(amax[it], fabsf(y[it][v]));
+      }
+      if (a.y && c < a.C) {
+        Vec<T, V> o;
+        o.put(y[it]);
+        store_vec<T, V>(a.y + t * a.C + c, o);
+      }
+    }
+    if constexpr (kMode != kNoFp8) {
+      // One lane computes one block's scale; the factors go back by shuffles.
+      constexpr bool e5 = kMode == kE5M2;
+      constexpr int lanes = kFp8Block / V;
+      const float mine = max_of_blocks<kIter, lanes>(amax, lane);
+      float factor;
+      const float scale = fp8_scale<e5>(mine, factor);
+      uint8_t* row = a.y8 + t * a.y8_ld;
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int32_t c = channel<V, 1>(it, 0, lane);
+        const int from = (lane & ~(lanes - 1)) + holder<kIter, lanes>(it);
+        const float f = __shfl_sync(kFull, factor, from);
+        if (lane == from && c / kFp8Block * kFp8Block < a.C)
+          a.scales[(int64_t)(c / kFp8Block) * a.N + t] = scale;
+        if (c < a.C) {
+          const float* q = y[it];
+          if constexpr (V == 8) {
+            uint2 o;
+            o.x = fp8x4<e5>(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
+            o.y = fp8x4<e5>(q[4] * f, q[5] * f, q[6] * f, q[7] * f);
+            *reinterpret_cast<uint2*>(row + c) = o;
+          } else {
+            *reinterpret_cast<uint32_t*>(row + c) =
+                fp8x4<e5>(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
+          }
+        }
+      }
     }
   }
 }
