@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads,
 rmsnorm_bwd_kernel(const BwdArgs<T> a) {
   constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
   constexpr int kGroups = kBlock / kGroup;
-  extern __shared__ float sums[];            // kGroup == 32: [C]
+  extern __shared__ float sums[];            // kGroup == 32: every warp's
   __shared__ float2 red[2][kBlock / 32];
   const int g = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
   float dw[kIter * V];
@@ -527,19 +527,20 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
         if (c < a.C) part[c] = dw[it * V + v];
       }
   } else {
-    for (int turn = 0; turn < kGroups; ++turn) {
-      if (group == turn) {
+    // [warp][vector element][lane], a row padded so that neither access conflicts.
+    constexpr int kLine = 33;
+    float* mine = sums + group * (kIter * V * kLine);
 #pragma unroll
-        for (int it = 0; it < kIter; ++it)
+    for (int i = 0; i < kIter * V; ++i) mine[i * kLine + g] = dw[i];
+    __syncthreads();
+    for (int32_t c = threadIdx.x; c < a.C; c += kBlock) {
+      const int vec = c / V, i = vec / 32 * V + c % V;
+      float total = 0.f;
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const int32_t c = (it * kGroup + g) * V + v;
-            if (c < a.C) sums[c] = (turn ? sums[c] : 0.f) + dw[it * V + v];
-          }
-      }
-      __syncthreads();
+      for (int w = 0; w < kGroups; ++w)
+        total += sums[(w * kIter * V + i) * kLine + vec % 32];
+      part[c] = total;
     }
-    for (int32_t c = threadIdx.x; c < a.C; c += kBlock) part[c] = sums[c];
   }
 }
 
@@ -566,7 +567,7 @@ pe_status launch_bwd_kernel(const BwdArgs<T>& a, float* dweight, cudaStream_t st
   constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
   unsigned grid = row_grid(a.N, kBlock / kGroup, kGroup > kThreads ? 1 : 2);
   if (grid > kBwdMaxBlocks) grid = kBwdMaxBlocks;
-  const size_t smem = kGroup == 32 ? (size_t)a.C * sizeof(float) : 0;
+  const size_t smem = kGroup == 32 ? (size_t)(kBlock / 32) * kIter * V * 33 * sizeof(float) : 0;
   rmsnorm_bwd_kernel<T, V, kIter, kGroup><<<grid, kBlock, smem, stream>>>(a);
   PE_CUDA_TRY(cudaGetLastError());
   return launch_after_previous(rmsnorm_dweight_kernel, dim3((unsigned)ceil_div(a.C, 32)),
