@@ -135,6 +135,27 @@ def test_rmsnorm_of_rows_with_nothing_in_them():
     assert torch.equal(q[[0, 4, 5]].float(), qc.float()) and torch.equal(s[:, [0, 4, 5]], sc)
 
 
+@pytest.mark.parametrize("c", [768, 333])
+def test_rmsnorm_sums_of_the_smallest_and_largest_numbers(c):
+    """The stored sum is the fp32 sum rounded to bf16 also for subnormal numbers,
+    sums that cancel, overflow, and infinities."""
+    x = _randn(_gen(307), 64, c).to(BF16)
+    r = _randn(_gen(308), 64, c).to(BF16)
+    x[:8] *= 2.0 ** -132
+    r[:8] *= 2.0 ** -133
+    x[8:16] = -r[8:16]
+    x[16:24] *= 2.0 ** -20
+    x[24:32], r[24:32] = 3e38, 3e38
+    x[32:40, ::3] = float("inf")
+    r[36:40, ::3] = float("-inf")
+    w = torch.ones(c, dtype=BF16, device=DEV)
+    want = (x.float() + r.float()).to(BF16)
+    _, h = pe.pe_rmsnorm(x, w, residual=r)
+    _, _, h8 = pe.pe_rmsnorm_fp8(x, w, residual=r)
+    for got in (h, h8):
+        assert torch.equal(got.nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+
+
 def test_rmsnorm_without_rows():
     x = torch.empty(0, 64, dtype=BF16, device=DEV)
     w = torch.ones(64, dtype=BF16, device=DEV)
