@@ -1,4 +1,5 @@
-// Matrix product of 8-bit operands with a scale for each block of 128.
+// Matrix product of 8-bit operands with a scale for each block of 128: the C entry,
+// the choice among the kernels, and the status word of their waits.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -38,12 +39,14 @@ std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
 }  // namespace
 
 // Estimated microseconds of every way, from times measured on a GB300 (m x n x k,
-// bf16 out; T: rows of a per CTA, S: split, whole tiles of the pair kernel last):
-//   1 x 2304 x 768     T16 4.4  T32 4.9  T64 5.9  pair 8.9
-//   1 x 1024 x 1024    T16 5.2, S8 4.4            pair 10.0
-//   320 x 2304 x 768   T16 8.9  T32 6.6  T64 6.7  pair 9.6
-//   1000 x 2304 x 768  T16 18.0 T32 11.6 T64 8.7  pair 9.9
-//   2500 x 2304 x 768                    T64 20.0 pair 14.5
+// bf16 out; T: rows of a per CTA, S: split; pair: whole tiles of the pair kernel):
+//   1 x 2304 x 768     T16 4.4   T32 4.9   T64 5.9   pair 8.9
+//   1 x 1024 x 1024    T16 5.2, S8 4.4               pair 10.0
+//   320 x 2304 x 768   T16 8.9   T32 6.6   T64 6.7   pair 8.8
+//   640 x 2304 x 768   T16 13.0  T32 9.9   T64 8.5   pair 8.8
+//   2500 x 2304 x 768                      T64 20.1  pair 12.6
+//   2304 x 768 x 4097            T32 30.6  T64 24.7  pair 20.4, runs 21.0
+//   768 x 768 x 32299  T64,S4 51.5         pair 113.9, runs 30.2
 //   200 x 200 x 20000  T16,S8 11.8  T32,S8 11.0  T64,S8 13.4
 //   100 x 1000 x 8000  T32,S2 13.9  T32,S4 9.3   T64,S8 10.7
 // A narrow CTA takes kFixed and kBlock for each block of k; CTAs that share an SM
@@ -53,10 +56,10 @@ MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
   constexpr int64_t kSms = 152, kPairs = kSms / 2;
   const int64_t blocks = ceil_div(k, kFp8Block);
   const int64_t tiles = ceil_div(m, 256) * ceil_div(n, 256);
-  const double whole = 0.6 * (double)ceil_div(tiles, kPairs) * (blocks + 1);
+  const double whole = 0.5 * (double)ceil_div(tiles, kPairs) * (blocks + 1);
   const double parts = (double)kPairs / tiles + 1;
   const double runs =
-      0.6 * (double)(ceil_div(tiles * blocks, kPairs) + ceil_div(tiles, kPairs)) + 4 + 0.6 * parts;
+      0.5 * (double)(ceil_div(tiles * blocks, kPairs) + ceil_div(tiles, kPairs)) + 8 + 0.5 * parts;
   MatmulPlan plan = {0, 1, runs < whole};
   double best = 5 + (runs < whole ? runs : whole);
   constexpr int32_t kRows[3] = {16, 32, 64};

@@ -10,6 +10,11 @@
 // of out, so stores of a warp are consecutive for any n; the scale of b is one
 // number a block, those of a one for each of the thread's kT sums.
 //
+// Measured (GB300, device time): 1 x 2304 x 768 in 4.4 us and 320 x 1001 x 1140 in
+// 6.4 us, of which a launch that does nothing is 2.3 us and each block of k 0.29 us
+// (kT = 16) to 0.43 us (64); the pair kernel takes 8.9 and 14 us. 128 rows a CTA lost
+// to 64 everywhere (640 x 2304 x 768: 9.0 against 8.4 us).
+//
 //   warps 0-3   scaling and sums
 //   warp 4      TMA producer
 //   warp 5      MMA issue

@@ -6,7 +6,15 @@
 //   backward: with n = h rstd, dx = rstd (w dy - n mean(w dy n)) (+ dresidual);
 //             dw = sum over rows of dy n.
 // All are bandwidth kernels: a row is read once, held in registers, and every
-// output written once. Statistics, products and sums are fp32.
+// output written once. Statistics, products and sums are fp32. Rows whose width or
+// address does not allow 16-byte vectors, and very wide rows, take two passes of
+// which the second finds the row in the caches.
+// Measured (GB300, device time): forward with residual and 8-bit output 32299 x 768
+// bf16 in 29.0 us (6.0 TB/s, 0.88 of the measured copy rate), 90487 x 500 fp32 in
+// 41 us (0.82); backward with the residual's gradient 32299 x 768 bf16 in 39.7 us
+// (5.0 TB/s, 0.74, 3 us of it the second kernel). The backward holds 24 weight sums a
+// thread, so two blocks of 256 threads fit an SM (three spill: 41.5 us), and waits
+// for memory; rows through a shared-memory ring did not help (46.5 us).
 #include <math.h>
 
 #include "pe_fp8.cuh"
