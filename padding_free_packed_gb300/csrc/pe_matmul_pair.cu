@@ -28,13 +28,15 @@
 //
 // Measured (GB300, device time): 169151 x 1024 x 1024 to bf16 in 153 us (2.31
 // PFLOP/s, 1.21 of the measured dense bf16 rate; the floor at twice that rate is
-// 93 us), 32299 x 2304 x 768 in 57 us, 2304 x 768 x 32299 to fp32 in 62 us. It is
-// bound by the epilogue warps: without the multiply-adds the first takes 129 us,
-// without the stores 134, with neither 109, which is the chain of hand-overs (MMAs,
-// commit, read, arrival from the other CTA 250 cycles away, next MMAs) over the two
-// accumulators of a half. Tried and slower on 169151 x 1024 x 1024: sixteen epilogue
-// warps of 64 columns 189 us, one N = 256 accumulator a block 163-166 us, output
-// straight from registers in 32-byte pieces 230 us (as 187 us through boxes).
+// 93 us), 32299 x 2304 x 768 in 57 us, 2304 x 768 x 32299 to fp32 in 62 us. The
+// epilogue's part in the first: 142 us without its multiply-adds, 134 without the
+// stores, 109 with neither; what is left then is the chain of hand-overs (MMAs,
+// commit, read, arrival from the other CTA some 250 cycles away, next MMAs) over the
+// two accumulators of a half. Tried and slower there: sixteen epilogue warps of 64
+// columns 189 us; one N = 256 accumulator a block 163 us; 256 x 128 tiles with four
+// accumulators 190 us; rows of out straight from registers in 32-byte pieces 230 us
+// (187 us through boxes then). Asking for the next block's barrier and scales before
+// the last sums changed nothing (155 us).
 #include "pe_matmul_fp8.cuh"
 
 namespace pe {

@@ -13,7 +13,7 @@
 // Measured (GB300, device time): 1 x 2304 x 768 in 4.4 us and 320 x 1001 x 1140 in
 // 6.4 us, of which a launch that does nothing is 2.3 us and each block of k 0.29 us
 // (kT = 16) to 0.43 us (64); the pair kernel takes 8.9 and 14 us. 128 rows a CTA lost
-// to 64 everywhere (640 x 2304 x 768: 9.0 against 8.4 us).
+// to 64 wherever the pair kernel did too (320 x 2304 x 768: 9.0 against 6.7 us).
 //
 //   warps 0-3   scaling and sums
 //   warp 4      TMA producer

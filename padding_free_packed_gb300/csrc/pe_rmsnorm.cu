@@ -12,7 +12,7 @@
 // Measured (GB300, device time): forward with residual and 8-bit output 32299 x 768
 // bf16 in 29.0 us (6.0 TB/s, 0.88 of the measured copy rate), 90487 x 500 fp32 in
 // 41 us (0.82); backward with the residual's gradient 32299 x 768 bf16 in 39.7 us
-// (5.0 TB/s, 0.74, 3 us of it the second kernel). The backward holds 24 weight sums a
+// (5.0 TB/s, 0.74; 2 to 3 us of it the second kernel). The backward holds 24 weight sums a
 // thread, so two blocks of 256 threads fit an SM (three spill: 41.5 us), and waits
 // for memory; rows through a shared-memory ring did not help (46.5 us).
 #include <math.h>
