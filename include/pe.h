@@ -477,7 +477,8 @@ pe_status pe_quantize_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x, i
  * and records PE_ERR_DEVICE_TIMEOUT in the device's matrix-product status word:
  * pe_read_matmul_status synchronizes `stream`, returns that word of the current
  * device and sets it back to PE_OK. One word serves all calls on a device, so
- * it tells that some product since the last read was incomplete.
+ * it tells that some product since the last read was incomplete; a product that
+ * runs on another stream during the read may be missed by it.
  * Errors: PE_ERR_INVALID_ARG for negative sizes or NULL pointers;
  * PE_ERR_OVERFLOW for sizes of 2^31 - 1024 or more, or 2^30 blocks of
  * 256 x 256 x 128;

@@ -85,10 +85,6 @@ __device__ __forceinline__ void copy_async4(void* dst, const float* src, bool in
                "r"(in ? 4 : 0)
                : "memory");
 }
-// An arrival on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void copy_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }

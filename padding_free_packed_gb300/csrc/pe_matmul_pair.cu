@@ -78,7 +78,7 @@ struct alignas(1024) Smem {
   uint32_t tmem_base;
   WaitGuard guard;
 };
-static_assert(kScaleSlots >= kScaleAhead + 4, "a slot is reused only after its last reader");
+static_assert(kScaleSlots >= kScaleAhead + 5, "a slot is reused only after its last reader");
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory exceeds the per-CTA limit");
 
 struct Params {
@@ -441,7 +441,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       for (int32_t i = 0; i < blocks; ++i) {
         const uint32_t buf = i & 1;
         if (!__all_sync(0xffffffffu, free && loaded)) {
-          if (!eager_warp_wait(acc_empty + buf * 8, ((i >> 1) & 1) ^ 1, guard, p.status, kSiteMma)) break;
+          if (!eager_warp_wait(acc_empty + buf * 8, ((i >> 1) & 1) ^ 1, guard, p.status, kSiteMma))
+            break;
           if (!eager_warp_wait(full0 + stage * 8, parity, guard, p.status, kSiteMma)) break;
         }
         tc_fence_after();
@@ -483,8 +484,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       if (more) locate();
       for (int32_t i = -kScaleAhead; i < blocks; ++i) {
         if (more) {
-          // The slot's last reader is done: that block is at least four before i,
-          // and the MMAs of block i - 2 waited for it to be read.
+          // The slot held block i - 8, and both CTAs are done with it: the MMAs of block
+          // i - 3, which have completed, waited for block i - 5 to be read.
           const int slot = (i + kScaleAhead) % kScaleSlots;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -611,6 +612,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
 __global__ void __launch_bounds__(256)
 matmul_parts_kernel(const Params p, int32_t pairs) {
   __shared__ float tile[32][129];
+  griddep_wait();                                        // before any block may leave
   const int piece = blockIdx.x & 15;                     // 2 CTAs x 4 row quarters x 2 halves
   const int32_t t = blockIdx.x >> 4;
   const int rank = piece >> 3, quad = (piece >> 1) & 3, half = piece & 1;
@@ -626,7 +628,6 @@ matmul_parts_kernel(const Params p, int32_t pairs) {
   const int row = threadIdx.x & 31, g0 = threadIdx.x >> 5;
   const float4* parts = reinterpret_cast<const float4*>(p.parts) +
                         (rank * 64 + half * 32) * 128 + quad * 32 + row + g0 * 128;
-  griddep_wait();
   float4 sum[4] = {};
   // Four parts in flight, added in the order of k. A pair's part of the tile is its
   // first segment unless its run began before the tile.
@@ -641,7 +642,8 @@ matmul_parts_kernel(const Params p, int32_t pairs) {
       const int64_t slot = 2 * (q + j) + (start >= lo ? 0 : 1);
       if (in[j]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = parts[slot * (int64_t)(kPartFloats / 4) + 8 * i * 128];
+        for (int i = 0; i < 4; ++i)
+          v[j][i] = parts[slot * (int64_t)(kPartFloats / 4) + 8 * i * 128];
       }
     }
 #pragma unroll
