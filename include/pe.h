@@ -413,7 +413,8 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  * pe_rmsnorm writes y in the I/O dtype. pe_rmsnorm_fp8 writes y, unrounded, in
  * 8 bits with 1 x 128 blocks into y8 (leading dimension y8_ld) and y8_scales
  * [ceil(channels / 128)][num_tokens], and, when y is non-NULL, also y in the
- * I/O dtype.
+ * I/O dtype. A row's result does not depend on the other rows, nor on their
+ * number (with tensors of the same alignment).
  * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
  * finite and > 0, NULL required pointers, residual_out without residual;
  * PE_ERR_UNSUPPORTED for other dtypes or devices and for an 8-bit output whose
@@ -433,7 +434,8 @@ pe_status pe_rmsnorm_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x,
  *     dweight[c] = sum over tokens of dy n.
  * dx is the gradient of x and of residual alike, in the I/O dtype; it may be
  * the buffer dy or dresidual. dweight is fp32 [channels], written (zeros when
- * num_tokens is 0) and bitwise the same in every run. channels <= 16384, else
+ * num_tokens is 0) and bitwise the same in every run. A row of dx does not depend
+ * on the other rows. channels <= 16384, else
  * PE_ERR_UNSUPPORTED. workspace: device, 16-byte aligned, >=
  * pe_rmsnorm_bwd_workspace_size(channels) bytes, else PE_ERR_WORKSPACE. */
 size_t pe_rmsnorm_bwd_workspace_size(int32_t channels);

@@ -33,46 +33,36 @@ enum Mode { kNoFp8 = 0, kE4M3 = 1, kE5M2 = 2 };
 // until they are used.
 template <typename T, int V>
 struct Vec;
-template <>
-struct Vec<float, 1> {
-  float w;
-  __device__ float get(int) const { return w; }
-  __device__ void zero() { w = 0.f; }
-  __device__ void put(const float* x) { w = x[0]; }
-  __device__ void add(const Vec& o) { w += o.w; }
-};
-template <>
-struct Vec<__nv_bfloat16, 1> {
-  __nv_bfloat16 w;
-  __device__ float get(int) const { return __bfloat162float(w); }
-  __device__ void zero() { w = __float2bfloat16_rn(0.f); }
-  __device__ void put(const float* x) { w = __float2bfloat16_rn(x[0]); }
-  __device__ void add(const Vec& o) { w = __float2bfloat16_rn(get(0) + o.get(0)); }
-};
-template <>
-struct alignas(16) Vec<float, 4> {
-  float w[4];
+template <int V>
+struct alignas(4 * V) Vec<float, V> {
+  float w[V];
   __device__ float get(int v) const { return w[v]; }
-  __device__ void zero() { w[0] = w[1] = w[2] = w[3] = 0.f; }
+  __device__ void zero() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = 0.f;
+  }
   __device__ void put(const float* x) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) w[v] = x[v];
+    for (int v = 0; v < V; ++v) w[v] = x[v];
   }
   __device__ void add(const Vec& o) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) w[v] += o.w[v];
+    for (int v = 0; v < V; ++v) w[v] += o.w[v];
   }
 };
-template <>
-struct alignas(16) Vec<__nv_bfloat16, 8> {
-  uint32_t w[4];
+template <int V>
+struct alignas(2 * V) Vec<__nv_bfloat16, V> {
+  uint32_t w[V / 2];
   __device__ float get(int v) const {
     return __uint_as_float(v & 1 ? w[v >> 1] & 0xffff0000u : w[v >> 1] << 16);
   }
-  __device__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ void zero() {
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) w[v] = 0u;
+  }
   __device__ void put(const float* x) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < V / 2; ++v) {
       const __nv_bfloat162 pair = __floats2bfloat162_rn(x[2 * v], x[2 * v + 1]);
       w[v] = *reinterpret_cast<const uint32_t*>(&pair);
     }
@@ -81,35 +71,57 @@ struct alignas(16) Vec<__nv_bfloat16, 8> {
   // unless one is below 2^-16 of the other, when rounding it first changes nothing.
   __device__ void add(const Vec& o) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < V / 2; ++v) {
       const __nv_bfloat162 sum = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&w[v]),
                                             *reinterpret_cast<const __nv_bfloat162*>(&o.w[v]));
       w[v] = *reinterpret_cast<const uint32_t*>(&sum);
     }
   }
 };
+template <>
+struct Vec<__nv_bfloat16, 1> {
+  __nv_bfloat16 w[1];
+  __device__ float get(int) const { return __bfloat162float(w[0]); }
+  __device__ void zero() { w[0] = __float2bfloat16_rn(0.f); }
+  __device__ void put(const float* x) { w[0] = __float2bfloat16_rn(x[0]); }
+  __device__ void add(const Vec& o) { w[0] = __float2bfloat16_rn(get(0) + o.get(0)); }
+};
+
+// One access of a vector's bytes.
+template <int kBytes>
+struct Bits;
+template <>
+struct Bits<2> { using type = uint16_t; };
+template <>
+struct Bits<4> { using type = uint32_t; };
+template <>
+struct Bits<8> { using type = uint2; };
+template <>
+struct Bits<16> { using type = uint4; };
 
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
+  using B = typename Bits<(int)sizeof(T) * V>::type;
   Vec<T, V> v;
-  if constexpr (V > 1)
-    *reinterpret_cast<uint4*>(v.w) = *reinterpret_cast<const uint4*>(p);
-  else
-    v.w = *p;
+  *reinterpret_cast<B*>(v.w) = *reinterpret_cast<const B*>(p);
   return v;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
-  if constexpr (V > 1)
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v.w);
-  else
-    *p = v.w;
+  using B = typename Bits<(int)sizeof(T) * V>::type;
+  *reinterpret_cast<B*>(p) = *reinterpret_cast<const B*>(v.w);
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
   return x;
+}
+
+// A barrier of the kGroup threads that share a row.
+template <int kGroup>
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kGroup) : "memory");
 }
 
 template <typename T>
@@ -134,6 +146,23 @@ struct FwdArgs {
 template <int V, int U>
 __device__ __forceinline__ int32_t channel(int32_t step, int u, int lane) {
   return (step * U + u) * 32 * V + lane * V;
+}
+
+// V neighbouring 8-bit values.
+template <int V, bool e5>
+__device__ __forceinline__ void store_fp8(uint8_t* p, const float* q, float f) {
+  if constexpr (V == 8) {
+    uint2 o;
+    o.x = fp8x4<e5>(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
+    o.y = fp8x4<e5>(q[4] * f, q[5] * f, q[6] * f, q[7] * f);
+    *reinterpret_cast<uint2*>(p) = o;
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint32_t*>(p) = fp8x4<e5>(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)fp8x2<e5>(q[0] * f, q[1] * f);
+  } else {
+    *p = (uint8_t)fp8x2<e5>(q[0] * f, 0.f);
+  }
 }
 
 // Output of one step from its h: y in T when wanted, and the 8-bit block.
@@ -178,18 +207,7 @@ __device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t ste
     for (int u = 0; u < U; ++u) {
       const int32_t c = channel<V, U>(step, u, lane);
       if (c < a.C) {
-        const float* q = y + u * V;
-        if constexpr (V == 8) {
-          uint2 o;
-          o.x = fp8x4<e5>(q[0] * factor, q[1] * factor, q[2] * factor, q[3] * factor);
-          o.y = fp8x4<e5>(q[4] * factor, q[5] * factor, q[6] * factor, q[7] * factor);
-          *reinterpret_cast<uint2*>(row + c) = o;
-        } else if constexpr (V == 4) {
-          *reinterpret_cast<uint32_t*>(row + c) =
-              fp8x4<e5>(q[0] * factor, q[1] * factor, q[2] * factor, q[3] * factor);
-        } else {
-          row[c] = (uint8_t)fp8x2<e5>(q[0] * factor, 0.f);
-        }
+        store_fp8<V, e5>(row + c, y + u * V, factor);
       }
     }
   }
@@ -233,86 +251,113 @@ __device__ __forceinline__ float max_of_blocks(const float (&amax)[kIter], int l
   return m[0];
 }
 
-// One warp per row of up to 32 V kIter channels, held in registers: all loads
-// of a row are issued before any arithmetic.
-template <typename T, int V, int kIter, int kMode>
-__global__ void __launch_bounds__(kThreads, kIter <= 4 ? 4 : 2)
-rmsnorm_row_kernel(const FwdArgs<T> a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < a.N;
-       t += warps) {
-    Vec<T, V> hv[kIter], rv[kIter];
+// x[0] .. x[N - 1], N a power of two: the second half is added to the first, and again.
+template <int N>
+__device__ __forceinline__ float sum_of_halves(float (&x)[N]) {
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int32_t c = channel<V, 1>(it, 0, lane);
-      hv[it].zero();
-      if (c < a.C) hv[it] = load_vec<T, V>(a.x + t * a.C + c);
+  for (int half = N / 2; half > 0; half /= 2)
+#pragma unroll
+    for (int i = 0; i < half; ++i) x[i] += x[i + half];
+  return x[0];
+}
+
+// Vectors of a warp that make up a whole block of 128 channels.
+template <int V>
+constexpr int kUnit = V < 4 ? 4 / V : 1;
+
+// kWarps warps per row of up to 32 V kUnit kIter kWarps channels, held in registers:
+// all loads of a row are issued before any arithmetic. A warp has every kWarps-th
+// step of the row, so whole blocks. A row's sum of squares does not depend on kWarps,
+// nor its bits on the rows beside it: a lane's steps j, j + 8, .. make up its sum j,
+// the sums are added as ((0 4) (2 6)) ((1 5) (3 7)), a pair of halves at a time in
+// whichever warp holds both, and the lanes' totals last.
+template <typename T, int V, int kIter, int kWarps, int kBlocks, int kMode>
+__global__ void __launch_bounds__(kThreads, kBlocks) rmsnorm_row_kernel(const FwdArgs<T> a) {
+  constexpr int U = kUnit<V>, kVecs = kIter * U, kRows = kThreads / (32 * kWarps);
+  constexpr int kSums = 8 / kWarps;          // sums of a lane in each warp
+  __shared__ float red[2][kThreads];
+  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / kWarps;
+  const int warp = (threadIdx.x >> 5) % kWarps;
+  int phase = 0;
+  for (int64_t t = (int64_t)blockIdx.x * kRows + group; t < a.N;
+       t += (int64_t)gridDim.x * kRows) {
+    Vec<T, V> hv[kVecs], rv[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int32_t c = channel<V, U>(i / U * kWarps + warp, i % U, lane);
+      hv[i].zero();
+      if (c < a.C) hv[i] = load_vec<T, V>(a.x + t * a.C + c);
     }
     if (a.res) {
 #pragma unroll
-      for (int it = 0; it < kIter; ++it) {
-        const int32_t c = channel<V, 1>(it, 0, lane);
-        if (c < a.C) rv[it] = load_vec<T, V>(a.res + t * a.C + c);
+      for (int i = 0; i < kVecs; ++i) {
+        const int32_t c = channel<V, U>(i / U * kWarps + warp, i % U, lane);
+        if (c < a.C) rv[i] = load_vec<T, V>(a.res + t * a.C + c);
       }
     }
-    float sq = 0.f;
+    float sums[kSums];
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int32_t c = channel<V, 1>(it, 0, lane);
+    for (int i = 0; i < kSums; ++i) sums[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int32_t c = channel<V, U>(i / U * kWarps + warp, i % U, lane);
       if (a.res && c < a.C) {
-        hv[it].add(rv[it]);
-        if (a.res_out) store_vec<T, V>(a.res_out + t * a.C + c, hv[it]);
+        hv[i].add(rv[i]);
+        if (a.res_out) store_vec<T, V>(a.res_out + t * a.C + c, hv[i]);
       }
+      float& sq = sums[i / U % kSums];
 #pragma unroll
-      for (int v = 0; v < V; ++v) sq = fmaf(hv[it].get(v), hv[it].get(v), sq);
+      for (int v = 0; v < V; ++v) sq = fmaf(hv[i].get(v), hv[i].get(v), sq);
     }
-    const float rstd = rsqrtf(fmaf(warp_sum(sq), a.inv_c, a.eps));
-    float y[kIter][V], amax[kIter];
+    float sq = sum_of_halves<kSums>(sums);
+    if constexpr (kWarps > 1) {              // two sets of sums: one barrier a row
+      red[phase][threadIdx.x] = sq;
+      group_sync<32 * kWarps>(group);
+      float all[kWarps];
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int32_t c = channel<V, 1>(it, 0, lane);
+      for (int i = 0; i < kWarps; ++i) all[i] = red[phase][(group * kWarps + i) * 32 + lane];
+      sq = sum_of_halves<kWarps>(all);
+      phase ^= 1;
+    }
+    sq = warp_sum(sq);
+    const float rstd = rsqrtf(fmaf(sq, a.inv_c, a.eps));
+    float y[kVecs][V], amax[kIter];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int32_t c = channel<V, U>(i / U * kWarps + warp, i % U, lane);
       Vec<T, V> w;
       w.zero();
       if (c < a.C) w = load_vec<T, V>(a.w + c);
-      amax[it] = 0.f;
+      if (i % U == 0) amax[i / U] = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        y[it][v] = hv[it].get(v) * rstd * w.get(v);
-        amax[it] = max_nan(amax[it], fabsf(y[it][v]));
+        y[i][v] = hv[i].get(v) * rstd * w.get(v);
+        amax[i / U] = max_nan(amax[i / U], fabsf(y[i][v]));
       }
       if (a.y && c < a.C) {
         Vec<T, V> o;
-        o.put(y[it]);
+        o.put(y[i]);
         store_vec<T, V>(a.y + t * a.C + c, o);
       }
     }
     if constexpr (kMode != kNoFp8) {
       // One lane computes one block's scale; the factors go back by shuffles.
       constexpr bool e5 = kMode == kE5M2;
-      constexpr int lanes = kFp8Block / V;
+      constexpr int lanes = kFp8Block / (V * U);
       const float mine = max_of_blocks<kIter, lanes>(amax, lane);
       float factor;
       const float scale = fp8_scale<e5>(mine, factor);
       uint8_t* row = a.y8 + t * a.y8_ld;
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
-        const int32_t c = channel<V, 1>(it, 0, lane);
         const int from = (lane & ~(lanes - 1)) + holder<kIter, lanes>(it);
         const float f = __shfl_sync(kFull, factor, from);
-        if (lane == from && c / kFp8Block * kFp8Block < a.C)
-          a.scales[(int64_t)(c / kFp8Block) * a.N + t] = scale;
-        if (c < a.C) {
-          const float* q = y[it];
-          if constexpr (V == 8) {
-            uint2 o;
-            o.x = fp8x4<e5>(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
-            o.y = fp8x4<e5>(q[4] * f, q[5] * f, q[6] * f, q[7] * f);
-            *reinterpret_cast<uint2*>(row + c) = o;
-          } else {
-            *reinterpret_cast<uint32_t*>(row + c) =
-                fp8x4<e5>(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
-          }
+        const int32_t block = channel<V, U>(it * kWarps + warp, 0, lane) / kFp8Block;
+        if (lane == from && block * kFp8Block < a.C) a.scales[(int64_t)block * a.N + t] = scale;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int32_t c = channel<V, U>(it * kWarps + warp, u, lane);
+          if (c < a.C) store_fp8<V, e5>(row + c, y[it * U + u], f);
         }
       }
     }
@@ -326,7 +371,7 @@ rmsnorm_row_kernel(const FwdArgs<T> a) {
 template <typename T, int V, int kMode>
 __global__ void __launch_bounds__(kThreads)
 rmsnorm_any_kernel(const FwdArgs<T> a) {
-  constexpr int U = V == 1 ? 4 : 1;
+  constexpr int U = kUnit<V>;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
   const int32_t steps = (a.C + 32 * V * U - 1) / (32 * V * U);
@@ -380,30 +425,76 @@ unsigned row_grid(int64_t rows, int rows_per_block, int blocks_per_sm) {
   return (unsigned)(blocks < cap ? blocks : cap);
 }
 
+template <typename T, int V, int kIter, int kWarps, int kBlocks, int kMode>
+void launch_row(const FwdArgs<T>& a, cudaStream_t stream) {
+  rmsnorm_row_kernel<T, V, kIter, kWarps, kBlocks, kMode>
+      <<<row_grid(a.N, kThreads / (32 * kWarps), 16), kThreads, 0, stream>>>(a);
+}
+
+// The form for V neighbouring channels per access: warps a row, vectors a lane and
+// blocks an SM, by the row's width. Few rows (two an SM) take a block each: 300 x 768
+// bf16 in 2.5 us (a warp each 3.2), 300 x 2001 in 4.4 (two passes 35).
+// Many rows keep 16 to 20 channels a lane: with more the registers leave too few
+// rows in flight, with fewer the barrier shows. bf16, residual, 8-bit output:
+//   90487 x 500  V 4: 1 warp 53 us, 2 warps 65;      V 1: 1 warp 86, 2 warps 100
+//   32299 x 768  V 8: 1 warp 29 us, 2 warps 32 (fp32 40000 rows: 62 both)
+//   32299 x 1024 V 8: 1 warp 38 us, 2 warps 38, 4 warps 47
+//   32299 x 2304 V 4: 4 warps 83 us, 8 warps 99;     V 8: 2 warps 84, 1 warp 97
+//   32299 x 2001 V 1: 8 warps 141 us, 4 warps 252, two passes 212
+template <typename T, int V, int kMode>
+void launch_rows(const FwdArgs<T>& a, cudaStream_t stream) {
+  const int32_t C = a.C;
+  const bool few = a.N <= 2 * (int64_t)device_sm_count() && C > 256;
+  if constexpr (V == 8) {
+    if (C > 2048 && C <= 2560) return launch_rows<T, 4, kMode>(a, stream);
+    if (few && C <= 2048) return launch_row<T, V, 1, 8, 6, kMode>(a, stream);
+    if (C <= 256) return launch_row<T, V, 1, 1, 6, kMode>(a, stream);
+    if (C <= 512) return launch_row<T, V, 2, 1, 4, kMode>(a, stream);
+    if (C <= 768) return launch_row<T, V, 3, 1, 3, kMode>(a, stream);
+    if (C <= 1024) return launch_row<T, V, 2, 2, 4, kMode>(a, stream);
+    if (C <= 1536) return launch_row<T, V, 3, 2, 3, kMode>(a, stream);
+    if (C <= 2048) return launch_row<T, V, 2, 4, 4, kMode>(a, stream);
+    if (C <= 4096) return launch_row<T, V, 2, 8, 4, kMode>(a, stream);
+  } else {
+    if (!few) {
+      if (C <= 256) return launch_row<T, V, 2, 1, V == 1 ? 4 : 6, kMode>(a, stream);
+      if (C <= 512) return launch_row<T, V, 4, 1, 4, kMode>(a, stream);
+      if (C <= 768) return launch_row<T, V, 3, 2, 4, kMode>(a, stream);
+      if constexpr (V > 1) {
+        if (C <= 1024) return launch_row<T, V, 4, 2, 4, kMode>(a, stream);
+      }
+      if (C > 1024 && C <= 1536) return launch_row<T, V, 3, 4, 4, kMode>(a, stream);
+      if constexpr (V > 1) {
+        if (C > 1024 && C <= 2560)
+          return launch_row<T, V, 5, 4, V == 4 ? 4 : 3, kMode>(a, stream);
+      }
+    }
+    if (C <= 1 * 1024) return launch_row<T, V, 1, 8, 6, kMode>(a, stream);
+    if (C <= 2 * 1024) return launch_row<T, V, 2, 8, 4, kMode>(a, stream);
+    if (C <= 3 * 1024) return launch_row<T, V, 3, 8, 4, kMode>(a, stream);
+  }
+  rmsnorm_any_kernel<T, V, kMode><<<row_grid(a.N, kThreads / 32, 16), kThreads, 0, stream>>>(a);
+}
+
+// Whether rows of C channels and their tensors allow accesses of V channels.
+template <int V, typename T, typename... P>
+bool vectors(int32_t C, const T* p, P... rest) {
+  bool ok = C % V == 0 && aligned(p, V * sizeof(T));
+  ((ok = ok && aligned(rest, V * sizeof(T))), ...);
+  return ok;
+}
+
 template <typename T, int kMode>
 pe_status launch_fwd(const FwdArgs<T>& a, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(T);
-  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.w, 16) &&
-                   (!a.y || aligned(a.y, 16)) && (!a.res || aligned(a.res, 16)) &&
-                   (!a.res_out || aligned(a.res_out, 16));
-  const unsigned grid = row_grid(a.N, kThreads / 32, 16);
-  const int64_t steps = ceil_div(a.C, 32 * V);
-  if (!vec)
-    rmsnorm_any_kernel<T, 1, kMode><<<grid, kThreads, 0, stream>>>(a);
-  else if (steps <= 1)
-    rmsnorm_row_kernel<T, V, 1, kMode><<<grid, kThreads, 0, stream>>>(a);
-  else if (steps <= 2)
-    rmsnorm_row_kernel<T, V, 2, kMode><<<grid, kThreads, 0, stream>>>(a);
-  else if (steps <= 3)
-    rmsnorm_row_kernel<T, V, 3, kMode><<<grid, kThreads, 0, stream>>>(a);
-  else if (steps <= 4)
-    rmsnorm_row_kernel<T, V, 4, kMode><<<grid, kThreads, 0, stream>>>(a);
-  else if (steps <= 6)
-    rmsnorm_row_kernel<T, V, 6, kMode><<<grid, kThreads, 0, stream>>>(a);
-  else if (steps <= 9)
-    rmsnorm_row_kernel<T, V, 9, kMode><<<grid, kThreads, 0, stream>>>(a);
+  if (vectors<V>(a.C, a.x, a.w, a.y, a.res, a.res_out))
+    launch_rows<T, V, kMode>(a, stream);
+  else if (vectors<4>(a.C, a.x, a.w, a.y, a.res, a.res_out))
+    launch_rows<T, 4, kMode>(a, stream);
+  else if (vectors<2>(a.C, a.x, a.w, a.y, a.res, a.res_out))
+    launch_rows<T, 2, kMode>(a, stream);
   else
-    rmsnorm_any_kernel<T, V, kMode><<<grid, kThreads, 0, stream>>>(a);
+    launch_rows<T, 1, kMode>(a, stream);
   PE_CUDA_TRY(cudaGetLastError());
   return PE_OK;
 }
@@ -431,7 +522,7 @@ pe_status run_fwd(int mode, const void* x, const void* res, const void* w, int64
 
 // ---------------------------------------------------------------- backward
 constexpr int32_t kBwdMaxChannels = 16384;
-constexpr int kBwdMaxBlocks = 480;
+constexpr int kBwdMaxBlocks = 640;
 
 template <typename T>
 struct BwdArgs {
@@ -451,9 +542,8 @@ struct BwdArgs {
 // of V channels, the same for all of its rows: the weight's gradient stays in
 // fp32 registers until the block's last row. Blocks of warps add their warps'
 // sums in warp order.
-template <typename T, int V, int kIter, int kGroup>
-__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads,
-                                  kGroup > kThreads ? 1 : kIter * V <= 16 ? 3 : 2)
+template <typename T, int V, int kIter, int kGroup, int kBlocks>
+__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads, kBlocks)
 rmsnorm_bwd_kernel(const BwdArgs<T> a) {
   constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
   constexpr int kGroups = kBlock / kGroup;
@@ -493,14 +583,15 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
     }
     sq = warp_sum(sq);
     dot = warp_sum(dot);
-    if constexpr (kGroup > 32) {             // kGroups == 1: the loop is uniform in the block
+    if constexpr (kGroup > 32) {
       if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = make_float2(sq, dot);
-      __syncthreads();
+      group_sync<kGroup>(group);
       sq = dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < kBlock / 32; ++i) {
-        sq += red[phase][i].x;
-        dot += red[phase][i].y;
+      for (int i = 0; i < kGroup / 32; ++i) {
+        const float2 r = red[phase][group * (kGroup / 32) + i];
+        sq += r.x;
+        dot += r.y;
       }
       phase ^= 1;
     }
@@ -526,7 +617,7 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
     }
   }
   float* part = a.part + (int64_t)blockIdx.x * a.C;
-  if constexpr (kGroup > 32) {
+  if constexpr (kGroups == 1) {
 #pragma unroll
     for (int it = 0; it < kIter; ++it)
 #pragma unroll
@@ -535,18 +626,18 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
         if (c < a.C) part[c] = dw[it * V + v];
       }
   } else {
-    // [warp][vector element][lane], a row padded so that neither access conflicts.
-    constexpr int kLine = 33;
+    // [group][vector element][thread], a row padded so that neither access conflicts.
+    constexpr int kLine = kGroup + 1;
     float* mine = sums + group * (kIter * V * kLine);
 #pragma unroll
     for (int i = 0; i < kIter * V; ++i) mine[i * kLine + g] = dw[i];
     __syncthreads();
     for (int32_t c = threadIdx.x; c < a.C; c += kBlock) {
-      const int vec = c / V, i = vec / 32 * V + c % V;
+      const int vec = c / V, i = vec / kGroup * V + c % V;
       float total = 0.f;
 #pragma unroll
       for (int w = 0; w < kGroups; ++w)
-        total += sums[(w * kIter * V + i) * kLine + vec % 32];
+        total += sums[(w * kIter * V + i) * kLine + vec % kGroup];
       part[c] = total;
     }
   }
@@ -570,24 +661,77 @@ rmsnorm_dweight_kernel(const float* __restrict__ part, int32_t blocks, int32_t C
   if (x == 0 && blockIdx.x * 32 + y < C) dweight[blockIdx.x * 32 + y] = s;
 }
 
-template <typename T, int V, int kIter, int kGroup>
+template <typename T, int V, int kIter, int kGroup, int kBlocks>
 pe_status launch_bwd_kernel(const BwdArgs<T>& a, float* dweight, cudaStream_t stream) {
   constexpr int kBlock = kGroup > kThreads ? kGroup : kThreads;
-  unsigned grid = row_grid(a.N, kBlock / kGroup, kGroup > kThreads ? 1 : 2);
+  unsigned grid = row_grid(a.N, kBlock / kGroup, kBlocks);
   if (grid > kBwdMaxBlocks) grid = kBwdMaxBlocks;
-  const size_t smem = kGroup == 32 ? (size_t)(kBlock / 32) * kIter * V * 33 * sizeof(float) : 0;
-  rmsnorm_bwd_kernel<T, V, kIter, kGroup><<<grid, kBlock, smem, stream>>>(a);
+  constexpr size_t smem =
+      kGroup < kBlock ? (size_t)(kBlock / kGroup) * kIter * V * (kGroup + 1) * sizeof(float) : 0;
+  static_assert(smem <= 47 << 10, "the sums fit without an opt-in");
+  rmsnorm_bwd_kernel<T, V, kIter, kGroup, kBlocks><<<grid, kBlock, smem, stream>>>(a);
   PE_CUDA_TRY(cudaGetLastError());
   return launch_after_previous(rmsnorm_dweight_kernel, dim3((unsigned)ceil_div(a.C, 32)),
                                dim3(1024), 0, stream, (const float*)a.part, (int32_t)grid, a.C,
                                dweight);
 }
 
+// The form for V neighbouring channels per access: vectors a thread, threads a row and
+// blocks an SM, by the row's width; 8 to 20 weight sums a thread. With the residual's
+// gradient:
+//   bf16 32299 x 768   V 8: 64 threads 40.1 us, 32 40.5, 128 43.7, 256 (two blocks) 108
+//   bf16 32299 x 2304  V 4: 128 threads 106 us;      V 8: 64 112, 128 116, 256 118
+//   fp32 40000 x 1024  V 4: 128 threads 99 us, 64 104, 256 112, 32 118
+//   fp32 20000 x 2304  V 4: 256 threads 113 us, 128 120, 64 175
+//   bf16 90487 x 501   V 1: 64 threads 91 us, 32 105, 128 110, 256 170
+template <typename T, int V>
+pe_status launch_bwd(const BwdArgs<T>& a, float* dweight, cudaStream_t stream) {
+  constexpr bool bf16 = sizeof(T) == 2;
+  const int32_t C = a.C;
+  if constexpr (V == 8) {
+    if (C <= 256) return launch_bwd_kernel<T, V, 1, 32, 3>(a, dweight, stream);
+    if (C <= 512) return launch_bwd_kernel<T, V, 2, 32, 3>(a, dweight, stream);
+    if (C <= 1024) return launch_bwd_kernel<T, V, 2, 64, 3>(a, dweight, stream);
+    if (C <= 2048) return launch_bwd_kernel<T, V, 2, 128, 3>(a, dweight, stream);
+    if (C <= 2560) return launch_bwd<T, 4>(a, dweight, stream);
+    if (C <= 4096) return launch_bwd_kernel<T, V, 2, 256, 4>(a, dweight, stream);
+    return launch_bwd_kernel<T, V, 2, 1024, 1>(a, dweight, stream);
+  } else if constexpr (V == 4) {
+    if (C <= 256) return launch_bwd_kernel<T, V, 2, 32, 3>(a, dweight, stream);
+    if constexpr (bf16) {
+      if (C <= 512) return launch_bwd_kernel<T, V, 4, 32, 3>(a, dweight, stream);
+      if (C <= 1024) return launch_bwd_kernel<T, V, 4, 64, 3>(a, dweight, stream);
+      if (C <= 2560) return launch_bwd_kernel<T, V, 5, 128, 3>(a, dweight, stream);
+    } else {
+      if (C <= 768) return launch_bwd_kernel<T, V, 3, 64, 3>(a, dweight, stream);
+      if (C <= 1024) return launch_bwd_kernel<T, V, 2, 128, 4>(a, dweight, stream);
+    }
+    if (C <= 3 * 1024) return launch_bwd_kernel<T, V, 3, 256, 4>(a, dweight, stream);
+    return launch_bwd_kernel<T, V, 4, 1024, 1>(a, dweight, stream);
+  } else {
+    if constexpr (V == 2) {
+      if constexpr (bf16) {
+        if (C <= 512) return launch_bwd_kernel<T, V, 8, 32, 3>(a, dweight, stream);
+        if (C <= 1024) return launch_bwd_kernel<T, V, 8, 64, 3>(a, dweight, stream);
+      } else {
+        if (C <= 256) return launch_bwd_kernel<T, V, 4, 32, 3>(a, dweight, stream);
+        if (C <= 1024) return launch_bwd_kernel<T, V, 4, 128, 4>(a, dweight, stream);
+      }
+      if (C <= 2304) return launch_bwd_kernel<T, V, 9, 128, bf16 ? 3 : 2>(a, dweight, stream);
+    } else {
+      if (C <= 256) return launch_bwd_kernel<T, V, 8, 32, 4>(a, dweight, stream);
+      if (C <= 512) return launch_bwd_kernel<T, V, 8, 64, 3>(a, dweight, stream);
+      if (C <= 1024) return launch_bwd_kernel<T, V, 8, 128, bf16 ? 4 : 3>(a, dweight, stream);
+      if (C <= 2304) return launch_bwd_kernel<T, V, 9, 256, 3>(a, dweight, stream);
+    }
+    return launch_bwd_kernel<T, V, 16 / V, 1024, 1>(a, dweight, stream);
+  }
+}
+
 template <typename T>
 pe_status run_bwd(const void* dy, const void* h, const void* w, const void* dres, int64_t N,
                   int32_t C, float eps, void* dx, float* dweight, void* ws,
                   cudaStream_t stream) {
-  constexpr int V = 16 / sizeof(T);
   const BwdArgs<T> a = {static_cast<const T*>(dy),
                         static_cast<const T*>(h),
                         static_cast<const T*>(w),
@@ -598,24 +742,11 @@ pe_status run_bwd(const void* dy, const void* h, const void* w, const void* dres
                         eps,
                         static_cast<T*>(dx),
                         static_cast<float*>(ws)};
-  const bool vec = C % V == 0 && aligned(dy, 16) && aligned(h, 16) && aligned(w, 16) &&
-                   aligned(dx, 16) && (!dres || aligned(dres, 16));
-  if (vec) {
-    const int64_t warp_steps = ceil_div(C, 32 * V), block_steps = ceil_div(C, 256 * V);
-    if (warp_steps <= 1) return launch_bwd_kernel<T, V, 1, 32>(a, dweight, stream);
-    if (warp_steps <= 2) return launch_bwd_kernel<T, V, 2, 32>(a, dweight, stream);
-    if (warp_steps <= 3) return launch_bwd_kernel<T, V, 3, 32>(a, dweight, stream);
-    if (warp_steps <= 4) return launch_bwd_kernel<T, V, 4, 32>(a, dweight, stream);
-    if (block_steps <= 1) return launch_bwd_kernel<T, V, 1, 256>(a, dweight, stream);
-    if (block_steps <= 2) return launch_bwd_kernel<T, V, 2, 256>(a, dweight, stream);
-    return launch_bwd_kernel<T, V, 16 / V * 1, 1024>(a, dweight, stream);
-  }
-  const int64_t steps = ceil_div(C, 256);
-  if (steps <= 1) return launch_bwd_kernel<T, 1, 1, 256>(a, dweight, stream);
-  if (steps <= 2) return launch_bwd_kernel<T, 1, 2, 256>(a, dweight, stream);
-  if (steps <= 4) return launch_bwd_kernel<T, 1, 4, 256>(a, dweight, stream);
-  if (steps <= 9) return launch_bwd_kernel<T, 1, 9, 256>(a, dweight, stream);
-  return launch_bwd_kernel<T, 1, 16, 1024>(a, dweight, stream);
+  if (sizeof(T) == 2 && vectors<8>(C, a.dy, a.w, a.h, a.dx, a.dres))
+    return launch_bwd<T, 16 / sizeof(T)>(a, dweight, stream);
+  if (vectors<4>(C, a.dy, a.w, a.h, a.dx, a.dres)) return launch_bwd<T, 4>(a, dweight, stream);
+  if (vectors<2>(C, a.dy, a.w, a.h, a.dx, a.dres)) return launch_bwd<T, 2>(a, dweight, stream);
+  return launch_bwd<T, 1>(a, dweight, stream);
 }
 
 bool dtype_ok(pe_dtype d) { return d == PE_BF16 || d == PE_FP32; }

@@ -98,6 +98,32 @@ def test_rmsnorm_fp8(dtype, fp8, c):
     assert torch.equal(plain.float(), got.float()) and torch.equal(plain_scales, scales)
 
 
+# One width at least for every number of neighbouring channels an access can have (8, 4, 2,
+# 1) and every number of warps a row is given; rows enough that a warp has several of them.
+MANY = [(20011, 250), (20011, 255), (20011, 506), (20011, 501), (9001, 764), (9001, 758),
+        (9001, 777), (5003, 1012), (5003, 1018), (5003, 1001), (5003, 1500), (5003, 1502),
+        (5003, 1501), (2503, 1536), (2503, 2048), (5003, 2001), (2503, 2304), (2503, 2300),
+        (2503, 2302), (2503, 2301), (2503, 2900), (2503, 2902), (2503, 2904), (2503, 4100)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,c", MANY)
+def test_rmsnorm_of_many_rows(n, c, dtype):
+    gen = _gen(308)
+    x, r = (_randn(gen, n, c) * 2).to(dtype), _randn(gen, n, c).to(dtype)
+    w = (1 + 0.3 * _randn(gen, c)).to(dtype)
+    want, h = ref.rmsnorm(x, w, 1e-5, r)
+    y = torch.empty_like(x)
+    q, scales, got_h = pe.pe_rmsnorm_fp8(x, w, 1e-5, residual=r, y=y)
+    assert torch.equal(got_h, h)
+    _close(y, want, ref.rmsnorm_rel(c), dtype, f"y {n} x {c}")
+    ref.check_quantized(q, scales, want, E4M3, 1, ref.rmsnorm_rel(c), f"rmsnorm_fp8 {n} x {c}")
+    few = pe.pe_rmsnorm_fp8(x[:3], w, 1e-5, residual=r[:3])       # a row's bits are its own
+    assert torch.equal(few[0].float(), q[:3].float()) and torch.equal(few[1], scales[:, :3])
+    plain, got_h = pe.pe_rmsnorm(x, w, 1e-5, residual=r, out=x, residual_out=r)   # in place
+    assert torch.equal(plain, y) and torch.equal(r, h) and got_h.data_ptr() == r.data_ptr()
+
+
 @pytest.mark.parametrize("c", [768, 1001, 9000])
 def test_rmsnorm_in_place(c):
     """residual_out may be the residual's buffer and y may be x's."""
@@ -189,6 +215,24 @@ def test_rmsnorm_bwd(dtype, c, n, with_residual):
     into = dy.clone()                                           # dx over dy
     over, _ = pe.pe_rmsnorm_bwd(into, h, w, 1e-5, dresidual=dr, out=into)
     assert torch.equal(over, dx)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,c", MANY)
+def test_rmsnorm_bwd_of_many_rows(n, c, dtype):
+    gen = _gen(309)
+    h, dy = (_randn(gen, n, c) * 1.5).to(dtype), _randn(gen, n, c).to(dtype)
+    w = (1 + 0.3 * _randn(gen, c)).to(dtype)
+    dr = _randn(gen, n, c).to(dtype)
+    want_dx, want_dw, size, dw_size = ref.rmsnorm_bwd(dy, h, w, 1e-5, dr)
+    dx, dw = pe.pe_rmsnorm_bwd(dy, h, w, 1e-5, dresidual=dr)
+    _close(dx, want_dx, (2.5 * ref.norm_depth(c) + 24) * ref.U, dtype, "dx", size)
+    rel = (n / 152 + 1 + 24 + ref.norm_depth(c) / 2 + 10) * ref.U     # as above
+    _close(dw, want_dw, rel, FP32, "dweight", dw_size)
+    few, _ = pe.pe_rmsnorm_bwd(dy[:3], h[:3], w, 1e-5, dresidual=dr[:3])
+    assert torch.equal(few, dx[:3])
+    over, dw_over = pe.pe_rmsnorm_bwd(dy, h, w, 1e-5, dresidual=dr, out=dy)       # dx over dy
+    assert torch.equal(over, dx) and torch.equal(dw_over, dw)
 
 
 def test_rmsnorm_bwd_against_differences():
