@@ -150,6 +150,7 @@ def _check(call: str, status: int):
 # The handle of a device's current stream without a Stream object around it
 # (2 us a call on the GPU's host); the public way where torch lacks it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(device: torch.device) -> int:
@@ -566,7 +567,7 @@ def _fp8_code(dtype: torch.dtype) -> int:
 def _call(name: str, device: torch.device, *args) -> None:
     """Runs one entry point on `device` and its current stream."""
     fn = getattr(_lib or load_library(), name)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         status = fn(*args, _stream(device))
     else:
         with torch.cuda.device(device):
@@ -578,12 +579,13 @@ def _call(name: str, device: torch.device, *args) -> None:
 def _input(t: torch.Tensor, name: str, like: torch.Tensor | None = None,
            shape=None) -> torch.Tensor:
     """A contiguous CUDA tensor on the device and in the dtype of `like`."""
-    t = _cuda(t, name)
-    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _output(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Tensor:
@@ -610,8 +612,9 @@ def _round16(n: int) -> int:
 def _fp8_rows_ok(t: torch.Tensor) -> bool:
     """Rows of adjacent bytes that start at multiples of 16."""
     rows, cols = t.shape
-    return (t.data_ptr() % 16 == 0 and (cols <= 1 or t.stride(1) == 1)
-            and (rows <= 1 or (t.stride(0) % 16 == 0 and t.stride(0) >= cols)))
+    ld, step = t.stride()
+    return (t.data_ptr() % 16 == 0 and (cols <= 1 or step == 1)
+            and (rows <= 1 or (ld % 16 == 0 and ld >= cols)))
 
 
 def _fp8_ld(t: torch.Tensor) -> int:
@@ -620,9 +623,7 @@ def _fp8_ld(t: torch.Tensor) -> int:
 
 def _fp8_empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
     """An 8-bit matrix whose rows start at multiples of 16 bytes."""
-    ld = _round16(cols)
-    t = torch.empty((rows, ld), dtype=dtype, device=device)
-    return t if ld == cols else t[:, :cols]
+    return torch.empty_strided((rows, cols), (_round16(cols), 1), dtype=dtype, device=device)
 
 
 def _fp8_output(t: torch.Tensor | None, name: str, rows: int, cols: int, dtype, device):
@@ -675,8 +676,8 @@ def pe_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
                    y=None, residual_out=None):
     """RMSNorm with an 8-bit output: returns (q [N, C], scales fp32
     [ceil(C / 128), N]), and also h = x + residual with a residual. q's rows
-    start at multiples of 16 bytes (a view of a wider matrix when C is not a
-    multiple of 16). With `y` (a tensor like x) the norm is also written there
+    start at multiples of 16 bytes (its stride is C rounded up to a multiple of
+    16). With `y` (a tensor like x) the norm is also written there
     in x's dtype."""
     x, weight, residual = _norm_inputs(x, weight, residual)
     n, c = x.shape
