@@ -323,17 +323,24 @@ __device__ __forceinline__ void store_quarter(const Params& p, const CUtensorMap
                    "f"(x[4 * g]), "f"(x[4 * g + 1]), "f"(x[4 * g + 2]), "f"(x[4 * g + 3])
                    : "memory");
     __syncwarp();
-    const int32_t rows = p.m - row0 < 32 ? p.m - row0 : 32;
     const int32_t col = col0 + q * 32 + lane;
-    if (col < p.n) {
-      for (int32_t r = 0; r < rows; ++r) {
-        const float v =
-            load_shared(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-        const int64_t at = (int64_t)(row0 + r) * p.n + col;
-        if (p.out_fp32)
-          static_cast<float*>(p.out)[at] = v;
-        else
-          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+    const int32_t rows = col >= p.n ? 0 : p.m - row0;
+    int64_t at = (int64_t)row0 * p.n + col;
+#pragma unroll
+    for (int32_t r0 = 0; r0 < 32; r0 += 8, at += 8 * (int64_t)p.n) {   // eight reads in flight
+      float v[8];
+#pragma unroll
+      for (int32_t r = 0; r < 8; ++r)
+        v[r] = load_shared(stage + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4);
+      if (p.out_fp32) {
+#pragma unroll
+        for (int32_t r = 0; r < 8; ++r)
+          if (r0 + r < rows) static_cast<float*>(p.out)[at + r * (int64_t)p.n] = v[r];
+      } else {
+#pragma unroll
+        for (int32_t r = 0; r < 8; ++r)
+          if (r0 + r < rows)
+            static_cast<__nv_bfloat16*>(p.out)[at + r * (int64_t)p.n] = __float2bfloat16_rn(v[r]);
       }
     }
   }
