@@ -10,7 +10,7 @@
 // transposed bytes are packed along a lane's 16 rows and exchanged through
 // shared memory so that every output row is written in runs of 128 bytes.
 // Measured (GB300, device time): 32299 x 2304 bf16 to e5m2 both ways in 52.6 us
-// (5.7 TB/s, 0.84 of the measured copy rate); a weight of 2304 x 768 in 2.9 us.
+// (5.7 TB/s, 0.85 of the measured copy rate); a weight of 2304 x 768 in 2.8 us.
 #include "pe_fp8.cuh"
 
 namespace pe {
@@ -51,6 +51,20 @@ struct Four<__nv_bfloat16> {
     w |= static_cast<uint32_t>(__bfloat16_as_ushort(x)) << (j & 1 ? 16 : 0);
   }
   __device__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+  // The first `valid` of the four elements at p, which starts anywhere: the two
+  // aligned 8-byte words around them, shifted together. They reach up to 3 elements
+  // before p and 8 from p on.
+  __device__ void load_anywhere(const __nv_bfloat16* p, int valid) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint2* word = reinterpret_cast<const uint2*>(at & ~(uintptr_t)7);
+    const uint2 a = __ldg(word), b = __ldg(word + 1);
+    const bool far = at & 4;                       // the same for a whole row
+    const uint32_t bits = (uint32_t)(at & 2) * 8;
+    v.x = __funnelshift_r(far ? a.y : a.x, far ? b.x : a.y, bits);
+    v.y = __funnelshift_r(far ? b.x : a.y, far ? b.y : b.x, bits);
+    if (valid < 4) v.y &= valid == 3 ? 0xffffu : 0u;
+    if (valid < 2) v.x &= 0xffffu;
+  }
 };
 template <>
 struct Four<float> {
@@ -118,8 +132,9 @@ __device__ __forceinline__ float max_of_rows(float (&v)[kRowsPerWarp], int lane)
   return max_nan(v[0], __shfl_xor_sync(kFull, v[0], 1));
 }
 
-// kVec: a lane's 4 columns are adjacent (rows of x start at multiples of 4
-// elements); otherwise they are 32 apart and move one element at a time.
+// kVec: rows of x start at multiples of 4 elements. A lane's 4 columns are adjacent,
+// but in fp32 without kVec, where they are 32 apart and move one element at a time
+// (bf16 in that way: 32299 x 777 both ways 46 us, 34 as it is; 2303 columns 100 and 73).
 // kWhole: the tile lies inside the matrix.
 template <typename T, bool kVec, bool kE5M2, bool kSquare, bool kWhole>
 __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt, int64_t ct,
@@ -129,19 +144,38 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
   const int row_count = kWhole ? kTile : (int)(a.rows - r0 < kTile ? a.rows - r0 : kTile);
   const int col_count = kWhole ? kTile : (int)(a.cols - c0 < kTile ? a.cols - c0 : kTile);
   const int wr = warp * kRowsPerWarp;              // this warp's first row in the tile
-  auto col = [&](int j) { return kVec ? lane * 4 + j : j * 32 + lane; };
+  constexpr bool kNear = kVec || sizeof(T) == 2;
+  auto col = [&](int j) { return kNear ? lane * 4 + j : j * 32 + lane; };
 
   Four<T> x[kRowsPerWarp];
   const T* src = static_cast<const T*>(a.x) + (r0 + wr) * a.cols + c0 + col(0);
+  // bf16 rows that start anywhere: whether the words around this warp's elements lie
+  // inside x (they do but for the matrix's first and last ones).
+  bool words = false;
+  if constexpr (kNear && !kVec) {
+    const T* begin = static_cast<const T*>(a.x);
+    const T* first = begin + (r0 + wr) * a.cols + c0;
+    const T* last = first + (row_count - wr - 1) * a.cols + col_count;
+    words = first - begin >= 4 && begin + a.rows * a.cols - last >= 8;
+  }
+  if (words) {
+    if constexpr (kNear && !kVec) {
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i, src += a.cols) {
-    if (kWhole || wr + i < row_count) {
-      if constexpr (kVec) {
-        if (kWhole || col(0) < col_count) x[i].load(src);   // cols is a multiple of 4
-      } else {
+      for (int i = 0; i < kRowsPerWarp; ++i, src += a.cols)
+        if ((kWhole || wr + i < row_count) && (kWhole || col(0) < col_count))
+          x[i].load_anywhere(src, kWhole ? 4 : col_count - col(0));
+    }
+  } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (kWhole || col(j) < col_count) x[i].set(j, src[32 * j]);
+    for (int i = 0; i < kRowsPerWarp; ++i, src += a.cols) {
+      if (kWhole || wr + i < row_count) {
+        if constexpr (kVec) {
+          if (kWhole || col(0) < col_count) x[i].load(src);   // cols is a multiple of 4
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (kWhole || col(j) < col_count) x[i].set(j, src[kNear ? j : 32 * j]);
+        }
       }
     }
   }
@@ -173,7 +207,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
     tile_scale = fp8_scale<kE5M2>(m, tile_factor);
   } else if (a.yt) {
     const float4 m = over_rows.get();
-    if constexpr (kVec) {
+    if constexpr (kNear) {
       *reinterpret_cast<float4*>(&colmax[warp][lane * 4]) = m;
     } else {
       colmax[warp][col(0)] = m.x;
@@ -200,12 +234,12 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
       const uint32_t q = fp8x4<kE5M2>(x[i].get(0) * f, x[i].get(1) * f, x[i].get(2) * f,
                                       x[i].get(3) * f);
       if (kWhole || wr + i < row_count) {
-        if constexpr (kVec) {
-          if (kWhole || col(0) < col_count) *reinterpret_cast<uint32_t*>(dst) = q;
-        } else {
+        if (kNear && (kWhole || col(3) < col_count)) {
+          *reinterpret_cast<uint32_t*>(dst) = q;
+        } else if (!kVec) {                          // cols is a multiple of 4 with kVec
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (kWhole || col(j) < col_count) dst[32 * j] = (uint8_t)(q >> (8 * j));
+            if (kWhole || col(j) < col_count) dst[kNear ? j : 32 * j] = (uint8_t)(q >> (8 * j));
         }
       }
     }
@@ -219,7 +253,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
       for (int j = 0; j < 4; ++j) cmax[j] = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if constexpr (kVec) {
+        if constexpr (kNear) {
           const float4 m = *reinterpret_cast<const float4*>(&colmax[w][lane * 4]);
           cmax[0] = max_nan(cmax[0], m.x);
           cmax[1] = max_nan(cmax[1], m.y);
@@ -244,7 +278,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
       for (int i = 0; i < 4; ++i)
         q[i] = fp8x4<kE5M2>(x[4 * i].get(j) * f, x[4 * i + 1].get(j) * f, x[4 * i + 2].get(j) * f,
                             x[4 * i + 3].get(j) * f);
-      exchange[col(j)][warp ^ ((col(j) >> (kVec ? 2 : 0)) & 7)] =
+      exchange[col(j)][warp ^ ((col(j) >> (kNear ? 2 : 0)) & 7)] =
           make_uint4(q[0], q[1], q[2], q[3]);
     }
     __syncthreads();
@@ -256,7 +290,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
     for (int i = 0; i < kTile / 32; ++i, dst += 32 * a.yt_ld) {
       const int c = i * 32 + (threadIdx.x >> 3);
       if (!kWhole && c >= col_count) continue;
-      const uint4 v = exchange[c][run ^ ((c >> (kVec ? 2 : 0)) & 7)];
+      const uint4 v = exchange[c][run ^ ((c >> (kNear ? 2 : 0)) & 7)];
       if (kWhole || run_rows >= 16) {
         *reinterpret_cast<uint4*>(dst) = v;
       } else {

@@ -290,6 +290,21 @@ def test_quantize(dtype, fp8, block_rows, rows, cols):
         assert torch.equal(got.float(), want.float())
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3, 5])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 130), (129, 3), (140, 256), (257, 253), (300, 390),
+                                       (384, 131)])
+def test_quantize_of_rows_that_start_anywhere(rows, cols, offset, block_rows, dtype):
+    """A matrix at any element of a buffer; what lies around it is not used."""
+    buffer = torch.full((rows * cols + 16,), float("nan"), device=DEV, dtype=dtype)
+    x = buffer[offset:offset + rows * cols].view(rows, cols)
+    x.copy_(_randn(_gen(315), rows, cols) * torch.exp(2 * _randn(_gen(316), cols)))
+    q, s, qt, st = pe.pe_quantize_fp8(x, block_rows, transposed=True)
+    ref.check_quantized(q, s, x.double(), E4M3, block_rows, 0.0, "as it is")
+    ref.check_quantized(qt, st, x.double().t(), E4M3, block_rows, 0.0, "transposed")
+
+
 @pytest.mark.parametrize("rows,cols", [(37, 100), (128, 33), (200, 384)])
 def test_quantize_writes_nothing_outside(rows, cols):
     """The C entry with leading dimensions of its own and guarded buffers."""
