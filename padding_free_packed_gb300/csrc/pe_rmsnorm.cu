@@ -5,16 +5,18 @@
 //             in 8 bits: one scale for each 128 channels of a row.
 //   backward: with n = h rstd, dx = rstd (w dy - n mean(w dy n)) (+ dresidual);
 //             dw = sum over rows of dy n.
-// All are bandwidth kernels: a row is read once, held in registers, and every
-// output written once. Statistics, products and sums are fp32. Rows whose width or
-// address does not allow 16-byte vectors, and very wide rows, take two passes of
-// which the second finds the row in the caches.
+// All are bandwidth kernels: a row is read once, held in the registers of 1 to 8
+// warps, and every output written once. Statistics, products and sums are fp32. Very
+// wide rows take two passes of which the second finds the row in the caches.
 // Measured (GB300, device time): forward with residual and 8-bit output 32299 x 768
-// bf16 in 29.0 us (6.0 TB/s, 0.88 of the measured copy rate), 90487 x 500 fp32 in
-// 41 us (0.82); backward with the residual's gradient 32299 x 768 bf16 in 39.7 us
-// (5.0 TB/s, 0.74; 2 to 3 us of it the second kernel). The backward holds 24 weight sums a
-// thread, so two blocks of 256 threads fit an SM (three spill: 41.5 us), and waits
-// for memory; rows through a shared-memory ring did not help (46.5 us).
+// bf16 in 28.5 us (6.1 TB/s, 0.90 of the measured copy rate), 90487 x 500 fp32 in
+// 41 us (0.82), one row of 768 in 1.6; backward with the residual's gradient 32299 x
+// 768 bf16 in 39.3 us (5.05 TB/s, 0.74; 2 to 3 us of it the second kernel). The
+// backward waits for memory: 64 threads a row with 16 weight sums each, three blocks of
+// 256 threads an SM; rows through a shared-memory ring did not help (46.5 us). bf16 rows
+// of odd width move two bytes at a time, 0.4 to 0.55 of the copy rate (32299 x 777 in 69
+// us, backward 58); reading them by aligned 8-byte words shifted together, with the sum
+// written two bytes at a time, took 81.
 #include <math.h>
 
 #include "pe_fp8.cuh"
