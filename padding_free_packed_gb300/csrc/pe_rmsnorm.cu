@@ -434,8 +434,9 @@ void launch_row(const FwdArgs<T>& a, cudaStream_t stream) {
 }
 
 // The form for V neighbouring channels per access: warps a row, vectors a lane and
-// blocks an SM, by the row's width. Few rows (two an SM) take a block each: 300 x 768
-// bf16 in 2.5 us (a warp each 3.2), 300 x 2001 in 4.4 (two passes 35).
+// blocks an SM, by the row's width. Few rows (up to four an SM) take a block each, in us
+// (otherwise): bf16 76 x 768 2.0 (2.8), 608 x 768 2.6 (2.8), 1216 x 768 3.8 (2.9), 304 x
+// 333 2.8 (4.7), 608 x 1501 4.4 (5.1), 1216 x 1501 7.5 (5.6); fp32 608 x 2304 3.6 (4.3).
 // Many rows keep 16 to 20 channels a lane: with more the registers leave too few
 // rows in flight, with fewer the barrier shows. bf16, residual, 8-bit output:
 //   90487 x 500  V 4: 1 warp 53 us, 2 warps 65;      V 1: 1 warp 86, 2 warps 100
@@ -446,7 +447,7 @@ void launch_row(const FwdArgs<T>& a, cudaStream_t stream) {
 template <typename T, int V, int kMode>
 void launch_rows(const FwdArgs<T>& a, cudaStream_t stream) {
   const int32_t C = a.C;
-  const bool few = a.N <= 2 * (int64_t)device_sm_count() && C > 256;
+  const bool few = a.N <= 4 * (int64_t)device_sm_count() && C > 256;
   if constexpr (V == 8) {
     if (C > 2048 && C <= 2560) return launch_rows<T, 4, kMode>(a, stream);
     if (few && C <= 2048) return launch_row<T, V, 1, 8, 6, kMode>(a, stream);
