@@ -589,6 +589,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                                           s.guard.abort);
   __syncthreads();
   cluster_sync();
+  // The issuing warps' last commits arrive in both CTAs: the second stays until they,
+  // and so every arrival before them, have reached its barriers.
+  if (rank == 1 && threadIdx.x == 0)
+    for (int i = 0; i < kIssueWarps; ++i) mbar_drain_wait(smem_u32(&s.drain[i]), 0);
   if (rank == 0 && threadIdx.x == 0 && (s.aborted[0] || s.aborted[1])) {
     // Both producers have stopped. Blocks that only one CTA loaded are put right
     // on their barrier, then every load that may be in flight is waited for.

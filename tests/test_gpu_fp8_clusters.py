@@ -22,3 +22,16 @@ def test_split_sums_with_a_ragged_last_column_tile(m, n):
     for _ in range(20):
         assert torch.equal(pe.pe_matmul_fp8(a, sa, b, sb, dtype=FP32).double(), want)
     assert pe.pe_read_matmul_status() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(9000, 1152, 128), (40000, 256, 130), (2304, 768, 20000)])
+def test_many_launches_of_pairs_in_a_row(m, n, k):
+    """Each launch reuses the shared memory that the one before signalled into."""
+    a, sa, b, sb = _operands(_gen(542), m, n, k, ints=True)
+    want, _ = ref.matmul(a, sa, b, sb)
+    outs = [torch.empty(m, n, dtype=FP32, device=a.device) for _ in range(4)]
+    for i in range(200):
+        pe.pe_matmul_fp8(a, sa, b, sb, out=outs[i % 4])
+    for out in outs:
+        assert torch.equal(out.double(), want)
+    assert pe.pe_read_matmul_status() == 0
