@@ -401,9 +401,10 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  *     A = max(amax, 2^-117) for e4m3, max(amax, 2^-110) for e5m2,
  *     scale = A / F, value = x * (F / A) rounded to the nearest 8-bit number,
  *     ties to even,
- * with the two quotients in fp32, scale within 2 and F / A within 3 roundings.
- * The floor keeps both normal fp32 numbers; an all-zero block holds zeros. A NaN in a block makes the whole block NaN; an infinity makes
- * its scale infinite, so the whole block stands for NaN.
+ * the two quotients and the product each the nearest fp32 number. The floor
+ * keeps both quotients normal fp32 numbers; an all-zero block holds zeros. A NaN
+ * in a block makes the whole block NaN; an infinity makes its scale infinite, so
+ * the whole block stands for NaN.
  * ------------------------------------------------------------------------ */
 
 /* RMSNorm of num_tokens rows of `channels`: with h = x, or h = x + residual

@@ -39,20 +39,30 @@ __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
   return fp8x2<kE5M2>(a, b) | (fp8x2<kE5M2>(c, d) << 16);
 }
 
-// The scale of a block with largest magnitude amax, and the factor that takes
-// its elements to the 8-bit range. Two correctly rounded divisions for each block
-// were a third of the quantisation kernel's instructions; the product with 1 / F
-// is within 2 roundings of the quotient (1 / F is off by 0.75 of one), the
-// reciprocal within one ulp, so the factor is within 3. The power of two keeps
-// the reciprocal of the largest magnitudes out of the subnormal range.
+// A block with largest magnitude amax: the magnitude it is quantised with, the factor
+// that takes its elements to the 8-bit range, and its scale. Both quotients are the
+// nearest fp32 numbers: the rounded 1 / F alone would put the same bias of up to 0.75
+// of a rounding on every scale, an approximate reciprocal two roundings more on every
+// factor. Measured: 32299 x 768 normalised 28.6 us against 28.5 with both of these, 90487
+// x 500 fp32 41.8 against 41.1, 32299 x 2304 quantised both ways 53.4 against 52.6.
 template <bool kE5M2>
-__device__ __forceinline__ float fp8_scale(float amax, float& factor) {
-  constexpr float kLargest = fp8_largest(kE5M2), kDown = 0x1p-9f;
-  const float a = max_nan(amax, fp8_smallest_amax(kE5M2));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * kDown));
-  factor = r * (kLargest * kDown);
-  return a * (1.f / kLargest);
+__device__ __forceinline__ float fp8_block(float amax) {
+  return max_nan(amax, fp8_smallest_amax(kE5M2));
+}
+template <bool kE5M2>
+__device__ __forceinline__ float fp8_factor(float block) {
+  return __fdiv_rn(fp8_largest(kE5M2), block);
+}
+// A known divisor: the product with its rounded reciprocal, corrected once by the exact
+// remainder, is the rounded quotient (Brisebarre, Muller and Raina, "Accelerating
+// correctly rounded floating-point division when the divisor is known in advance",
+// 2004; compared with division for all 2^23 significands). An infinity stays one.
+template <bool kE5M2>
+__device__ __forceinline__ float fp8_scale(float block) {
+  constexpr float kLargest = fp8_largest(kE5M2), kInverse = 1.f / kLargest;
+  const float q = block * kInverse;
+  const float rest = fmaf(-kLargest, q, block);
+  return isinf(block) ? block : fmaf(rest, kInverse, q);
 }
 
 inline bool fp8_type_ok(pe_fp8_type t) { return t == PE_E4M3 || t == PE_E5M2; }

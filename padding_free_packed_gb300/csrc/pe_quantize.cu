@@ -204,7 +204,9 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) m = max_nan(m, colmax[0][w]);
-    tile_scale = fp8_scale<kE5M2>(m, tile_factor);
+    const float block = fp8_block<kE5M2>(m);
+    tile_factor = fp8_factor<kE5M2>(block);
+    tile_scale = fp8_scale<kE5M2>(block);
   } else if (a.yt) {
     const float4 m = over_rows.get();
     if constexpr (kNear) {
@@ -223,9 +225,11 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
     if constexpr (kSquare) {
       if (threadIdx.x == 0) a.scales[ct * ((a.rows + kTile - 1) / kTile) + rt] = tile_scale;
     } else {
-      const float scale = fp8_scale<kE5M2>(max_of_rows(row_max, lane), factor);
+      const float block = fp8_block<kE5M2>(max_of_rows(row_max, lane));
+      factor = fp8_factor<kE5M2>(block);
       const int r = wr + (lane >> 1);
-      if (!(lane & 1) && (kWhole || r < row_count)) a.scales[ct * a.rows + r0 + r] = scale;
+      if (!(lane & 1) && (kWhole || r < row_count))
+        a.scales[ct * a.rows + r0 + r] = fp8_scale<kE5M2>(block);
     }
     uint8_t* dst = a.y + (r0 + wr) * a.y_ld + c0 + col(0);
 #pragma unroll
@@ -269,9 +273,10 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& a, int64_t rt,
     for (int j = 0; j < 4; ++j) {
       float f = tile_factor;
       if constexpr (!kSquare) {
-        const float scale = fp8_scale<kE5M2>(cmax[j], f);
+        const float block = fp8_block<kE5M2>(cmax[j]);
+        f = fp8_factor<kE5M2>(block);
         if (warp == 0 && (kWhole || col(j) < col_count))
-          a.scales_t[rt * a.cols + c0 + col(j)] = scale;
+          a.scales_t[rt * a.cols + c0 + col(j)] = fp8_scale<kE5M2>(block);
       }
       uint32_t q[4];
 #pragma unroll

@@ -199,11 +199,11 @@ __device__ __forceinline__ void emit(const FwdArgs<T>& a, int64_t t, int32_t ste
 #pragma unroll
     for (int off = lanes / 2; off > 0; off >>= 1)
       amax = max_nan(amax, __shfl_xor_sync(kFull, amax, off));
-    float factor;
-    const float scale = fp8_scale<e5>(amax, factor);
+    const float block = fp8_block<e5>(amax);
+    const float factor = fp8_factor<e5>(block);
     const int32_t c0 = channel<V, U>(step, 0, lane);
     if (lane % lanes == 0 && c0 < a.C)
-      a.scales[(int64_t)(c0 / kFp8Block) * a.N + t] = scale;
+      a.scales[(int64_t)(c0 / kFp8Block) * a.N + t] = fp8_scale<e5>(block);
     uint8_t* row = a.y8 + t * a.y8_ld;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -346,9 +346,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rmsnorm_row_kernel(const Fw
       // One lane computes one block's scale; the factors go back by shuffles.
       constexpr bool e5 = kMode == kE5M2;
       constexpr int lanes = kFp8Block / (V * U);
-      const float mine = max_of_blocks<kIter, lanes>(amax, lane);
-      float factor;
-      const float scale = fp8_scale<e5>(mine, factor);
+      const float mine = fp8_block<e5>(max_of_blocks<kIter, lanes>(amax, lane));
+      const float factor = fp8_factor<e5>(mine), scale = fp8_scale<e5>(mine);
       uint8_t* row = a.y8 + t * a.y8_ld;
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
