@@ -96,6 +96,31 @@ __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
+// The product of a block's two scales may leave the range of normal fp32 numbers although
+// the block's part of the result does not (quantisation makes scales from 2^-126 up); it
+// is then added in two steps. Whether a scale is one of which that can happen: neither
+// zero nor from 2^-62 to 2^63.
+__device__ __forceinline__ bool scale_is_far(float x) {
+  const uint32_t twice = __float_as_uint(x) << 1;       // without the sign
+  return twice != 0 && twice - ((127u - 62u) << 24) >= (126u << 24);
+}
+// Factors x and y so that sum + (d x) y, the second step a fused multiply-add, is the sum
+// with d a b: 1 and a b where a b is a normal number (the same bits as sum + d (a b)), or
+// zero, infinite or NaN because a or b is; else y is a power of two that keeps d x in
+// range. d, the block's sum of products, is zero or from 2^-32 to 2^39: with a b below
+// 2^-126, x y = a b 2^64 2^-64; with a b above 2^128, a b 2^-96 2^96, where x is cut off
+// at the largest number, beyond which only d = 0 has a finite result.
+__device__ __forceinline__ float2 far_factors(float a, float b) {
+  constexpr float kLargest = 3.402823466e38f, kSmallest = 0x1p-126f;
+  const float s = fabsf(a * b);
+  if ((s >= kSmallest && s <= kLargest) || a == 0.f || b == 0.f || !(fabsf(a) <= kLargest) ||
+      !(fabsf(b) <= kLargest))
+    return make_float2(1.f, a * b);
+  if (s < 1.f) return make_float2(a * 0x1p64f * b, 0x1p-64f);
+  const float x = (a * 0x1p-48f) * (b * 0x1p-48f);
+  return make_float2(fminf(fmaxf(x, -kLargest), kLargest), 0x1p96f);
+}
+
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator, both operands K-major.
 constexpr uint32_t idesc_fp8(int M, int N, bool a_e5m2, bool b_e5m2) {
   return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) |

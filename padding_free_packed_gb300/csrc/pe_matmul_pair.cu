@@ -201,30 +201,41 @@ __device__ __forceinline__ int32_t pair_blocks(const Params& p, int32_t pair, in
   OP(q, h, 14) OP(q, h, 15) OP(q, h, 16) OP(q, h, 17) OP(q, h, 18) OP(q, h, 19) OP(q, h, 20) \
   OP(q, h, 21) OP(q, h, 22) OP(q, h, 23) OP(q, h, 24) OP(q, h, 25) OP(q, h, 26)              \
   OP(q, h, 27) OP(q, h, 28) OP(q, h, 29) OP(q, h, 30) OP(q, h, 31)
-#define PE_FMA(q, h, i) "fma.rn.f32 pe_s" #q "_" #i ", pe_d" #h "_" #i ", %0, pe_s" #q "_" #i ";\n\t"
+#define PE_FMA(q, h, i) "fma.rn.f32 pe_s" #q "_" #i ", pe_d" #h "_" #i ", f, pe_s" #q "_" #i ";\n\t"
 #define PE_D8(h, a, b, c, d, e, f, g, i)                                                    \
   "pe_d" #h "_" #a ", pe_d" #h "_" #b ", pe_d" #h "_" #c ", pe_d" #h "_" #d ", pe_d" #h "_" #e \
   ", pe_d" #h "_" #f ", pe_d" #h "_" #g ", pe_d" #h "_" #i
 // 32 columns of this thread's lane, from column `off` on, into group h.
 #define PE_LOAD(h, off)                                                                   \
-  "add.u32 a, %1, " #off ";\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(            \
+  "add.u32 a, %2, " #off ";\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {" PE_D8(            \
       h, 0, 1, 2, 3, 4, 5, 6, 7) ", " PE_D8(h, 8, 9, 10, 11, 12, 13, 14, 15) ", " PE_D8(    \
       h, 16, 17, 18, 19, 20, 21, 22, 23) ", " PE_D8(h, 24, 25, 26, 27, 28, 29, 30, 31)      \
       "}, [a];\n\t"
 #define PE_WAIT_LOADS "tcgen05.wait::ld.sync.aligned;\n\t"
 // One block of k: the 128 columns at tensor-memory address `src`, scaled, added to
 // the sums. The accumulator is handed back as soon as it has been read, by the lane
-// with `first` set, on the barrier `back` of the pair's first CTA.
-__device__ __forceinline__ void add_block(float scale, uint32_t src, uint32_t back,
-                                          uint32_t first) {
-  asm volatile("{\n\t.reg .b32 a;\n\t.reg .pred q;\n\t" PE_LOAD(0, 0) PE_LOAD(1, 32)
+// with `first` set, on the barrier `back` of the pair's first CTA. Where the scale of
+// some lane is not a normal number (the two scales' product may have left the range of
+// fp32), such lanes add nothing, the accumulator is kept, and the return value asks for
+// add_far (zero and infinite scales come that way too). Looked at while the loads are
+// in flight, which costs nothing: 169151 x 1024 x 1024 153 us with and without.
+__device__ __forceinline__ uint32_t add_block(float scale, uint32_t src, uint32_t back,
+                                              uint32_t first) {
+  uint32_t far;
+  asm volatile("{\n\t.reg .b32 a;\n\t.reg .f32 f;\n\t.reg .pred p, q;\n\t"
+                   PE_LOAD(0, 0) PE_LOAD(1, 32)
+               "abs.f32 f, %1;\n\tsetp.lt.f32 p, f, 0f00800000;\n\t"
+               "setp.gt.or.f32 p, f, 0f7F7FFFFF, p;\n\tselp.f32 f, 0f00000000, %1, p;\n\t"
+               "vote.sync.any.pred p, p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t"
                    PE_WAIT_LOADS PE_EACH32(PE_FMA, 0, 0) PE_LOAD(0, 64) PE_EACH32(PE_FMA, 1, 1)
                        PE_LOAD(1, 96) PE_WAIT_LOADS
                "tcgen05.fence::before_thread_sync;\n\tbar.warp.sync 0xffffffff;\n\t"
-               "setp.ne.b32 q, %3, 0;\n\t@q mbarrier.arrive.shared::cluster.b64 _, [%2];\n\t"
-               PE_EACH32(PE_FMA, 2, 0) PE_EACH32(PE_FMA, 3, 1) "}" ::"f"(scale),
+               "setp.ne.and.b32 q, %4, 0, !p;\n\t"
+               "@q mbarrier.arrive.shared::cluster.b64 _, [%3];\n\t"
+               PE_EACH32(PE_FMA, 2, 0) PE_EACH32(PE_FMA, 3, 1) "}" : "=r"(far) : "f"(scale),
                "r"(src), "r"(back), "r"(first)
                : "memory");
+  return far;
 }
 #define PE_ZERO(q, h, i) "mov.b32 pe_s" #q "_" #i ", 0;\n\t"
 __device__ __forceinline__ void clear_sums() {
@@ -262,6 +273,35 @@ __device__ __forceinline__ float load_shared(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The lanes that add_block left out: their products with the factors of far_factors (the
+// other lanes': zeros) are summed in memory, so that this rare path leaves the registers
+// of the block loop alone (as a second form of add_block it made that loop a tenth slower).
+__device__ __forceinline__ void add_far(float (&far)[kRows], bool begun, float2 f, uint32_t src) {
+#pragma unroll 1
+  for (int c = 0; c < kRows; c += 8) {
+    uint32_t d[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]),
+          "=r"(d[7])
+        : "r"(src + c)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      far[c + i] = fmaf(__uint_as_float(d[i]) * f.x, f.y, begun ? far[c + i] : 0.f);
+  }
+}
+
+#define PE_ADD(q, h, i)                                                                     \
+  asm volatile("add.rn.f32 pe_s" #q "_" #i ", pe_s" #q "_" #i ", %0;" ::"f"(far[32 * q + i]));
+__device__ __forceinline__ void merge_far(const float (&far)[kRows]) {
+  PE_EACH32(PE_ADD, 0, 0) PE_EACH32(PE_ADD, 1, 0) PE_EACH32(PE_ADD, 2, 0) PE_EACH32(PE_ADD, 3, 0)
 }
 
 // How rows of out are written: bf16 or fp32 boxes by TMA, or, where rows start
@@ -478,15 +518,16 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
       bool more = w.start(p, pair, pairs);
       const float* a_src = nullptr;
       const float* b_src = nullptr;
-      bool a_in[4], b_in = false;
+      uint32_t a_step[4];                  // to this lane's rows 32, 64 and 96 further
       auto locate = [&]() {                // this lane's rows (and columns) in w's tile
+        // Rows and columns outside the matrix take row or column 0's scale: their sums are
+        // zeros (operands outside are) or NaN, and not stored.
         const int32_t rt = w.tile / p.col_tiles, cb = 2 * (w.tile - rt * p.col_tiles) + (lane & 1);
         const int32_t row = rt * kTile + (int32_t)rank * kRows + lane;
         a_src = p.a_scales + (int64_t)w.first * p.m + (row < p.m ? row : 0);
         b_src = p.b_scales + (int64_t)w.first * col_blocks + (cb < col_blocks ? cb : 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a_in[i] = row + 32 * i < p.m;
-        b_in = cb < col_blocks;
+        for (int i = 0; i < 4; ++i) a_step[i] = row + 32 * i < p.m ? 32 * i : 0;
       };
       if (more) locate();
       for (int32_t i = -kScaleAhead; i < blocks; ++i) {
@@ -496,8 +537,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
           const int slot = (i + kScaleAhead) % kScaleSlots;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            copy_async4(&s.a_scale[slot][j * 32 + lane], a_src + (a_in[j] ? 32 * j : 0), a_in[j]);
-          if (lane < 2) copy_async4(&s.b_scale[slot][lane], b_src, b_in);
+            copy_async4(&s.a_scale[slot][j * 32 + lane], a_src + a_step[j], true);
+          if (lane < 2) copy_async4(&s.b_scale[slot][lane], b_src, true);
           a_src += p.m;
           b_src += col_blocks;
           if (++w.first == w.last) {
@@ -544,20 +585,32 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
     if (w.start(p, pair, pairs)) {
       for (bool begins = true;; begins = false) {       // begins: the pair's first segment
         clear_sums();
+        float far[kRows];                               // what add_block leaves out,
+        bool any_far = false;                           // if anything
         for (int32_t block = w.first; block < w.last; ++block) {
           if (!eager_warp_wait(acc_full + buf * 8, parity, guard, p.status, kSiteEpilogue)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const float scale =
-              load_shared(a_scale + slot * (kRows * 4)) * load_shared(b_scale + slot * 8);
-          add_block(scale, lane_base + buf * kTile, acc_empty + buf * 8, first);
+          const float sa = load_shared(a_scale + slot * (kRows * 4));
+          const float sb = load_shared(b_scale + slot * 8);
+          const float scale = sa * sb;
+          if (add_block(scale, lane_base + buf * kTile, acc_empty + buf * 8, first)) {
+            const bool left_out = fabsf(scale) < 0x1p-126f || fabsf(scale) > 3.402823466e38f;
+            add_far(far, any_far, left_out ? far_factors(sa, sb) : make_float2(0.f, 0.f),
+                    lane_base + buf * kTile);
+            any_far = true;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty + buf * 8);
+          }
           slot = (slot + 1) % kScaleSlots;
           parity ^= buf;
           buf ^= 1;
         }
         if (!ok) break;
+        if (any_far) merge_far(far);
         // The segment's sums: a whole tile goes to out, a part to the workspace.
         const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
         const int32_t row0 = rt * kTile + row_in, col0 = ct * kTile + half * 128;

@@ -18,6 +18,11 @@
 //   warps 0-3   scaling and sums
 //   warp 4      TMA producer
 //   warp 5      MMA issue
+//   warp 6      looks for scales that are far: where it finds one, the CTA sums its
+//               blocks again, each in two steps (a test in the loop of warps 0-3 took
+//               768 x 768 x 9001 from 20.6 us to 24 and more, one before it to 22)
+#include <type_traits>
+
 #include "pe_matmul_fp8.cuh"
 
 namespace pe {
@@ -26,7 +31,7 @@ namespace {
 
 using namespace sm103;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kBufs = 4;                  // accumulators in flight
 constexpr int kScaleAhead = 6;            // blocks of k that scales are copied ahead
 constexpr int kScaleSlots = 8;
@@ -171,120 +176,159 @@ matmul_rows_kernel(const __grid_constant__ CUtensorMap tm_a,
   const uint32_t tmem = s.tmem_base;
 
   float sum[kT];
-#pragma unroll
-  for (int c = 0; c < kT; ++c) sum[c] = 0.f;
+  const int32_t col_blocks = (p.n + kFp8Block - 1) / kFp8Block;
 
-  if (warp == 4) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- producer
-      int32_t issued = 0;
-      for (; issued < count; ++issued) {
-        const int stage = issued % S;
-        if (!mbar_wait(smem_u32(&s.empty[stage]), ((issued / S) & 1) ^ 1, guard, p.status,
-                       kSiteProducer))
-          break;
-        const uint32_t bar = smem_u32(&s.full[stage]);
-        mbar_arrive_expect_tx(bar, (128 + kT) * kFp8Block);
-        tma_load_2d(smem_u32(s.in.b[stage]), &tm_b, bar, (lo + issued) * kFp8Block, col0);
-        tma_load_2d(smem_u32(s.in.a[stage]), &tm_a, bar, (lo + issued) * kFp8Block, row0);
-      }
-      // No load is in flight past this (all have been waited for unless a wait gave up).
-      for (int32_t i = issued > S ? issued - S : 0; i < issued; ++i)
-        mbar_drain_wait(smem_u32(&s.full[i % S]), (i / S) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issue
-    for (int32_t i = 0; i < count; ++i) {
-      const int stage = i % S, buf = i % kBufs;
-      if (!warp_wait(smem_u32(&s.full[stage]), (i / S) & 1, guard, p.status, kSiteMma)) break;
-      if (!warp_wait(smem_u32(&s.acc_empty[buf]), ((i / kBufs) & 1) ^ 1, guard, p.status,
-                     kSiteMma))
-        break;
-      tc_fence_after();
-      const uint64_t db = smem_desc_sw128(smem_u32(s.in.b[stage]), 16, 1024);
-      const uint64_t da = smem_desc_sw128(smem_u32(s.in.a[stage]), 16, 1024);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)          // 32 bytes of k each: 2 units of 16 bytes
-        mma_fp8(tmem + buf * kT, db + 2 * k, da + 2 * k, p.idesc, k > 0);
-      tc_commit_warp(smem_u32(&s.acc_full[buf]));
-      tc_commit_warp(smem_u32(&s.empty[stage]));
-    }
-    tc_commit_warp(smem_u32(&s.drain));    // no MMA is in flight past this
-    mbar_drain_wait(smem_u32(&s.drain), 0);
-  } else {
-    // ------------------------------------------------------------ scaling and sums
-    const int32_t col_blocks = (p.n + kFp8Block - 1) / kFp8Block;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    auto copy_scales = [&](int32_t i) {    // of block i, into this warp's ring
-      if (i < count) {
-        float* slot = s.scale[warp][i % kScaleSlots];
-        const float* src = p.a_scales + (int64_t)(lo + i) * p.m + row0;
-#pragma unroll
-        for (int c = 0; c < kT; c += 32) {
-          const int at = c + lane;
-          if (kT >= 32 || at < kT)
-            copy_async4(&slot[at], src + (row0 + at < p.m ? at : 0), row0 + at < p.m);
+  // All blocks of this CTA. `from` counts the blocks of earlier calls, so that barriers go
+  // on in their phases; `far` is whether the blocks are added in two steps. Returns, in
+  // warp 6, whether they have to be.
+  auto add_blocks = [&](int32_t from, auto far) {
+    bool found = false;
+    if (warp == 4) {
+      if (lane == 0) {
+        // ---------------------------------------------------------- producer
+        int32_t issued = from;
+        for (; issued < from + count; ++issued) {
+          const int stage = issued % S;
+          if (!mbar_wait(smem_u32(&s.empty[stage]), ((issued / S) & 1) ^ 1, guard, p.status,
+                         kSiteProducer))
+            break;
+          const uint32_t bar = smem_u32(&s.full[stage]);
+          const int32_t x = (lo + issued - from) * kFp8Block;
+          mbar_arrive_expect_tx(bar, (128 + kT) * kFp8Block);
+          tma_load_2d(smem_u32(s.in.b[stage]), &tm_b, bar, x, col0);
+          tma_load_2d(smem_u32(s.in.a[stage]), &tm_a, bar, x, row0);
         }
-        if (lane == 0)
-          copy_async4(&slot[kT], p.b_scales + (int64_t)(lo + i) * col_blocks + col_tile, true);
+        // No load is in flight past this (all have been waited for unless a wait gave up).
+        for (int32_t i = issued > S ? issued - S : 0; i < issued; ++i)
+          mbar_drain_wait(smem_u32(&s.full[i % S]), (i / S) & 1);
       }
-      copy_async_commit();
-    };
-    for (int32_t i = 0; i < kScaleAhead; ++i) copy_scales(i);
-    for (int32_t i = 0; i < count; ++i) {
-      copy_scales(i + kScaleAhead);        // the slot's block has been read (syncwarp below)
-      copy_async_wait<kScaleAhead>();
       __syncwarp();
-      const float* slot = s.scale[warp][i % kScaleSlots];
-      const float sb = slot[kT];
-      const int buf = i % kBufs;
-      if (!warp_wait(smem_u32(&s.acc_full[buf]), (i / kBufs) & 1, guard, p.status, kSiteEpilogue))
-        break;
-      tc_fence_after();
-      const uint32_t src = lane_base + buf * kT;
-      if constexpr (kT == 16) {
-        uint32_t d[16];
-        tmem_ld16(src, d);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+    } else if (warp == 5) {
+      // ------------------------------------------------------------ MMA issue
+      for (int32_t i = from; i < from + count; ++i) {
+        const int stage = i % S, buf = i % kBufs;
+        if (!warp_wait(smem_u32(&s.full[stage]), (i / S) & 1, guard, p.status, kSiteMma)) break;
+        if (!warp_wait(smem_u32(&s.acc_empty[buf]), ((i / kBufs) & 1) ^ 1, guard, p.status,
+                       kSiteMma))
+          break;
+        tc_fence_after();
+        const uint64_t db = smem_desc_sw128(smem_u32(s.in.b[stage]), 16, 1024);
+        const uint64_t da = smem_desc_sw128(smem_u32(s.in.a[stage]), 16, 1024);
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          const float4 sa = *reinterpret_cast<const float4*>(slot + c);
-          sum[c] = fmaf(sa.x * sb, __uint_as_float(d[c]), sum[c]);
-          sum[c + 1] = fmaf(sa.y * sb, __uint_as_float(d[c + 1]), sum[c + 1]);
-          sum[c + 2] = fmaf(sa.z * sb, __uint_as_float(d[c + 2]), sum[c + 2]);
-          sum[c + 3] = fmaf(sa.w * sb, __uint_as_float(d[c + 3]), sum[c + 3]);
-        }
-      } else {
+        for (int k = 0; k < 4; ++k)          // 32 bytes of k each: 2 units of 16 bytes
+          mma_fp8(tmem + buf * kT, db + 2 * k, da + 2 * k, p.idesc, k > 0);
+        tc_commit_warp(smem_u32(&s.acc_full[buf]));
+        tc_commit_warp(smem_u32(&s.empty[stage]));
+      }
+      tc_commit_warp(smem_u32(&s.drain));    // no MMA is in flight past this
+      mbar_drain_wait(smem_u32(&s.drain), from ? 1 : 0);
+    } else if (warp == 6) {
+      // ------------------------------------------------------------ far scales
+      if constexpr (!decltype(far)::value) {
+        constexpr int kFlight = 8;           // loads; past the end, the last one again
+        for (int32_t e = lane; e < count * kT; e += 32 * kFlight) {
+          float v[kFlight];
 #pragma unroll
-        for (int h = 0; h < kT; h += 32) {
-          uint32_t d[32];
-          tmem_ld32(src + h, d);
-          tmem_wait_ld(d);
-          if (h + 32 == kT) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+          for (int u = 0; u < kFlight; ++u) {
+            const int32_t at = e + 32 * u < count * kT ? e + 32 * u : count * kT - 1;
+            const int32_t row = row0 + at % kT;
+            v[u] = __ldg(p.a_scales + (int64_t)(lo + at / kT) * p.m + (row < p.m ? row : row0));
           }
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 sa = *reinterpret_cast<const float4*>(slot + h + c);
-            sum[h + c] = fmaf(sa.x * sb, __uint_as_float(d[c]), sum[h + c]);
-            sum[h + c + 1] = fmaf(sa.y * sb, __uint_as_float(d[c + 1]), sum[h + c + 1]);
-            sum[h + c + 2] = fmaf(sa.z * sb, __uint_as_float(d[c + 2]), sum[h + c + 2]);
-            sum[h + c + 3] = fmaf(sa.w * sb, __uint_as_float(d[c + 3]), sum[h + c + 3]);
+          for (int u = 0; u < kFlight; ++u) found |= scale_is_far(v[u]);
+        }
+        for (int32_t i = lane; i < count; i += 32)
+          found |= scale_is_far(__ldg(p.b_scales + (int64_t)(lo + i) * col_blocks + col_tile));
+        __syncwarp();
+      }
+    } else {
+      // ------------------------------------------------------------ scaling and sums
+#pragma unroll
+      for (int c = 0; c < kT; ++c) sum[c] = 0.f;
+      const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+      auto copy_scales = [&](int32_t i) {    // of block i, into this warp's ring
+        if (i < count) {
+          float* slot = s.scale[warp][i % kScaleSlots];
+          const float* src = p.a_scales + (int64_t)(lo + i) * p.m + row0;
+#pragma unroll
+          for (int c = 0; c < kT; c += 32) {
+            const int at = c + lane;
+            if (kT >= 32 || at < kT)
+              copy_async4(&slot[at], src + (row0 + at < p.m ? at : 0), row0 + at < p.m);
+          }
+          if (lane == 0)
+            copy_async4(&slot[kT], p.b_scales + (int64_t)(lo + i) * col_blocks + col_tile, true);
+        }
+        copy_async_commit();
+      };
+      // 16 or 32 columns of tensor memory, scaled, to the sums of rows h ...
+      auto add = [&](const auto& d, int h, const float* slot, float sb) {
+        constexpr int kCols = sizeof(d) / sizeof(d[0]);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4) {
+          const float4 sa = *reinterpret_cast<const float4*>(slot + h + c);
+          const float a[4] = {sa.x, sa.y, sa.z, sa.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float& to = sum[h + c + j];
+            const float v = __uint_as_float(d[c + j]);
+            if constexpr (decltype(far)::value) {
+              const float2 f = far_factors(a[j], sb);
+              to = fmaf(v * f.x, f.y, to);
+            } else {
+              to = fmaf(a[j] * sb, v, to);
+            }
+          }
+        }
+      };
+      for (int32_t i = 0; i < kScaleAhead; ++i) copy_scales(i);
+      for (int32_t i = 0; i < count; ++i) {
+        copy_scales(i + kScaleAhead);        // the slot's block has been read (syncwarp below)
+        copy_async_wait<kScaleAhead>();
+        __syncwarp();
+        const float* slot = s.scale[warp][i % kScaleSlots];
+        const float sb = slot[kT];
+        const int buf = (from + i) % kBufs;
+        if (!warp_wait(smem_u32(&s.acc_full[buf]), ((from + i) / kBufs) & 1, guard, p.status,
+                       kSiteEpilogue))
+          break;
+        tc_fence_after();
+        const uint32_t src = lane_base + buf * kT;
+        if constexpr (kT == 16) {
+          uint32_t d[16];
+          tmem_ld16(src, d);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+          add(d, 0, slot, sb);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kT; h += 32) {
+            uint32_t d[32];
+            tmem_ld32(src + h, d);
+            tmem_wait_ld(d);
+            if (h + 32 == kT) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+            }
+            add(d, h, slot, sb);
           }
         }
       }
+      copy_async_wait<0>();
     }
-    copy_async_wait<0>();
+    // Every load and MMA of this CTA is done.
+    tc_fence_before();
+    return __syncthreads_or(found);
+  };
+  if (add_blocks(0, std::false_type())) {
+    const bool gave_up = guard->abort;       // the same in all threads until the barrier
+    __syncthreads();
+    tc_fence_after();
+    if (!gave_up) add_blocks(count, std::true_type());
   }
-
-  // Every load and MMA of this CTA is done: its stages may hold its sums now.
-  tc_fence_before();
-  __syncthreads();
+  // This CTA's stages may hold its sums now.
   if (p.split == 1) {
     const int32_t col = col0 + threadIdx.x;
     if (warp < 4 && col < p.n) {
