@@ -418,6 +418,7 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  * number (with tensors of the same alignment).
  * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
  * finite and > 0, NULL required pointers, residual_out without residual;
+ * PE_ERR_OVERFLOW for 2^31 - 1024 channels or more;
  * PE_ERR_UNSUPPORTED for other dtypes or devices and for an 8-bit output whose
  * address or leading dimension is not as above. */
 pe_status pe_rmsnorm(pe_dtype dtype, const void* x, const void* residual, const void* weight,

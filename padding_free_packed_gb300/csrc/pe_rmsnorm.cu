@@ -751,12 +751,16 @@ pe_status run_bwd(const void* dy, const void* h, const void* w, const void* dres
   return launch_bwd<T, 1>(a, dweight, stream);
 }
 
+// Channels are counted in int32, up to a whole step of a warp (256) past the last one.
+constexpr int32_t kMaxChannels = 0x7fffffff - 1024;
+
 bool dtype_ok(pe_dtype d) { return d == PE_BF16 || d == PE_FP32; }
 
 pe_status check_fwd(pe_dtype dtype, const void* x, const void* residual, const void* weight,
                     int64_t N, int32_t C, float eps, const void* residual_out) {
   if (!dtype_ok(dtype)) return PE_ERR_UNSUPPORTED;
   if (N < 0 || C < 1 || !(eps > 0.f) || !isfinite(eps)) return PE_ERR_INVALID_ARG;
+  if (C > kMaxChannels) return PE_ERR_OVERFLOW;
   if (N > 0 && (!x || !weight || (residual_out && !residual))) return PE_ERR_INVALID_ARG;
   return PE_OK;
 }
