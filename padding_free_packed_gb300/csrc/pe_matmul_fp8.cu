@@ -12,6 +12,14 @@ namespace {
 
 // The kernels hold row, column and k coordinates of whole tiles in int32.
 constexpr int64_t kMaxSize = (1LL << 31) - 1024;
+// They count blocks of 256 x 256 x 128 in int32 too. Sizes up to kMaxSize give up to
+// 2^70 of them, hence the quotient.
+bool sizes_ok(int64_t m, int64_t n, int64_t k) {
+  constexpr int64_t kMaxBlocks = 1LL << 30;
+  if (m >= kMaxSize || n >= kMaxSize || k >= kMaxSize) return false;
+  if (m == 0 || n == 0 || k == 0) return true;
+  return ceil_div(m, 256) * ceil_div(n, 256) <= (kMaxBlocks - 1) / ceil_div(k, kFp8Block);
+}
 
 __device__ DeviceStatus g_matmul_status;
 
@@ -108,7 +116,7 @@ pe_status matmul_map(CUtensorMap* map, CUtensorMapDataType type, int size, const
 using namespace pe;
 
 extern "C" size_t pe_matmul_fp8_workspace_size(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || n <= 0 || k <= 0) return 0;
+  if (m <= 0 || n <= 0 || k <= 0 || !sizes_ok(m, n, k)) return 0;
   return matmul_plan(m, n, k).runs ? matmul_pair_workspace() : 0;
 }
 
@@ -122,7 +130,7 @@ extern "C" pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_
       (out_dtype != PE_BF16 && out_dtype != PE_FP32))
     return PE_ERR_UNSUPPORTED;
   if (m < 0 || n < 0 || k < 0) return PE_ERR_INVALID_ARG;
-  if (m >= kMaxSize || n >= kMaxSize || k >= kMaxSize) return PE_ERR_OVERFLOW;
+  if (!sizes_ok(m, n, k)) return PE_ERR_OVERFLOW;
   if (m == 0 || n == 0) return PE_OK;
   if (!out || (k > 0 && (!a || !b || !a_scales || !b_scales))) return PE_ERR_INVALID_ARG;
   if (k > 0 && (!fp8_layout_ok(a, a_ld, k) || !fp8_layout_ok(b, b_ld, k)))

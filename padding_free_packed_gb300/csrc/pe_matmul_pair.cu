@@ -785,7 +785,6 @@ pe_status matmul_pair(const MatmulFp8& q, bool runs, void* workspace, DeviceStat
   p.blocks = (int32_t)ceil_div(q.k, kFp8Block);
   p.col_tiles = (int32_t)ceil_div(q.n, kTile);
   const int64_t tiles = ceil_div(q.m, kTile) * p.col_tiles;
-  if (tiles * p.blocks >= (1LL << 30)) return PE_ERR_OVERFLOW;
   p.tiles = (int32_t)tiles;
   int32_t pairs = pair_count();
   p.shared_tiles = runs ? 1 : 0;

@@ -3,7 +3,7 @@ addresses here are fake and never read)."""
 
 import pytest
 
-from test_fp8_host import OK, OVERFLOW, UNSUPPORTED, _bwd, _norm, _norm8, lib  # noqa: F401
+from test_fp8_host import OK, OVERFLOW, UNSUPPORTED, _bwd, _mm, _norm, _norm8, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("below", [1, 2, 128, 255, 256, 1024])
@@ -15,3 +15,18 @@ def test_norms_of_nearly_two_to_the_31_channels_are_refused(lib, below):  # noqa
     assert _bwd(lib, c=c) == UNSUPPORTED
     assert _norm(lib, c=c, n=0) == OVERFLOW
     assert _norm(lib, c=1 << 20, n=0) == OK
+
+
+@pytest.mark.parametrize("m,n,k", [((1 << 31) - 1100,) * 3, (1 << 23, 1 << 23, 1 << 7),
+                                   (1 << 30, 1 << 30, 1 << 31 - 4), (1 << 20, 1 << 20, 1 << 20)])
+def test_products_of_too_many_blocks_are_refused(lib, m, n, k):  # noqa: F811
+    """2^30 blocks of 256 x 256 x 128 or more, also where their number passes 2^64."""
+    assert _mm(lib, m=m, n=n, k=k, lda=1 << 32, ldb=1 << 32) == OVERFLOW
+    assert lib.pe_matmul_fp8_workspace_size(m, n, k) == 0
+
+
+def test_workspace_of_sizes_that_no_product_takes(lib):  # noqa: F811
+    for size in (1 << 31, 1 << 40, (1 << 63) - 1):
+        for sizes in ((size, 64, 64), (64, size, 64), (64, 64, size), (size, size, size)):
+            assert lib.pe_matmul_fp8_workspace_size(*sizes) == 0
+    assert lib.pe_matmul_fp8_workspace_size(2304, 768, 32299) > 0
