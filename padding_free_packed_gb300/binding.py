@@ -644,6 +644,16 @@ def _fp8_operand(t: torch.Tensor, name: str) -> torch.Tensor:
     return _fp8_empty(t.shape[0], t.shape[1], t.dtype, t.device).copy_(t)
 
 
+def _workspace_for(t: torch.Tensor | None, need: int, device) -> tuple[torch.Tensor, int]:
+    """The caller's workspace after a check (kernels write there), or a new one, and
+    its bytes."""
+    if t is None:
+        t = _workspace(need, device)
+    elif t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t, t.numel() * t.element_size()
+
+
 def _norm_inputs(x, weight, residual):
     x = _input(x, "x")
     _, c = _two_dims(x, "x")
@@ -712,11 +722,10 @@ def pe_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps:
         dresidual = _input(dresidual, "dresidual", h, h.shape)
     dx = _output(out, "out", h.shape, h.dtype, h.device)
     dweight = torch.empty(c, dtype=torch.float32, device=h.device)
-    if workspace is None:
-        workspace = _workspace(lib.pe_rmsnorm_bwd_workspace_size(c), h.device)
+    ws, ws_bytes = _workspace_for(workspace, lib.pe_rmsnorm_bwd_workspace_size(c), h.device)
     _call("pe_rmsnorm_bwd", h.device, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
           weight.data_ptr(), _ptr(dresidual), n, c, float(eps), dx.data_ptr(),
-          dweight.data_ptr(), workspace.data_ptr(), workspace.numel())
+          dweight.data_ptr(), ws.data_ptr(), ws_bytes)
     return dx, dweight
 
 
@@ -768,12 +777,11 @@ def pe_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
             raise ValueError(f"{name} must be float32 of shape {shape} on {dev}")
     a_scales, b_scales = a_scales.contiguous(), b_scales.contiguous()
     out = _output(out, "out", (m, n), dtype if out is None else out.dtype, dev)
-    if workspace is None:
-        need = lib.pe_matmul_fp8_workspace_size(m, n, k)
-        workspace = _workspace(need, dev) if need else None
+    need = lib.pe_matmul_fp8_workspace_size(m, n, k)
+    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
     _call("pe_matmul_fp8", dev, a_code, a.data_ptr(), _fp8_ld(a), a_scales.data_ptr(), b_code,
           b.data_ptr(), _fp8_ld(b), b_scales.data_ptr(), m, n, k, _dtype_code(out.dtype),
-          out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
+          out.data_ptr(), _ptr(ws), ws_bytes)
     return out
 
 
