@@ -654,12 +654,19 @@ def _workspace_for(t: torch.Tensor | None, need: int, device) -> tuple[torch.Ten
     return t, t.numel() * t.element_size()
 
 
+def _norm_weight(weight, rows, c) -> torch.Tensor:
+    """The weight in the rows' dtype: another one is refused, since a cast here would
+    round it without the caller's knowledge."""
+    if weight.dtype is not rows.dtype:
+        _dtype_code(rows.dtype)
+        raise ValueError(f"weight must be {rows.dtype} like the rows, got {weight.dtype}")
+    return _input(weight, "weight", rows, (c,))
+
+
 def _norm_inputs(x, weight, residual):
     x = _input(x, "x")
     _, c = _two_dims(x, "x")
-    if weight.dtype != x.dtype:
-        weight = weight.to(x.dtype)
-    weight = _input(weight, "weight", x, (c,))
+    weight = _norm_weight(weight, x, c)
     if residual is not None:
         residual = _input(residual, "residual", x, x.shape)
     return x, weight, residual
@@ -668,7 +675,8 @@ def _norm_inputs(x, weight, residual):
 def pe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
                residual: torch.Tensor | None = None, out=None, residual_out=None):
     """RMSNorm over the last dim of x [N, C]; with a residual, of h = x + residual
-    (rounded to x's dtype), returning (y, h). Otherwise returns y."""
+    (rounded to x's dtype), returning (y, h). Otherwise returns y. weight [C] and
+    residual are in x's dtype."""
     x, weight, residual = _norm_inputs(x, weight, residual)
     n, c = x.shape
     y = _output(out, "out", x.shape, x.dtype, x.device)
@@ -687,8 +695,8 @@ def pe_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     """RMSNorm with an 8-bit output: returns (q [N, C], scales fp32
     [ceil(C / 128), N]), and also h = x + residual with a residual. q's rows
     start at multiples of 16 bytes (its stride is C rounded up to a multiple of
-    16). With `y` (a tensor like x) the norm is also written there
-    in x's dtype."""
+    16). With `y` (a tensor like x) the norm is also written there in x's dtype.
+    weight [C] and residual are in x's dtype."""
     x, weight, residual = _norm_inputs(x, weight, residual)
     n, c = x.shape
     code = _fp8_code(dtype)
@@ -709,15 +717,14 @@ def pe_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
 def pe_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
                    dresidual: torch.Tensor | None = None, out=None, workspace=None):
     """RMSNorm backward for the stored norm input h [N, C]; dresidual is the
-    gradient that reaches h by other ways. Returns (dx, dweight): dx (of x and of
-    residual alike) in h's dtype, dweight fp32 [C]."""
+    gradient that reaches h by other ways; dy, weight and dresidual are in h's dtype.
+    Returns (dx, dweight): dx (of x and of residual alike) in h's dtype, dweight fp32
+    [C]."""
     lib = load_library()
     h = _input(h, "h")
     n, c = _two_dims(h, "h")
     dy = _input(dy, "dy", h, h.shape)
-    if weight.dtype != h.dtype:
-        weight = weight.to(h.dtype)
-    weight = _input(weight, "weight", h, (c,))
+    weight = _norm_weight(weight, h, c)
     if dresidual is not None:
         dresidual = _input(dresidual, "dresidual", h, h.shape)
     dx = _output(out, "out", h.shape, h.dtype, h.device)
