@@ -47,37 +47,45 @@ std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
 }  // namespace
 
 // Estimated microseconds of every way, from times measured on a GB300 (m x n x k,
-// bf16 out; T: rows of a per CTA, S: split; pair: whole tiles of the pair kernel):
+// bf16 out; T: rows of a per CTA, S: split; pair: whole tiles of the pair kernel, runs:
+// equal runs of blocks):
 //   1 x 2304 x 768     T16 4.4   T32 4.9   T64 5.9   pair 8.9
-//   1 x 1024 x 1024    T16 5.2, S8 4.4               pair 10.0
 //   320 x 2304 x 768   T16 8.9   T32 6.6   T64 6.7   pair 8.8
 //   640 x 2304 x 768   T16 13.0  T32 9.9   T64 8.5   pair 8.8
-//   2500 x 2304 x 768                      T64 20.1  pair 12.6
-//   2304 x 768 x 4097            T32 30.6  T64 24.7  pair 20.4, runs 21.0
-//   768 x 768 x 32299  T64,S4 51.5         pair 113.9, runs 30.2
+//   2500 x 2304 x 768                      T64 20.1  pair 12.6, runs 22.6
+//   768 x 768 x 9001             T64,S2 21.0         pair 34.9, runs 18.7
 //   200 x 200 x 20000  T16,S8 11.8  T32,S8 11.0  T64,S8 13.4
-//   100 x 1000 x 8000  T32,S2 13.9  T32,S4 9.3   T64,S8 10.7
-// A narrow CTA takes kFixed and kBlock for each block of k; CTAs that share an SM
-// slow each other, and the join of a split costs kJoin. Splitting pays once a sum
-// has 8 blocks.
+// A narrow CTA takes kFixed and kBlock for each block of k; CTAs that share an SM slow
+// each other, and the join of a split costs kJoin. Splitting pays from a sum of 7 blocks
+// on, with two blocks or more a CTA (S1 and the best split):
+//   6 blocks  1 x 2304 x 768 4.4, 4.5    64 x 768 x 768 4.8, 5.05   200 x 768 x 768 4.9, 5.2
+//   7 blocks  1 x 1024 x 896 4.9, S3 4.85, S7 4.5
+//   8 blocks  1 x 2304 x 1024 5.2, S4 4.7, S8 5.3    1 x 1024 x 1024 5.2, S4 4.7, S8 4.8
+// Whole tiles take 0.41 for each block of a wave of pairs; runs have no last wave, but
+// parts, a second kernel and worse sharing of the operands in L2:
+//   2304 x 768, 27 tiles   k 4097: whole 20.1, runs 21.7   5000: 22.9, 23.4   6000: 26.0, 24.8
+//                          k 9000: 36, 28.5                32299: 109, 62
+//   2304 x 1152, 45 tiles  k 4096: whole 19.8, runs 26.2   9000: 36.4, 37.5   32299: 118, 102
+//   2304 x 2304, 81 tiles  k 4096: whole 34.5, runs 36.1   6000: 47.5, 44.2   8192: 60.6, 52.1
+//   128 tiles, 64 blocks: whole 61.3, runs 71.5            160, 16: 28.8, 38.2
+//   256 tiles, 128 blocks: 229, 231    400, 40: 112, 123   1024, 64: 404, 449
+// Beyond two tiles a pair runs are never better, and are not asked for.
 MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
   constexpr int64_t kSms = 152, kPairs = kSms / 2;
   const int64_t blocks = ceil_div(k, kFp8Block);
   const int64_t tiles = ceil_div(m, 256) * ceil_div(n, 256);
-  const double whole = 0.5 * (double)ceil_div(tiles, kPairs) * (blocks + 1);
-  const double parts = (double)kPairs / tiles + 1;
-  const double runs =
-      0.5 * (double)(ceil_div(tiles * blocks, kPairs) + ceil_div(tiles, kPairs)) + 8 + 0.5 * parts;
-  MatmulPlan plan = {0, 1, runs < whole};
-  double best = 5 + (runs < whole ? runs : whole);
+  const double whole = 6 + (double)ceil_div(tiles, kPairs) * (0.41 * (double)blocks + 1);
+  const double runs = 15 + 0.045 * (double)tiles + 0.48 * (double)(tiles * blocks) / kPairs;
+  MatmulPlan plan = {0, 1, tiles <= 2 * kPairs && runs < whole};
+  double best = plan.runs ? runs : whole;
   constexpr int32_t kRows[3] = {16, 32, 64};
   constexpr double kFixed[3] = {3.0, 3.4, 3.6}, kBlock[3] = {0.285, 0.30, 0.43},
                    kJoin[3] = {0.8, 0.8, 1.5};
   for (int i = 0; i < 3; ++i) {
     const int64_t ctas = ceil_div(m, kRows[i]) * ceil_div(n, 128);
     if (ctas > 8 * kSms || ceil_div(m, kRows[i]) > 65535) continue;
-    int64_t split = blocks < 8 ? 1 : kSms / ctas;
-    split = split < 1 ? 1 : split > 8 ? 8 : split;
+    int64_t split = kSms / ctas < blocks / 2 ? kSms / ctas : blocks / 2;
+    split = blocks < 7 || split < 1 ? 1 : split > 8 ? 8 : split;
     const double shared = (double)ceil_div(ctas * split, kSms) - 1;
     const double t = kFixed[i] + kBlock[i] * (double)ceil_div(blocks, split) * (1 + 0.6 * shared) +
                      1.2 * shared + (split > 1 ? kJoin[i] : 0);

@@ -30,3 +30,14 @@ def test_workspace_of_sizes_that_no_product_takes(lib):  # noqa: F811
         for sizes in ((size, 64, 64), (64, size, 64), (64, 64, size), (size, size, size)):
             assert lib.pe_matmul_fp8_workspace_size(*sizes) == 0
     assert lib.pe_matmul_fp8_workspace_size(2304, 768, 32299) > 0
+
+
+# Beyond two 256 x 256 tiles for each of the 76 pairs of SMs, whole tiles in turn were
+# faster wherever both ways were measured; only runs need a workspace.
+@pytest.mark.parametrize("m,n,k,runs", [
+    (8192, 8192, 8192, False), (12288, 12288, 8192, False), (5120, 5120, 5120, False),
+    (4096, 4096, 16384, False), (20000, 512, 4096, False), (2304, 2304, 4096, False),
+    (2304, 768, 4097, False), (2304, 1152, 9000, False), (2304, 768, 6000, True),
+    (2304, 768, 32299, True), (2304, 2304, 8192, True), (2500, 999, 9001, True)])
+def test_runs_of_blocks_are_for_few_tiles_with_long_sums(lib, m, n, k, runs):  # noqa: F811
+    assert (lib.pe_matmul_fp8_workspace_size(m, n, k) > 0) == runs

@@ -16,8 +16,8 @@ BF16, FP32 = torch.bfloat16, torch.float32
 # Every kernel form: 16, 32 and 64 rows a CTA, without and with a split sum; pairs on
 # whole tiles with each form of output; pairs that share tiles, even and ragged.
 WAYS = [(5, 300, 500), (3, 512, 4000), (320, 1001, 1140), (300, 130, 20000), (1537, 768, 1152),
-        (768, 768, 9001), (9000, 1152, 768), (9000, 1001, 768), (2304, 768, 20000),
-        (2500, 999, 9001)]
+        (768, 768, 4500), (768, 768, 9001), (9000, 1152, 768), (9000, 1001, 768),
+        (2304, 768, 20000), (2500, 999, 9001)]
 
 
 def _operands(m, n, k, low, high):

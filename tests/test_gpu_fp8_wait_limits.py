@@ -14,8 +14,8 @@ TIMEOUT = 7
 # 16, 32 and 64 rows a CTA without and with a split sum; pairs on whole and on shared
 # tiles.
 WAYS = [(5, 300, 500, BF16), (3, 512, 4000, FP32), (320, 1001, 1140, BF16),
-        (300, 130, 20000, FP32), (1537, 768, 1152, FP32), (768, 768, 9001, BF16),
-        (9000, 1152, 768, BF16), (9000, 1001, 768, FP32), (2304, 768, 20000, FP32),
+        (300, 130, 20000, FP32), (1537, 768, 1152, FP32), (768, 768, 4500, BF16),
+        (768, 768, 9001, BF16), (9000, 1152, 768, BF16), (9000, 1001, 768, FP32), (2304, 768, 20000, FP32),
         (2500, 999, 9001, BF16)]
 
 
