@@ -475,7 +475,7 @@ pe_status pe_quantize_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x, i
  * the same order: the result is bitwise the same in every run on a device. Where
  * the product of a block's two scales would leave the range of normal fp32
  * numbers, the block is added in two steps, so that only the result's own range
- * counts. k = 0 writes zeros. out must not overlap the operands.
+ * counts (an infinite e5m2 operand in such a block gives an infinity or a NaN). k = 0 writes zeros. out must not overlap the operands.
  * workspace: device, 16-byte aligned, >= pe_matmul_fp8_workspace_size(m, n, k)
  * bytes; may be NULL when that is 0. Calls that may run at the same time need
  * one each.

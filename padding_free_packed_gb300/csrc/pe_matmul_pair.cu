@@ -216,9 +216,10 @@ __device__ __forceinline__ int32_t pair_blocks(const Params& p, int32_t pair, in
 // the sums. The accumulator is handed back as soon as it has been read, by the lane
 // with `first` set, on the barrier `back` of the pair's first CTA. Where the scale of
 // some lane is not a normal number (the two scales' product may have left the range of
-// fp32), such lanes add nothing, the accumulator is kept, and the return value asks for
-// add_far (zero and infinite scales come that way too). Looked at while the loads are
-// in flight, which costs nothing: 169151 x 1024 x 1024 153 us with and without.
+// fp32), such lanes add zero times the block, the accumulator is kept, and the return
+// value asks for add_far (zero and infinite scales come that way too). Looked at while
+// the loads are in flight, which costs nothing: 169151 x 1024 x 1024 153 us with and
+// without (171 with multiply-adds that such lanes skip).
 __device__ __forceinline__ uint32_t add_block(float scale, uint32_t src, uint32_t back,
                                               uint32_t first) {
   uint32_t far;
@@ -278,10 +279,11 @@ __device__ __forceinline__ float load_shared(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The lanes that add_block left out: their products with the factors of far_factors (the
-// other lanes': zeros) are summed in memory, so that this rare path leaves the registers
-// of the block loop alone (as a second form of add_block it made that loop a tenth slower).
-__device__ __forceinline__ void add_far(float (&far)[kRows], bool begun, float2 f, uint32_t src) {
+// The lanes that add_block left out: their products with the factors of far_factors are
+// summed in memory, so that this rare path leaves the registers of the block loop alone
+// (as a second form of add_block it made that loop a tenth slower).
+__device__ __forceinline__ void add_far(float (&far)[kRows], bool begun, bool left_out, float2 f,
+                                        uint32_t src) {
 #pragma unroll 1
   for (int c = 0; c < kRows; c += 8) {
     uint32_t d[8];
@@ -293,8 +295,10 @@ __device__ __forceinline__ void add_far(float (&far)[kRows], bool begun, float2 
         : "r"(src + c)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      far[c + i] = fmaf(__uint_as_float(d[i]) * f.x, f.y, begun ? far[c + i] : 0.f);
+    for (int i = 0; i < 8; ++i) {
+      const float before = begun ? far[c + i] : 0.f;
+      far[c + i] = left_out ? fmaf(__uint_as_float(d[i]) * f.x, f.y, before) : before;
+    }
   }
 }
 
@@ -598,8 +602,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
           const float scale = sa * sb;
           if (add_block(scale, lane_base + buf * kTile, acc_empty + buf * 8, first)) {
             const bool left_out = fabsf(scale) < 0x1p-126f || fabsf(scale) > 3.402823466e38f;
-            add_far(far, any_far, left_out ? far_factors(sa, sb) : make_float2(0.f, 0.f),
-                    lane_base + buf * kTile);
+            add_far(far, any_far, left_out, far_factors(sa, sb), lane_base + buf * kTile);
             any_far = true;
             tc_fence_before();
             __syncwarp();

@@ -102,3 +102,20 @@ def test_scales_that_are_not_numbers_and_zeros(m, n, k):
     got = pe.pe_matmul_fp8(a, sa, b, sb, dtype=FP32)
     assert not bool(got[0].isfinite().any()) and bool(got[1].isnan().all())
     assert bool((got[2] == 0).all()) and torch.equal(got[3:], want[3:])
+
+
+@pytest.mark.parametrize("m,n,k", WAYS)
+def test_infinite_operands_next_to_far_scales(m, n, k):
+    """e5m2 has infinities: a row that holds one is infinite as the formula says, whatever
+    the scales of the rows beside it, and no number where its own block's are far."""
+    a, sa, b, sb, _ = _operands(m, n, k, -4, 4)
+    a, sa = a.clone(), sa.clone()
+    a[0, 0], a[1, 0], a[2, k - 1] = float("inf"), float("-inf"), float("inf")
+    sa[0, 1] *= 2.0 ** -126
+    sa[-1, 2] *= 2.0 ** 126
+    for small in (sb * 2.0 ** -14, sb * 2.0 ** 10):
+        got = pe.pe_matmul_fp8(a, sa, b, small, dtype=FP32)
+        want, _ = ref.matmul(a, sa, b, small)
+        assert torch.equal(got[:1].double(), want[:1]) and bool(got[0].isinf().all())
+        assert not bool(got[1:3].isfinite().any())
+        assert bool(got[3:].isfinite().all())
