@@ -410,14 +410,16 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
 /* RMSNorm of num_tokens rows of `channels`: with h = x, or h = x + residual
  * rounded to the I/O dtype (written to residual_out when that is non-NULL),
  *     y = h / sqrt(mean(h^2) + eps) * weight.
- * y and residual_out may be the buffers x or residual themselves.
+ * y and residual_out may be the buffers x or residual themselves, but not one
+ * buffer; otherwise no output may overlap another tensor.
  * pe_rmsnorm writes y in the I/O dtype. pe_rmsnorm_fp8 writes y, unrounded, in
  * 8 bits with 1 x 128 blocks into y8 (leading dimension y8_ld) and y8_scales
  * [ceil(channels / 128)][num_tokens], and, when y is non-NULL, also y in the
  * I/O dtype. A row's result does not depend on the other rows, nor on their
  * number (with tensors of the same alignment).
  * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
- * finite and > 0, NULL required pointers, residual_out without residual;
+ * finite and > 0, NULL required pointers, residual_out without residual or
+ * equal to y;
  * PE_ERR_OVERFLOW for 2^31 - 1024 channels or more;
  * PE_ERR_UNSUPPORTED for other dtypes or devices and for an 8-bit output whose
  * address or leading dimension is not as above. */
@@ -451,7 +453,8 @@ pe_status pe_rmsnorm_bwd(pe_dtype dtype, const void* dy, const void* h, const vo
  * scales (skipped when y is NULL), and its transpose into yt [cols, rows] with
  * scales_t (skipped when yt is NULL); x is read once for both. The transpose
  * is quantised as a matrix of its own: with block_rows 1 its blocks are 128
- * rows of x by one column; with 128 it holds y's values.
+ * rows of x by one column; with 128 it holds y's values. No output may overlap
+ * another tensor.
  * Operands of pe_matmul_fp8 made this way, for Y = X W^T with X [N, K],
  * W [M, K] and a gradient dY [N, M]:
  *     forward          a = X (block_rows 1), b = W (128)
@@ -475,7 +478,8 @@ pe_status pe_quantize_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const void* x, i
  * the same order: the result is bitwise the same in every run on a device. Where
  * the product of a block's two scales would leave the range of normal fp32
  * numbers, the block is added in two steps, so that only the result's own range
- * counts (an infinite e5m2 operand in such a block gives an infinity or a NaN). k = 0 writes zeros. out must not overlap the operands.
+ * counts (an infinite e5m2 operand in such a block gives an infinity or a NaN).
+ * k = 0 writes zeros. out must not overlap the operands.
  * workspace: device, 16-byte aligned, >= pe_matmul_fp8_workspace_size(m, n, k)
  * bytes; may be NULL when that is 0. Calls that may run at the same time need
  * one each.

@@ -757,11 +757,12 @@ constexpr int32_t kMaxChannels = 0x7fffffff - 1024;
 bool dtype_ok(pe_dtype d) { return d == PE_BF16 || d == PE_FP32; }
 
 pe_status check_fwd(pe_dtype dtype, const void* x, const void* residual, const void* weight,
-                    int64_t N, int32_t C, float eps, const void* residual_out) {
+                    int64_t N, int32_t C, float eps, const void* y, const void* residual_out) {
   if (!dtype_ok(dtype)) return PE_ERR_UNSUPPORTED;
   if (N < 0 || C < 1 || !(eps > 0.f) || !isfinite(eps)) return PE_ERR_INVALID_ARG;
   if (C > kMaxChannels) return PE_ERR_OVERFLOW;
-  if (N > 0 && (!x || !weight || (residual_out && !residual))) return PE_ERR_INVALID_ARG;
+  if (N > 0 && (!x || !weight || (residual_out && (!residual || residual_out == y))))
+    return PE_ERR_INVALID_ARG;
   return PE_OK;
 }
 
@@ -775,7 +776,7 @@ extern "C" pe_status pe_rmsnorm(pe_dtype dtype, const void* x, const void* resid
                                 const void* weight, int64_t N, int32_t C, float eps, void* y,
                                 void* residual_out, pe_stream_t stream_) {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  PE_TRY(check_fwd(dtype, x, residual, weight, N, C, eps, residual_out));
+  PE_TRY(check_fwd(dtype, x, residual, weight, N, C, eps, y, residual_out));
   if (N == 0) return PE_OK;
   if (!y) return PE_ERR_INVALID_ARG;
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
@@ -793,7 +794,7 @@ extern "C" pe_status pe_rmsnorm_fp8(pe_dtype dtype, pe_fp8_type fp8_type, const 
                                     pe_stream_t stream_) {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (!fp8_type_ok(fp8_type)) return PE_ERR_UNSUPPORTED;
-  PE_TRY(check_fwd(dtype, x, residual, weight, N, C, eps, residual_out));
+  PE_TRY(check_fwd(dtype, x, residual, weight, N, C, eps, y, residual_out));
   if (N == 0) return PE_OK;
   if (!y8 || !y8_scales) return PE_ERR_INVALID_ARG;
   if (!fp8_layout_ok(y8, y8_ld, C)) return PE_ERR_UNSUPPORTED;

@@ -3,7 +3,8 @@ addresses here are fake and never read)."""
 
 import pytest
 
-from test_fp8_host import OK, OVERFLOW, UNSUPPORTED, _bwd, _mm, _norm, _norm8, lib  # noqa: F401
+from test_fp8_host import (INVALID, OK, OVERFLOW, UNSUPPORTED, _bwd, _mm, _norm,  # noqa: F401
+                           _norm8, lib)
 
 
 @pytest.mark.parametrize("below", [1, 2, 128, 255, 256, 1024])
@@ -41,3 +42,9 @@ def test_workspace_of_sizes_that_no_product_takes(lib):  # noqa: F811
     (2304, 768, 32299, True), (2304, 2304, 8192, True), (2500, 999, 9001, True)])
 def test_runs_of_blocks_are_for_few_tiles_with_long_sums(lib, m, n, k, runs):  # noqa: F811
     assert (lib.pe_matmul_fp8_workspace_size(m, n, k) > 0) == runs
+
+
+def test_a_norm_and_its_sum_need_a_buffer_each(lib):  # noqa: F811
+    assert _norm(lib, res=32, y=64, res_out=64) == INVALID
+    assert _norm8(lib, res=32, y=64, res_out=64) == INVALID
+    assert _norm(lib, res=32, y=64, res_out=64, n=0) == OK
