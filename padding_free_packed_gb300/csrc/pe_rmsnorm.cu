@@ -646,10 +646,11 @@ rmsnorm_bwd_kernel(const BwdArgs<T> a) {
 }
 
 // dweight[c] = the blocks' sums, added in a fixed order: 32 columns per block,
-// 32 rows of threads, each adding every 32nd block's sum.
+// 32 rows of threads, each adding every 32nd block's sum. `part` is not __restrict__:
+// the kernel before may still write it at this one's start, so its loads must not pass
+// for loads of constant memory, which could be moved before the wait.
 __global__ void __launch_bounds__(1024)
-rmsnorm_dweight_kernel(const float* __restrict__ part, int32_t blocks, int32_t C,
-                       float* __restrict__ dweight) {
+rmsnorm_dweight_kernel(const float* part, int32_t blocks, int32_t C, float* dweight) {
   __shared__ float sum[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int32_t c = blockIdx.x * 32 + x;

@@ -42,3 +42,21 @@ def test_calls_refuse_other_workspaces():
     want = pe.pe_matmul_fp8(a, sa, b, sb)
     words = torch.empty(more // 4, dtype=torch.float32, device="cuda:0")
     assert torch.equal(pe.pe_matmul_fp8(a, sa, b, sb, workspace=words), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,c,dtype", [(1, 768, torch.bfloat16), (300, 333, torch.float32),
+                                       (5000, 768, torch.bfloat16)])
+def test_calls_in_turn_through_one_workspace(n, c, dtype):
+    """The second kernel of a call sums what the first left in the workspace, never what
+    the call before did."""
+    gen = torch.Generator(device="cuda:0").manual_seed(551)
+    sets = [[torch.randn(n, c, generator=gen, device="cuda:0").to(dtype) for _ in range(2)]
+            for _ in range(2)]
+    w = torch.ones(c, device="cuda:0", dtype=dtype)
+    want = [pe.pe_rmsnorm_bwd(*s, w) for s in sets]
+    ws = torch.full((pe.load_library().pe_rmsnorm_bwd_workspace_size(c),), 0xFF,
+                    dtype=torch.uint8, device="cuda:0")
+    got = [pe.pe_rmsnorm_bwd(*sets[i % 2], w, workspace=ws) for i in range(200)]
+    for i, one in enumerate(got):
+        assert torch.equal(one[0], want[i % 2][0]) and torch.equal(one[1], want[i % 2][1])
