@@ -26,9 +26,11 @@
 // several pairs share is then summed from their fp32 parts, in the order of k,
 // by a second kernel.
 //
-// Measured (GB300, device time): 169151 x 1024 x 1024 to bf16 in 153 us (2.31
-// PFLOP/s, 1.21 of the measured dense bf16 rate; the floor at twice that rate is
-// 93 us), 32299 x 2304 x 768 in 57 us, 2304 x 768 x 32299 to fp32 in 62 us. The
+// Measured (GB300, device time of a burst): 169151 x 1024 x 1024 to bf16 in 155 us (2.29
+// PFLOP/s, 1.20 of the measured dense bf16 rate; the floor at twice that rate is
+// 93 us; 169 us for seconds on end, when the power cap holds the clock at 1.85 GHz),
+// 32299 x 2304 x 768 in 57 us, 2304 x 768 x 32299 to fp32 in 62 us. A block's MMAs take
+// 517 of the 900 cycles between blocks, in two halves of N = 128 as in one of 256. The
 // epilogue's part in the first: 142 us without its multiply-adds, 134 without the
 // stores, 109 with neither; what is left then is the chain of hand-overs (MMAs,
 // commit, read, arrival from the other CTA some 250 cycles away, next MMAs) over the

@@ -9,8 +9,8 @@
 // scale; column maxima and the tile's maximum go through shared memory. The
 // transposed bytes are packed along a lane's 16 rows and exchanged through
 // shared memory so that every output row is written in runs of 128 bytes.
-// Measured (GB300, device time): 32299 x 2304 bf16 to e5m2 both ways in 52.6 us
-// (5.7 TB/s, 0.85 of the measured copy rate); a weight of 2304 x 768 in 2.8 us.
+// Measured (GB300, device time): 32299 x 2304 bf16 to e5m2 both ways in 53.1 us
+// (5.7 TB/s, 0.84 of the measured copy rate); a weight of 2304 x 768 in 2.8 us.
 #include "pe_fp8.cuh"
 
 namespace pe {

@@ -9,12 +9,12 @@
 // warps, and every output written once. Statistics, products and sums are fp32. Very
 // wide rows take two passes of which the second finds the row in the caches.
 // Measured (GB300, device time): forward with residual and 8-bit output 32299 x 768
-// bf16 in 28.5 us (6.1 TB/s, 0.90 of the measured copy rate), 90487 x 500 fp32 in
-// 41 us (0.82), one row of 768 in 1.6; backward with the residual's gradient 32299 x
+// bf16 in 28.7 us (6.1 TB/s, 0.90 of the measured copy rate), 90487 x 500 fp32 in
+// 42 us (0.81), one row of 768 in 1.7; backward with the residual's gradient 32299 x
 // 768 bf16 in 39.3 us (5.05 TB/s, 0.74; 2 to 3 us of it the second kernel). The
 // backward waits for memory: 64 threads a row with 16 weight sums each, three blocks of
 // 256 threads an SM; rows through a shared-memory ring did not help (46.5 us). bf16 rows
-// of odd width move two bytes at a time, 0.4 to 0.55 of the copy rate (32299 x 777 in 69
+// of odd width move two bytes at a time, 0.4 to 0.55 of the copy rate (32299 x 777 in 71
 // us, backward 58); reading them by aligned 8-byte words shifted together, with the sum
 // written two bytes at a time, took 81.
 #include <math.h>
