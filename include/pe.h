@@ -61,6 +61,15 @@ typedef enum pe_dtype { PE_BF16 = 0, PE_FP32 = 1 } pe_dtype;
  * value F = 448, no infinities) and e5m2 (F = 57344). */
 typedef enum pe_fp8_type { PE_E4M3 = 0, PE_E5M2 = 1 } pe_fp8_type;
 
+/* Activations of pe_matmul and pe_activation_bwd: none, max(z, 0), exact (erf)
+ * GELU, and gelu(z[:, :F]) * z[:, F:] for rows of 2F (as pe_geglu). */
+typedef enum pe_activation {
+  PE_ACT_NONE = 0,
+  PE_ACT_RELU = 1,
+  PE_ACT_GELU = 2,
+  PE_ACT_GEGLU = 3
+} pe_activation;
+
 /* Text for a status code; never NULL. */
 const char* pe_status_string(int status);
 
@@ -73,7 +82,8 @@ const char* pe_status_string(int status);
  * pe_read_noalloc_status; later additions within 3:
  * pe_attention_kernel_local, pe_rmsnorm, pe_rmsnorm_fp8, pe_rmsnorm_bwd and its
  * workspace size, pe_quantize_fp8, pe_matmul_fp8 and its workspace size,
- * pe_read_matmul_status). */
+ * pe_read_matmul_status, pe_matmul and its workspace size, pe_activation_bwd,
+ * pe_layernorm_bwd and their workspace sizes, pe_dropout, pe_rope_axes). */
 int pe_abi_version(void);
 
 /* ------------------------------------------------------------------------
@@ -381,6 +391,96 @@ pe_status pe_layernorm(pe_dtype dtype, const void* x, const void* residual, cons
                        void* residual_out, pe_stream_t stream);
 pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t features, void* y,
                    pe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What training and multi-axis inputs add to the layer tail. As above: I/O
+ * tensors in bf16 or fp32, arithmetic in fp32, asynchronous on `stream`,
+ * nothing allocated, nothing read back, capturable in a CUDA graph. Tensors are
+ * contiguous unless a stride is given. Results are bitwise the same in every
+ * run. Workspaces are device memory, 16-byte aligned, of the size that the
+ * *_workspace_size call gives, else PE_ERR_WORKSPACE; two calls that may run at
+ * the same time need one each.
+ * ------------------------------------------------------------------------ */
+
+/* LayerNorm backward. h is the normalised input as pe_layernorm read or stored
+ * it (x, or residual_out), dy the gradient of y, dresidual (nullable) the
+ * gradient that reaches h by other ways. With n = (h - mean(h)) / sqrt(var(h) +
+ * eps), biased variance, and g = weight dy:
+ *     dx = (g - mean(g) - n mean(g n)) / sqrt(var(h) + eps) (+ dresidual),
+ *     dweight[c] = sum over tokens of dy n, dbias[c] = sum over tokens of dy.
+ * dx is the gradient of x and of residual alike, in the I/O dtype; it may be the
+ * buffer dy, h or dresidual. dweight and dbias (nullable) are fp32 [channels],
+ * zeros when num_tokens is 0. A row of dx does not depend on the other rows.
+ * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
+ * finite and > 0, NULL required pointers; PE_ERR_UNSUPPORTED for other dtypes or
+ * devices and more than 16384 channels. */
+size_t pe_layernorm_bwd_workspace_size(int32_t channels);
+pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void* h, const void* weight,
+                           const void* dresidual, int64_t num_tokens, int32_t channels, float eps,
+                           void* dx, float* dweight, float* dbias, void* workspace,
+                           size_t workspace_bytes, pe_stream_t stream);
+
+/* Backward of an activation and of the bias before it, for dy [rows, features]
+ * and z = pre [rows, features], or [rows, 2 features] with PE_ACT_GEGLU, as
+ * pe_matmul leaves it (pe_geglu's backward with its x as pre):
+ *     dz = dy act'(z)   (relu'(0) = 0; geglu: dy up gelu'(gate), dy gelu(gate)),
+ *     dbias[c] = sum over rows of dz (before its rounding).
+ * dz is shaped like pre and may be its buffer, or, but with PE_ACT_GEGLU, dy's.
+ * dbias (nullable, then no workspace is needed) is fp32, a number for each column
+ * of pre, zeros when rows is 0. PE_ACT_NONE has dz = dy, so pre and dz are NULL
+ * and dbias is the result.
+ * Errors: PE_ERR_INVALID_ARG for negative rows, features < 1, another
+ * activation, NULL required pointers or ones that have to be NULL, dz = dy with
+ * PE_ACT_GEGLU; PE_ERR_OVERFLOW for 2^30 - 1024 features or more;
+ * PE_ERR_UNSUPPORTED for other dtypes or devices. */
+size_t pe_activation_bwd_workspace_size(pe_activation activation, int32_t features);
+pe_status pe_activation_bwd(pe_dtype dtype, pe_activation activation, const void* dy,
+                            const void* pre, int64_t rows, int32_t features, void* dz,
+                            float* dbias, void* workspace, size_t workspace_bytes,
+                            pe_stream_t stream);
+
+/* Dropout of `count` elements, with a residual (nullable) added:
+ *     y[e] = x[e] / (1 - p) (+ residual[e]) where element e is kept,
+ *            0 (+ residual[e]) where it is not.
+ * Element e is kept iff word e % 4 of Philox4x32-10 (J. Salmon et al., SC 2011)
+ * with the key `seed` and the counter (e / 4, offset), 64 bits each, low word
+ * first, is at least p 2^32. So (seed, offset) names a mask, whatever the type,
+ * alignment or residual: the backward is the same call on dy without a residual,
+ * and calls of one seed need offsets of their own. device_offset (nullable, 8-byte
+ * aligned device memory) is added to offset modulo 2^64 when the kernel runs: a
+ * captured graph draws new masks when the caller changes that number between its
+ * launches. y may be x or residual.
+ * Errors: PE_ERR_INVALID_ARG for a negative count, p outside [0, 1), NULL required
+ * pointers; PE_ERR_OVERFLOW for more than 2^60 elements; PE_ERR_UNSUPPORTED for
+ * other dtypes, devices or a device_offset that is not aligned. */
+pe_status pe_dropout(pe_dtype dtype, const void* x, const void* residual, int64_t count, double p,
+                     uint64_t seed, uint64_t offset, const uint64_t* device_offset, void* y,
+                     pe_stream_t stream);
+
+/* Split-half rotary embedding with up to four position axes, of q [N, q_heads, D]
+ * and k [N, k_heads, D] into q_out and k_out (a tensor of 0 heads is left out and
+ * its pointers are not read). sections (HOST memory, num_axes numbers >= 0 that add
+ * up to D / 2) deals a head's D / 2 channel pairs (i, i + D / 2) to the axes in
+ * turn; with a = positions[axis * N + t] * f, pair i of token t becomes
+ *     (x[i] cos a - x[i+D/2] sin a, x[i+D/2] cos a + x[i] sin a),
+ * f = theta^(-2i/D), or with per_axis theta^(-j/s) for pair j of its axis's s: every
+ * axis has the whole range of frequencies. `inverse` turns by -a: the backward, and
+ * the way back. positions is int32 [num_axes, N], of any value; the angle keeps full
+ * precision at far ones.
+ * A stride is the number of elements from a token to the next, at least heads * D
+ * (heads lie D apart), so q and k may be parts of one buffer of q, k and v. q_out may
+ * be q (with the same stride), k_out k; otherwise no output may overlap another tensor.
+ * Errors: PE_ERR_INVALID_ARG for negative sizes, odd D or one above 256, theta that is
+ * not finite and > 1, num_axes outside 1 .. 4, sections that are negative or do not add
+ * up, strides below a token's size, in place with two strides, NULL required pointers;
+ * PE_ERR_OVERFLOW for more than 2^28 elements a token; PE_ERR_UNSUPPORTED for other
+ * dtypes or devices. */
+pe_status pe_rope_axes(pe_dtype dtype, const void* q, int64_t q_stride, void* q_out,
+                       int64_t q_out_stride, int32_t q_heads, const void* k, int64_t k_stride,
+                       void* k_out, int64_t k_out_stride, int32_t k_heads,
+                       const int32_t* positions, const int32_t* sections, int32_t num_axes,
+                       int64_t num_tokens, int32_t head_dim, double theta, int per_axis,
+                       int inverse, pe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The linear steps of a packed encoder layer in 8-bit floating point: a

@@ -10,12 +10,15 @@ from .binding import (  # noqa: F401
     PackedAttentionError,
     attention_workspace_bytes,
     load_library,
+    pe_activation_bwd,
     pe_attention_kernel,
     pe_download_padded,
+    pe_dropout,
     pe_gather_packed,
     pe_flatten_packed_metadata,
     pe_geglu,
     pe_layernorm,
+    pe_layernorm_bwd,
     pe_matmul_fp8,
     pe_pack_document_ids,
     pe_pack_sequences,
@@ -32,6 +35,7 @@ from .binding import (  # noqa: F401
     pe_rmsnorm,
     pe_rmsnorm_bwd,
     pe_rmsnorm_fp8,
+    pe_rope_axes,
     pe_rope_packed,
     pe_scatter_padded,
     pe_set_wait_limit_ns,

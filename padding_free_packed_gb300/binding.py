@@ -32,6 +32,8 @@ EXPORTED = (
     "pe_set_wait_limit_ns", "pe_attention_kernel_local", "pe_rmsnorm", "pe_rmsnorm_fp8",
     "pe_rmsnorm_bwd_workspace_size", "pe_rmsnorm_bwd", "pe_quantize_fp8",
     "pe_matmul_fp8_workspace_size", "pe_matmul_fp8", "pe_read_matmul_status",
+    "pe_layernorm_bwd_workspace_size", "pe_layernorm_bwd", "pe_activation_bwd_workspace_size",
+    "pe_activation_bwd", "pe_dropout", "pe_rope_axes",
 )
 
 _lib = None
@@ -135,6 +137,21 @@ def load_library(path: str = LIB_PATH):
     lib.pe_matmul_fp8.argtypes = [c.c_int, vp, i64, vp, c.c_int, vp, i64, vp, i64, i64, i64,
                                   c.c_int, vp, vp, sz, vp]
     lib.pe_matmul_fp8.restype = c.c_int
+    lib.pe_layernorm_bwd_workspace_size.argtypes = [i32]
+    lib.pe_layernorm_bwd_workspace_size.restype = sz
+    lib.pe_layernorm_bwd.argtypes = [c.c_int, vp, vp, vp, vp, i64, i32, c.c_float, vp, vp, vp, vp,
+                                     sz, vp]
+    lib.pe_layernorm_bwd.restype = c.c_int
+    lib.pe_activation_bwd_workspace_size.argtypes = [c.c_int, i32]
+    lib.pe_activation_bwd_workspace_size.restype = sz
+    lib.pe_activation_bwd.argtypes = [c.c_int, c.c_int, vp, vp, i64, i32, vp, vp, vp, sz, vp]
+    lib.pe_activation_bwd.restype = c.c_int
+    lib.pe_dropout.argtypes = [c.c_int, vp, vp, i64, c.c_double, c.c_uint64, c.c_uint64, vp, vp,
+                               vp]
+    lib.pe_dropout.restype = c.c_int
+    lib.pe_rope_axes.argtypes = [c.c_int, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp,
+                                 c.POINTER(i32), i32, i64, i32, c.c_double, c.c_int, c.c_int, vp]
+    lib.pe_rope_axes.restype = c.c_int
     lib.pe_read_matmul_status.argtypes = [vp]
     lib.pe_read_matmul_status.restype = c.c_int
     _lib = lib
@@ -799,3 +816,153 @@ def pe_read_matmul_status(device=None) -> int:
         torch.device(device))
     with torch.cuda.device(dev):
         return int(load_library().pe_read_matmul_status(_stream(dev)))
+
+
+# --------------------------------------------------------------------------- training the tail
+
+_ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "gelu": 2, "geglu": 3}
+
+
+def _activation_code(activation) -> int:
+    code = _ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"unknown activation {activation!r}: none, relu, gelu or geglu")
+    return code
+
+
+def pe_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                     dresidual: torch.Tensor | None = None, out=None, workspace=None):
+    """LayerNorm backward for the stored norm input h [N, C]; dresidual is the gradient
+    that reaches h by other ways; dy, weight and dresidual are in h's dtype. Returns (dx,
+    dweight, dbias): dx (of x and of residual alike) in h's dtype, or in out (which may
+    be dy, h or dresidual), dweight and dbias fp32 [C]."""
+    lib = load_library()
+    h = _input(h, "h")
+    n, c = _two_dims(h, "h")
+    dy = _input(dy, "dy", h, h.shape)
+    weight = _norm_weight(weight, h, c)
+    if dresidual is not None:
+        dresidual = _input(dresidual, "dresidual", h, h.shape)
+    dx = _output(out, "out", h.shape, h.dtype, h.device)
+    sums = torch.empty((2, c), dtype=torch.float32, device=h.device)
+    dweight, dbias = sums[0], sums[1]
+    ws, ws_bytes = _workspace_for(workspace, lib.pe_layernorm_bwd_workspace_size(c), h.device)
+    _call("pe_layernorm_bwd", h.device, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
+          weight.data_ptr(), _ptr(dresidual), n, c, float(eps), dx.data_ptr(),
+          dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), ws_bytes)
+    return dx, dweight, dbias
+
+
+def pe_activation_bwd(dy: torch.Tensor, pre: torch.Tensor | None, activation="none", out=None,
+                      need_dbias: bool = True, workspace=None):
+    """Backward of an activation ("none", "relu", "gelu" or "geglu") and the bias before
+    it: dy [N, F] and pre, what went into the activation ([N, F], [N, 2F] with geglu, None
+    with "none"), in dy's dtype. Returns (dz, dbias): dz like pre, or in out (which may be
+    pre, or dy but with geglu), dbias the fp32 sums of dz's columns, or None. With "none"
+    dz is dy itself."""
+    lib = load_library()
+    act = _activation_code(activation)
+    dy = _input(dy, "dy")
+    n, f = _two_dims(dy, "dy")
+    wide = 2 * f if act == 3 else f
+    if act == 0:
+        if pre is not None or out is not None or not need_dbias:
+            raise ValueError("without an activation there is only dbias: no pre, no out")
+        dz = None
+    else:
+        if pre is None:
+            raise ValueError("pre is what went into the activation")
+        pre = _input(pre, "pre", dy, (n, wide))
+        dz = _output(out, "out", (n, wide), dy.dtype, dy.device)
+    dbias = torch.empty(wide, dtype=torch.float32, device=dy.device) if need_dbias else None
+    ws, ws_bytes = None, 0
+    if need_dbias:
+        ws, ws_bytes = _workspace_for(workspace, lib.pe_activation_bwd_workspace_size(act, f),
+                                      dy.device)
+    _call("pe_activation_bwd", dy.device, _dtype_code(dy.dtype), act, dy.data_ptr(), _ptr(pre), n,
+          f, _ptr(dz), _ptr(dbias), _ptr(ws), ws_bytes)
+    return (dy if act == 0 else dz), dbias
+
+
+def pe_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+               residual: torch.Tensor | None = None, device_offset: torch.Tensor | None = None,
+               out=None) -> torch.Tensor:
+    """x / (1 - p) where an element is kept, 0 where it is not, plus residual. (seed,
+    offset) names the mask: an element is kept or not by its index alone, so the backward
+    is this call on the gradient with the same numbers. device_offset (int64, one element
+    on x's device) is added to offset when the kernel runs, for captured graphs. out may
+    be x or residual."""
+    x = _input(x, "x")
+    if residual is not None:
+        residual = _input(residual, "residual", x, x.shape)
+    if device_offset is not None:
+        if (device_offset.dtype != torch.int64 or device_offset.numel() != 1
+                or device_offset.device != x.device):
+            raise ValueError(f"device_offset must be one int64 on {x.device}")
+    if not (0 <= seed < 2 ** 64 and 0 <= offset < 2 ** 64):
+        raise ValueError("seed and offset must be from 0 to 2**64 - 1")
+    y = _output(out, "out", x.shape, x.dtype, x.device)
+    _call("pe_dropout", x.device, _dtype_code(x.dtype), x.data_ptr(), _ptr(residual), x.numel(),
+          float(p), int(seed), int(offset), _ptr(device_offset), y.data_ptr())
+    return y
+
+
+def _rope_rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> torch.Tensor:
+    """[N, H, D] on the GPU whose heads lie D apart; tokens may lie further apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got shape {tuple(t.shape)}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d) or (n > 1 and sn < h * d):
+        raise ValueError(f"{name} must have tokens of {h} adjacent heads of {d} adjacent "
+                         f"channels, got strides {t.stride()}")
+    return t
+
+
+def pe_rope_axes(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, sections,
+                 theta: float, per_axis: bool = False, inverse: bool = False, out_q=None,
+                 out_k=None):
+    """Split-half rotary embedding of q [N, Hq, D] and k [N, Hk, D] (or None) with
+    positions int32 [axes, N]: `sections` deals a head's D / 2 channel pairs to the axes in
+    turn, with the frequencies theta^(-2i/D), or with per_axis theta^(-j/s) for pair j of an
+    axis's s. `inverse` turns back (the backward). q and k may be views whose tokens lie
+    further apart, such as parts of one buffer of q, k and v. Returns (q, k) turned, in new
+    contiguous tensors or in out_q and out_k (q and k themselves, for in place)."""
+    load_library()
+    q = _rope_rows(q, "q")
+    sections = [int(s) for s in sections]
+    n, hq, d = q.shape
+    if k is not None:
+        k = _rope_rows(k, "k", q)
+        if k.shape[0] != n or k.shape[2] != d:
+            raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
+    if positions.dtype != torch.int32 or positions.shape != (len(sections), n) or (
+            positions.device != q.device):
+        raise ValueError(f"positions must be int32 of shape {(len(sections), n)} on {q.device}")
+    positions = positions.contiguous()
+
+    def target(out, src, name):
+        if src is None:
+            if out is not None:
+                raise ValueError(f"{name} needs its input")
+            return None
+        if out is None:
+            return torch.empty(src.shape, dtype=src.dtype, device=src.device)
+        if out.shape != src.shape:
+            raise ValueError(f"{name} must have shape {tuple(src.shape)}")
+        return _rope_rows(out, name, src)
+
+    def rows(t):                                 # heads and their stride from token to token
+        return (0, 0) if t is None else (t.shape[1], max(t.stride(0), t.shape[1] * d))
+
+    out_q, out_k = target(out_q, q, "out_q"), target(out_k, k, "out_k")
+    (_, q_step), (hk, k_step) = rows(q), rows(k)
+    _call("pe_rope_axes", q.device, _dtype_code(q.dtype), q.data_ptr(), q_step,
+          out_q.data_ptr(), rows(out_q)[1], hq, _ptr(k), k_step, _ptr(out_k), rows(out_k)[1], hk,
+          positions.data_ptr(), (ctypes.c_int32 * len(sections))(*sections), len(sections), n, d,
+          float(theta), int(bool(per_axis)), int(bool(inverse)))
+    return out_q, out_k

@@ -1,0 +1,305 @@
+// Backward of LayerNorm over packed token rows. h is the normalised input as the forward
+// stored it; with n = (h - mean) rstd and g = w dy,
+//   dx = rstd (g - mean(g) - n mean(g n)) (+ dresidual),
+//   dweight = sum over rows of dy n, dbias = sum over rows of dy.
+// A bandwidth kernel: a row of h and dy is read once into the registers of 1 to 8 warps, its
+// statistics are formed again from there (mean first, then squares of what is left, so a
+// large mean costs no precision), and dx is written once. The weight's and bias's sums of a
+// thread's own channels stay in fp32 registers until the block's last row; a second kernel
+// adds the blocks' lines in a fixed order. The next row's loads are in flight while a row is
+// worked on. Rows wider than 4096 channels take a block each and keep those sums in shared
+// memory.
+#include <math.h>
+
+#include "pe_vec.cuh"
+
+namespace pe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int32_t kMaxChannels = 16384;
+constexpr int32_t kWide = 4096;                 // wider rows: one block of 1024 threads a row
+constexpr int kMaxBlocks = 456, kMaxWideBlocks = 152;
+
+template <typename T>
+struct Args {
+  const T* dy;           // dy, h and dres may be dx: not read through the read-only path
+  const T* h;
+  const T* w;
+  const T* dres;
+  int64_t N;
+  int32_t C;
+  float inv_c;           // 1 / C
+  float eps;
+  T* dx;
+  float* part;           // [gridDim.x][2 C]: this block's sums for the weight, the bias
+};
+
+// Sums of kSums numbers a thread over the kGroup threads of a row, the same in all of them.
+template <int kSums, int kGroup>
+__device__ __forceinline__ void group_sum(float (&x)[kSums], float* red, int group) {
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) x[i] = warp_sum(x[i]);
+  if constexpr (kGroup > 32) {
+    constexpr int kWarps = kGroup / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) red[i * 32 + warp] = x[i];
+    }
+    group_sync<kGroup>(group);
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+      x[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) x[i] += red[i * 32 + group * kWarps + j];
+    }
+  }
+}
+
+// kGroup threads a row, each with kIter vectors of V channels, the same for all of its rows.
+template <typename T, int V, int kIter, int kGroup>
+__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads / kGroup * kGroup)
+layernorm_bwd_kernel(const Args<T> a) {
+  constexpr bool kIsWide = kGroup > kThreads;
+  constexpr int kGroups = kIsWide ? 1 : kThreads / kGroup;
+  constexpr int kBlock = kGroup * kGroups;
+  extern __shared__ float sums[];            // wide: [2][C]; else every group's, at the end
+  __shared__ float red[2][4 * 32];           // two sets: a row's writes miss the last's reads
+  const int g = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
+  const int64_t step = (int64_t)gridDim.x * kGroups;
+  int64_t t = (int64_t)blockIdx.x * kGroups + group;
+
+  constexpr int kKept = kIsWide ? 1 : kIter * V;
+  float dw[kKept], db[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) dw[i] = db[i] = 0.f;
+  if constexpr (kIsWide) {
+    for (int32_t c = threadIdx.x; c < 2 * a.C; c += kBlock) sums[c] = 0.f;
+    __syncthreads();
+  }
+
+  Vec<T, V> dyv[kIter], hv[kIter], rv[kIter];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      dyv[it].zero();
+      hv[it].zero();
+      if (c < a.C && row < a.N) {
+        dyv[it] = load_vec<T, V>(a.dy + row * a.C + c);
+        hv[it] = load_vec<T, V>(a.h + row * a.C + c);
+        if (!kIsWide && a.dres) rv[it] = load_vec<T, V>(a.dres + row * a.C + c);
+      }
+    }
+  };
+  load(t);
+  int phase = 0;
+  for (; t < a.N; t += step) {
+    Vec<T, V> dyn[kIter], hn[kIter], rn[kIter];
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      dyn[it] = dyv[it];
+      hn[it] = hv[it];
+      if constexpr (!kIsWide) rn[it] = rv[it];
+    }
+    if constexpr (!kIsWide) load(t + step);
+    float first[1] = {0.f};
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+#pragma unroll
+      for (int v = 0; v < V; ++v) first[0] += hn[it].get(v);
+    group_sum<1, kGroup>(first, red[phase], group);
+    const float mean = first[0] * a.inv_c;
+    // Squares of h - mean, and sums of g and g (h - mean).
+    float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      if (c < a.C) {
+        const Vec<T, V> wv = load_vec<T, V>(a.w + c);    // from the caches, here and below
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float d = hn[it].get(v) - mean, gv = dyn[it].get(v) * wv.get(v);
+          s[0] = fmaf(d, d, s[0]);
+          s[1] += gv;
+          s[2] = fmaf(gv, d, s[2]);
+        }
+      }
+    }
+    group_sum<3, kGroup>(s, red[phase] + 32, group);
+    phase ^= 1;
+    const float rstd = rsqrtf(fmaf(s[0], a.inv_c, a.eps));
+    const float mean_g = s[1] * a.inv_c;
+    const float along = rstd * (s[2] * a.inv_c) * rstd;      // mean(g n) rstd
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      if (c < a.C) {
+        const Vec<T, V> wv = load_vec<T, V>(a.w + c);
+        if constexpr (kIsWide) {
+          if (a.dres) rn[it] = load_vec<T, V>(a.dres + t * a.C + c);
+        }
+        float dx[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float dy = dyn[it].get(v), d = hn[it].get(v) - mean;
+          dx[v] = rstd * (fmaf(dy, wv.get(v), -mean_g) - d * along);
+          if (a.dres) dx[v] += rn[it].get(v);
+          if constexpr (kIsWide) {
+            sums[c + v] = fmaf(dy, d * rstd, sums[c + v]);
+            sums[a.C + c + v] += dy;
+          } else {
+            dw[it * V + v] = fmaf(dy, d * rstd, dw[it * V + v]);
+            db[it * V + v] += dy;
+          }
+        }
+        Vec<T, V> o;
+        o.put(dx);
+        store_vec<T, V>(a.dx + t * a.C + c, o);
+      }
+    }
+    if constexpr (kIsWide) load(t + step);
+  }
+
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
+  if constexpr (kIsWide) {
+    __syncthreads();
+    for (int32_t c = threadIdx.x; c < 2 * a.C; c += kBlock) part[c] = sums[c];
+  } else if constexpr (kGroups == 1) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int32_t c = (it * kGroup + g) * V + v;
+        if (c < a.C) {
+          part[c] = dw[it * V + v];
+          part[a.C + c] = db[it * V + v];
+        }
+      }
+  } else {
+    // [group][vector element][thread], a row padded so that neither access conflicts; the
+    // weight's sums, then the bias's.
+    constexpr int kLine = kGroup + 1;
+    float* mine = sums + group * (kIter * V * kLine);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kIter * V; ++i) mine[i * kLine + g] = which ? db[i] : dw[i];
+      __syncthreads();
+      for (int32_t c = threadIdx.x; c < a.C; c += kBlock) {
+        const int vec = c / V, i = vec / kGroup * V + c % V;
+        float total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGroups; ++w) total += sums[(w * kIter * V + i) * kLine + vec % kGroup];
+        part[which * a.C + c] = total;
+      }
+    }
+  }
+}
+
+template <typename T, int V, int kIter, int kGroup>
+pe_status launch(const Args<T>& a, float* dweight, float* dbias, cudaStream_t stream) {
+  constexpr bool wide = kGroup > kThreads;
+  constexpr int kGroups = wide ? 1 : kThreads / kGroup;
+  static_assert(!wide || kIter * kGroup * V >= kMaxChannels, "a block holds the widest row");
+  int64_t blocks = ceil_div(a.N, kGroups);
+  const int64_t most = wide ? kMaxWideBlocks : kMaxBlocks;
+  if (blocks > most) blocks = most;
+  const size_t smem = wide ? 2 * (size_t)a.C * sizeof(float)
+                      : kGroups > 1 ? (size_t)kGroups * kIter * V * (kGroup + 1) * sizeof(float)
+                                    : 0;
+  const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup>;
+  if (wide)
+    PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     2 * kMaxChannels * (int)sizeof(float)));
+  kernel<<<(unsigned)blocks, kGroup * kGroups, smem, stream>>>(a);
+  PE_CUDA_TRY(cudaGetLastError());
+  return launch_sum_parts(a.part, (int32_t)blocks, a.C, dweight, a.C, dbias, stream);
+}
+
+// The form for V neighbouring channels per access: vectors a thread and threads a row, by the
+// row's width.
+template <typename T, int V>
+pe_status launch_rows(const Args<T>& a, float* dweight, float* dbias, cudaStream_t stream) {
+  const int32_t C = a.C;
+  if (C > kWide) return launch<T, V, 16 / V, 1024>(a, dweight, dbias, stream);
+  if constexpr (V == 8) {
+    if (C <= 256) return launch<T, V, 1, 32>(a, dweight, dbias, stream);
+    if (C <= 512) return launch<T, V, 2, 32>(a, dweight, dbias, stream);
+    if (C <= 1024) return launch<T, V, 2, 64>(a, dweight, dbias, stream);
+    if (C <= 2048) return launch<T, V, 2, 128>(a, dweight, dbias, stream);
+    return launch<T, V, 2, 256>(a, dweight, dbias, stream);
+  } else {
+    constexpr int kIter = 8 / V;               // eight channels a thread
+    if (C <= 256) return launch<T, V, kIter, 32>(a, dweight, dbias, stream);
+    if (C <= 512) return launch<T, V, kIter, 64>(a, dweight, dbias, stream);
+    if (C <= 1024) return launch<T, V, kIter, 128>(a, dweight, dbias, stream);
+    if (C <= 2048) return launch<T, V, kIter, 256>(a, dweight, dbias, stream);
+    return launch<T, V, 2 * kIter, 256>(a, dweight, dbias, stream);
+  }
+}
+
+template <typename T>
+pe_status run(const void* dy, const void* h, const void* w, const void* dres, int64_t N,
+              int32_t C, float eps, void* dx, float* dweight, float* dbias, void* ws,
+              cudaStream_t stream) {
+  const Args<T> a = {static_cast<const T*>(dy),
+                     static_cast<const T*>(h),
+                     static_cast<const T*>(w),
+                     static_cast<const T*>(dres),
+                     N,
+                     C,
+                     1.f / (float)C,
+                     eps,
+                     static_cast<T*>(dx),
+                     static_cast<float*>(ws)};
+  constexpr int V = 16 / sizeof(T);
+  if (vectors<V>(C, a.dy, a.w, a.h, a.dx, a.dres))
+    return launch_rows<T, V>(a, dweight, dbias, stream);
+  if (V > 4 && vectors<4>(C, a.dy, a.w, a.h, a.dx, a.dres))
+    return launch_rows<T, 4>(a, dweight, dbias, stream);
+  if (vectors<2>(C, a.dy, a.w, a.h, a.dx, a.dres))
+    return launch_rows<T, 2>(a, dweight, dbias, stream);
+  return launch_rows<T, 1>(a, dweight, dbias, stream);
+}
+
+}  // namespace
+
+}  // namespace pe
+
+using namespace pe;
+
+extern "C" size_t pe_layernorm_bwd_workspace_size(int32_t C) {
+  if (C < 1 || C > kMaxChannels) return 0;
+  return (size_t)(C > kWide ? kMaxWideBlocks : kMaxBlocks) * 2 * (size_t)C * sizeof(float);
+}
+
+extern "C" pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void* h,
+                                      const void* weight, const void* dresidual, int64_t N,
+                                      int32_t C, float eps, void* dx, float* dweight,
+                                      float* dbias, void* workspace, size_t workspace_bytes,
+                                      pe_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype != PE_BF16 && dtype != PE_FP32) return PE_ERR_UNSUPPORTED;
+  if (N < 0 || C < 1 || !(eps > 0.f) || !isfinite(eps) || !dweight) return PE_ERR_INVALID_ARG;
+  if (C > kMaxChannels) return PE_ERR_UNSUPPORTED;
+  if (N > 0) {
+    if (!dy || !h || !weight || !dx) return PE_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < pe_layernorm_bwd_workspace_size(C))
+      return PE_ERR_WORKSPACE;
+  }
+  if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
+  if (N == 0) {
+    PE_CUDA_TRY(cudaMemsetAsync(dweight, 0, (size_t)C * sizeof(float), stream));
+    if (dbias) PE_CUDA_TRY(cudaMemsetAsync(dbias, 0, (size_t)C * sizeof(float), stream));
+    return PE_OK;
+  }
+  if (dtype == PE_FP32)
+    return run<float>(dy, h, weight, dresidual, N, C, eps, dx, dweight, dbias, workspace, stream);
+  return run<__nv_bfloat16>(dy, h, weight, dresidual, N, C, eps, dx, dweight, dbias, workspace,
+                            stream);
+}

@@ -20,111 +20,16 @@
 #include <math.h>
 
 #include "pe_fp8.cuh"
+#include "pe_vec.cuh"
 
 namespace pe {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr unsigned kFull = 0xffffffffu;
 
 // 8-bit output of a forward: none, e4m3 or e5m2.
 enum Mode { kNoFp8 = 0, kE4M3 = 1, kE5M2 = 2 };
-
-// V consecutive elements of a row, kept as loaded: bf16 pairs stay in one register
-// until they are used.
-template <typename T, int V>
-struct Vec;
-template <int V>
-struct alignas(4 * V) Vec<float, V> {
-  float w[V];
-  __device__ float get(int v) const { return w[v]; }
-  __device__ void zero() {
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = 0.f;
-  }
-  __device__ void put(const float* x) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = x[v];
-  }
-  __device__ void add(const Vec& o) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] += o.w[v];
-  }
-};
-template <int V>
-struct alignas(2 * V) Vec<__nv_bfloat16, V> {
-  uint32_t w[V / 2];
-  __device__ float get(int v) const {
-    return __uint_as_float(v & 1 ? w[v >> 1] & 0xffff0000u : w[v >> 1] << 16);
-  }
-  __device__ void zero() {
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) w[v] = 0u;
-  }
-  __device__ void put(const float* x) {
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) {
-      const __nv_bfloat162 pair = __floats2bfloat162_rn(x[2 * v], x[2 * v + 1]);
-      w[v] = *reinterpret_cast<const uint32_t*>(&pair);
-    }
-  }
-  // The rounded fp32 sum, two at a time: an fp32 sum of bf16 numbers is exact
-  // unless one is below 2^-16 of the other, when rounding it first changes nothing.
-  __device__ void add(const Vec& o) {
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) {
-      const __nv_bfloat162 sum = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&w[v]),
-                                            *reinterpret_cast<const __nv_bfloat162*>(&o.w[v]));
-      w[v] = *reinterpret_cast<const uint32_t*>(&sum);
-    }
-  }
-};
-template <>
-struct Vec<__nv_bfloat16, 1> {
-  __nv_bfloat16 w[1];
-  __device__ float get(int) const { return __bfloat162float(w[0]); }
-  __device__ void zero() { w[0] = __float2bfloat16_rn(0.f); }
-  __device__ void put(const float* x) { w[0] = __float2bfloat16_rn(x[0]); }
-  __device__ void add(const Vec& o) { w[0] = __float2bfloat16_rn(get(0) + o.get(0)); }
-};
-
-// One access of a vector's bytes.
-template <int kBytes>
-struct Bits;
-template <>
-struct Bits<2> { using type = uint16_t; };
-template <>
-struct Bits<4> { using type = uint32_t; };
-template <>
-struct Bits<8> { using type = uint2; };
-template <>
-struct Bits<16> { using type = uint4; };
-
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
-  using B = typename Bits<(int)sizeof(T) * V>::type;
-  Vec<T, V> v;
-  *reinterpret_cast<B*>(v.w) = *reinterpret_cast<const B*>(p);
-  return v;
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
-  using B = typename Bits<(int)sizeof(T) * V>::type;
-  *reinterpret_cast<B*>(p) = *reinterpret_cast<const B*>(v.w);
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
-  return x;
-}
-
-// A barrier of the kGroup threads that share a row.
-template <int kGroup>
-__device__ __forceinline__ void group_sync(int group) {
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kGroup) : "memory");
-}
 
 template <typename T>
 struct FwdArgs {
@@ -476,14 +381,6 @@ void launch_rows(const FwdArgs<T>& a, cudaStream_t stream) {
     if (C <= 3 * 1024) return launch_row<T, V, 3, 8, 4, kMode>(a, stream);
   }
   rmsnorm_any_kernel<T, V, kMode><<<row_grid(a.N, kThreads / 32, 16), kThreads, 0, stream>>>(a);
-}
-
-// Whether rows of C channels and their tensors allow accesses of V channels.
-template <int V, typename T, typename... P>
-bool vectors(int32_t C, const T* p, P... rest) {
-  bool ok = C % V == 0 && aligned(p, V * sizeof(T));
-  ((ok = ok && aligned(rest, V * sizeof(T))), ...);
-  return ok;
 }
 
 template <typename T, int kMode>
