@@ -13,7 +13,7 @@
  *     pe_download_padded. The library allocates nothing; between calls it
  *     keeps only per-device attribute caches, the process-wide wait limit
  *     (pe_set_wait_limit_ns), the allocation-free forward's static array and
- *     the 8-bit matrix product's status word.
+ *     the matrix products' status word.
  *   - Every call is asynchronous on `stream` (NULL = the legacy default
  *     stream), except pe_pack_sequences, pe_pack_document_ids and
  *     pe_flatten_packed_metadata, which perform one host read each, and the
@@ -393,7 +393,8 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
                    pe_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * What training and multi-axis inputs add to the layer tail. As above: I/O
+ * The layer's dense products in 16 and 32 bits, and what training and
+ * multi-axis inputs add to its tail. As above: I/O
  * tensors in bf16 or fp32, arithmetic in fp32, asynchronous on `stream`,
  * nothing allocated, nothing read back, capturable in a CUDA graph. Tensors are
  * contiguous unless a stride is given. Results are bitwise the same in every
@@ -401,6 +402,45 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  * *_workspace_size call gives, else PE_ERR_WORKSPACE; two calls that may run at
  * the same time need one each.
  * ------------------------------------------------------------------------ */
+
+/* The dense products of a layer, with what follows them in the same pass:
+ *     z = a b^T + bias,  out = act(z) + residual  (and z itself into pre)
+ * for a [m, k] and b [n, k]. a_transposed: a is stored [k, m]; b_transposed: b is
+ * stored [k, n]. With X [tokens, in], W [out, in] and an output gradient dZ
+ * [tokens, out] that is
+ *     Z  = X W^T     a = X,              b = W
+ *     dX = dZ W      a = dZ,             b = W transposed
+ *     dW = dZ^T X    a = dZ transposed,  b = X transposed (residual: a sum so far).
+ * PE_ACT_GEGLU: z has n = 2F columns, out [m, F] = gelu(z[:, :F]) * z[:, F:].
+ * dtype is that of a and b: PE_BF16, or PE_FP32, whose numbers are split into three
+ * bf16 parts and multiplied part by part on the tensor cores (six products; what is
+ * left out is below 2^-23 of |a| |b|). Sums are fp32, in an order that depends on the
+ * sizes alone: the result is bitwise the same in every run on a device. An infinity or
+ * a NaN among fp32 operands makes every sum it enters NaN; bf16 operands follow IEEE.
+ * Bias (n numbers), residual, out and pre are in out_dtype, out rounded once; bias,
+ * residual and pre are nullable. Every *_ld is the number of elements from a stored row
+ * to the next, at least the row's length (not looked at for a NULL tensor). bf16
+ * operands start at, and have rows that start at, multiples of 16 bytes. out may be the
+ * buffer residual (with the same ld); otherwise no output may overlap another tensor.
+ * k = 0 has sums of 0, and a and b are not read.
+ * workspace: device, 16-byte aligned, >= pe_matmul_workspace_size(...) bytes; may be
+ * NULL when that is 0. Calls that may run at the same time need one each.
+ * A pipeline wait that gives up (pe_set_wait_limit_ns) leaves out and pre incomplete and
+ * records PE_ERR_DEVICE_TIMEOUT in the word that pe_read_matmul_status reads.
+ * Errors: PE_ERR_INVALID_ARG for negative sizes, another activation, an odd n with
+ * PE_ACT_GEGLU, NULL required pointers, an ld below the row's length, pre = out or
+ * residual, out = residual with two lds; PE_ERR_OVERFLOW for m or n of 2^31 - 1024 or
+ * more, k of a sixth of that, more than 2^29 / 6 blocks of 256 x 128 x 64, or an ld above
+ * 2^36; PE_ERR_UNSUPPORTED for other dtypes or devices, operands that are not aligned,
+ * tensors not aligned to their elements, and PE_ACT_GEGLU with b_transposed where F is
+ * not a multiple of 8; PE_ERR_WORKSPACE. */
+size_t pe_matmul_workspace_size(pe_dtype dtype, int a_transposed, int b_transposed, int64_t m,
+                                int64_t n, int64_t k, pe_activation activation);
+pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int a_transposed, const void* b,
+                    int64_t b_ld, int b_transposed, int64_t m, int64_t n, int64_t k,
+                    const void* bias, pe_activation activation, const void* residual,
+                    int64_t residual_ld, pe_dtype out_dtype, void* out, int64_t out_ld, void* pre,
+                    int64_t pre_ld, void* workspace, size_t workspace_bytes, pe_stream_t stream);
 
 /* LayerNorm backward. h is the normalised input as pe_layernorm read or stored
  * it (x, or residual_out), dy the gradient of y, dresidual (nullable) the

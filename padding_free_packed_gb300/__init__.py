@@ -19,6 +19,7 @@ from .binding import (  # noqa: F401
     pe_geglu,
     pe_layernorm,
     pe_layernorm_bwd,
+    pe_matmul,
     pe_matmul_fp8,
     pe_pack_document_ids,
     pe_pack_sequences,

@@ -33,7 +33,7 @@ EXPORTED = (
     "pe_rmsnorm_bwd_workspace_size", "pe_rmsnorm_bwd", "pe_quantize_fp8",
     "pe_matmul_fp8_workspace_size", "pe_matmul_fp8", "pe_read_matmul_status",
     "pe_layernorm_bwd_workspace_size", "pe_layernorm_bwd", "pe_activation_bwd_workspace_size",
-    "pe_activation_bwd", "pe_dropout", "pe_rope_axes",
+    "pe_activation_bwd", "pe_dropout", "pe_rope_axes", "pe_matmul_workspace_size", "pe_matmul",
 )
 
 _lib = None
@@ -152,6 +152,11 @@ def load_library(path: str = LIB_PATH):
     lib.pe_rope_axes.argtypes = [c.c_int, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp,
                                  c.POINTER(i32), i32, i64, i32, c.c_double, c.c_int, c.c_int, vp]
     lib.pe_rope_axes.restype = c.c_int
+    lib.pe_matmul_workspace_size.argtypes = [c.c_int, c.c_int, c.c_int, i64, i64, i64, c.c_int]
+    lib.pe_matmul_workspace_size.restype = sz
+    lib.pe_matmul.argtypes = [c.c_int, vp, i64, c.c_int, vp, i64, c.c_int, i64, i64, i64, vp,
+                              c.c_int, vp, i64, c.c_int, vp, i64, vp, i64, vp, sz, vp]
+    lib.pe_matmul.restype = c.c_int
     lib.pe_read_matmul_status.argtypes = [vp]
     lib.pe_read_matmul_status.restype = c.c_int
     _lib = lib
@@ -810,7 +815,7 @@ def pe_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
 
 
 def pe_read_matmul_status(device=None) -> int:
-    """Status of the 8-bit matrix products on the device since the last read (0:
+    """Status of the matrix products on the device since the last read (0:
     every pipeline wait completed); waits for the current stream and clears it."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else (
         torch.device(device))
@@ -818,7 +823,7 @@ def pe_read_matmul_status(device=None) -> int:
         return int(load_library().pe_read_matmul_status(_stream(dev)))
 
 
-# --------------------------------------------------------------------------- training the tail
+# --------------------------------------------------------------------------- 16 and 32 bits
 
 _ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "gelu": 2, "geglu": 3}
 
@@ -828,6 +833,80 @@ def _activation_code(activation) -> int:
     if code is None:
         raise ValueError(f"unknown activation {activation!r}: none, relu, gelu or geglu")
     return code
+
+
+def _operand(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
+    """A matrix whose rows the product can read, and the elements from row to row: bf16 rows
+    that do not start at multiples of 16 bytes are copied into some that do."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    rows, cols = _two_dims(t, name)
+    ld, step = t.stride()
+    bf16 = t.dtype is torch.bfloat16
+    if rows <= 1:
+        ld = cols + 7 & -8
+    if (step == 1 or cols <= 1) and ld >= cols and not (
+            bf16 and (ld % 8 or t.data_ptr() % 16)):
+        return t, ld
+    ld = cols + 7 & -8
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=t.dtype, device=t.device).copy_(t), ld
+
+
+def _row_tensor(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """The elements from row to row of a caller's matrix of adjacent columns, after a check."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    ld, step = t.stride()
+    rows, cols = shape
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name} must have rows of adjacent elements, got strides {t.stride()}")
+    return ld if rows > 1 else cols
+
+
+def pe_matmul(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None,
+              activation="none", residual: torch.Tensor | None = None, dtype=None, out=None,
+              pre=None, a_transposed: bool = False, b_transposed: bool = False, workspace=None):
+    """act(a b^T + bias) + residual for a [M, K] (stored [K, M] with a_transposed) and b [N, K]
+    ([K, N] with b_transposed), both bfloat16 or both float32; activation "none", "relu",
+    "gelu" or "geglu" (gelu of the first N / 2 columns times the others). Returns [M, N] ([M,
+    N / 2] with geglu) in `dtype` (a's by default), or in `out` and its dtype. With `pre` [M,
+    N], a b^T + bias is also written there. bias, residual and pre are in out's dtype. out
+    may be residual; out, residual and pre may be parts of wider matrices. bf16 operands
+    whose rows do not start at multiples of 16 bytes are copied first."""
+    lib = load_library()
+    act = _activation_code(activation)
+    a, a_ld = _operand(a, "a")
+    b, b_ld = _operand(b, "b")
+    m, k = a.shape[::-1] if a_transposed else a.shape
+    n, kb = b.shape[::-1] if b_transposed else b.shape
+    dev = a.device
+    if kb != k or b.dtype is not a.dtype or b.device != dev:
+        raise ValueError(f"a is {a.dtype} {tuple(a.shape)} on {dev}, b is {b.dtype} "
+                         f"{tuple(b.shape)} on {b.device}")
+    if act == 3 and n % 2:
+        raise ValueError(f"geglu needs an even number of columns, got {n}")
+    wide = n // 2 if act == 3 else n
+    code = _dtype_code(a.dtype)
+    if out is None:
+        out = torch.empty((m, wide), dtype=a.dtype if dtype is None else dtype, device=dev)
+        out_ld = wide
+    else:
+        out_ld = _row_tensor(out, "out", (m, wide), out.dtype, dev)
+    out_code = _dtype_code(out.dtype)
+    residual_ld = pre_ld = 0
+    if bias is not None:
+        bias = _input(bias, "bias", out, (n,))
+    if residual is not None:
+        residual_ld = _row_tensor(residual, "residual", (m, wide), out.dtype, dev)
+    if pre is not None:
+        pre_ld = _row_tensor(pre, "pre", (m, n), out.dtype, dev)
+    need = lib.pe_matmul_workspace_size(code, a_transposed, b_transposed, m, n, k, act)
+    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
+    _call("pe_matmul", dev, code, a.data_ptr(), a_ld, a_transposed, b.data_ptr(), b_ld,
+          b_transposed, m, n, k, _ptr(bias), act, _ptr(residual), residual_ld, out_code,
+          out.data_ptr(), out_ld, _ptr(pre), pre_ld, _ptr(ws), ws_bytes)
+    return out
 
 
 def pe_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,

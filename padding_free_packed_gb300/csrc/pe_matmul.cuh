@@ -1,0 +1,168 @@
+// Internal interface of the 16- and 32-bit matrix product's kernels:
+//   z = a b^T + bias, out = act(z) + residual, and z itself as pre.
+#pragma once
+
+#include "pe_act.cuh"
+#include "pe_matmul_fp8.cuh"
+#include "pe_sm103.cuh"
+
+namespace pe {
+
+constexpr int kMatmulBlock = 64;           // k's elements in 128 bytes, the swizzle's width
+
+// A product's operand in bf16: `planes` matrices one after the other (three parts of an fp32
+// matrix, largest first, or the matrix itself).
+struct MatmulOperand {
+  const void* base;
+  int64_t ld;              // elements
+  bool transposed;         // stored [k, rows] instead of [rows, k]
+};
+
+// What follows the product. n counts the columns of out; with geglu z has twice as many.
+struct MatmulEpilogue {
+  const void* bias;        // in out's type, as residual and pre are
+  const void* residual;
+  void* out;
+  void* pre;
+  int64_t residual_ld, out_ld, pre_ld;     // elements
+  int32_t m, n;
+  int32_t act;
+  int32_t out_fp32;
+  int32_t by_four;         // rows of all of them start at multiples of four elements
+};
+
+struct Matmul {
+  MatmulOperand a, b;
+  int32_t m, n, k;         // n: rows of b
+  int32_t planes;          // 1, or 3 with six products of parts
+  MatmulEpilogue e;
+};
+
+// How a product runs. The choice depends on the sizes alone (the workspace size follows it);
+// it counts the 152 SMs of the device these kernels are built for.
+struct LinearPlan {
+  int32_t rows;            // of a per CTA of the narrow kernel: 16, 32 or 64; 0: tiles
+  int32_t split;           // narrow: CTAs of a cluster that share a tile's sum
+  bool runs;               // tiles: equal runs of blocks of k, parts summed by a second kernel
+};
+
+constexpr int kMaxMatmulTerms = 6;
+// Products of parts of x = h + m + l, the smallest first: l h, h l, m m, m h, h m, h h. A part
+// is at most 2^-8 of the one before it, so what is left out is below 2^-23 of |a| |b|.
+__host__ __device__ __forceinline__ int32_t term_a(int32_t term, int32_t terms) {
+  return (0x001102 >> (4 * (terms == 1 ? 5 : term))) & 3;
+}
+__host__ __device__ __forceinline__ int32_t term_b(int32_t term, int32_t terms) {
+  return (0x010120 >> (4 * (terms == 1 ? 5 : term))) & 3;
+}
+
+// Whole tiles of 256 x 256 (or runs of blocks) on pairs of CTAs.
+size_t matmul_tiles_workspace();
+pe_status matmul_tiles(const Matmul& p, bool runs, void* workspace, DeviceStatus* status,
+                       cudaStream_t stream);
+// What is left of a product without a sum: z = bias.
+pe_status matmul_no_sum(const Matmul& p, cudaStream_t stream);
+// Few rows: 128 rows of b by 16, 32 or 64 rows of a per CTA, the sum over k split over a
+// cluster.
+pe_status matmul_narrow(const Matmul& p, int32_t rows, int32_t split, DeviceStatus* status,
+                        cudaStream_t stream);
+
+namespace sm103 {
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ float load_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// An element of a tensor in out's type.
+__device__ __forceinline__ float io_get(const void* p, int64_t at, int32_t fp32) {
+  return fp32 ? static_cast<const float*>(p)[at]
+              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+}
+__device__ __forceinline__ void io_put(void* p, int64_t at, int32_t fp32, float v) {
+  if (fp32)
+    static_cast<float*>(p)[at] = v;
+  else
+    static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+}
+
+// gelu where the result is rounded to fp32; out of line, as it is long.
+static __device__ __noinline__ float gelu_fp32(float z) { return gelu<float>(z); }
+
+__device__ __forceinline__ float matmul_gelu(float z, int32_t out_fp32) {
+  return out_fp32 ? gelu_fp32(z) : gelu<__nv_bfloat16>(z);
+}
+
+// Four neighbouring columns of out from their sums (with geglu: gate and up), `left` of them
+// inside the matrix.
+__device__ __forceinline__ void finish4(const MatmulEpilogue& e, int64_t row, int32_t col,
+                                        int32_t left, const float (&sum)[4],
+                                        const float (&up_sum)[4]) {
+  const bool geglu = e.act == PE_ACT_GEGLU;
+  const int32_t count = left < 4 ? left : 4;
+  float z[4], u[4], y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    z[j] = sum[j];
+    u[j] = up_sum[j];
+    if (e.bias && j < count) {
+      z[j] += io_get(e.bias, col + j, e.out_fp32);
+      if (geglu) u[j] += io_get(e.bias, (int64_t)e.n + col + j, e.out_fp32);
+    }
+    y[j] = e.act == PE_ACT_RELU ? (z[j] < 0.f ? 0.f : z[j])
+           : e.act >= PE_ACT_GELU ? matmul_gelu(z[j], e.out_fp32)
+                                  : z[j];
+    if (geglu) y[j] *= u[j];
+  }
+  auto put = [&](void* p, int64_t at, const float (&v)[4], bool four) {
+    if (four) {
+      if (e.out_fp32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) =
+            make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < count) io_put(p, at + j, e.out_fp32, v[j]);
+    }
+  };
+  const bool four = e.by_four && count == 4;
+  if (e.pre) {
+    put(e.pre, row * e.pre_ld + col, z, four);
+    if (geglu) put(e.pre, row * e.pre_ld + e.n + col, u, four && e.n % 4 == 0);
+  }
+  if (e.residual) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < count) y[j] += io_get(e.residual, row * e.residual_ld + col + j, e.out_fp32);
+  }
+  put(e.out, row * e.out_ld + col, y, four);
+}
+
+}  // namespace sm103
+}  // namespace pe

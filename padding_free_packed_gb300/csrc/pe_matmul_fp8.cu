@@ -26,8 +26,12 @@ __device__ DeviceStatus g_matmul_status;
 constexpr int kMaxDevices = 64;
 std::atomic<DeviceStatus*> g_status_address[kMaxDevices];
 
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
+
+}  // namespace
+
 // The status word's address on the current device.
-pe_status status_word(DeviceStatus** out) {
+pe_status matmul_status_word(DeviceStatus** out) {
   int dev = 0;
   PE_CUDA_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= kMaxDevices) return PE_ERR_CUDA;
@@ -41,10 +45,6 @@ pe_status status_word(DeviceStatus** out) {
   *out = word;
   return PE_OK;
 }
-
-std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
-
-}  // namespace
 
 // Estimated microseconds of every way, from times measured on a GB300 (m x n x k,
 // bf16 out; T: rows of a per CTA, S: split; pair: whole tiles of the pair kernel, runs:
@@ -99,6 +99,12 @@ MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
 
 pe_status matmul_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base,
                      int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
+  return matmul_map_planes(map, type, size, base, rows, cols, pitch, box_rows, 0);
+}
+
+pe_status matmul_map_planes(CUtensorMap* map, CUtensorMapDataType type, int size,
+                            const void* base, int64_t rows, int64_t cols, int64_t pitch,
+                            uint32_t box_rows, int32_t planes) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = g_encode.load();
   if (!encode) {
     void* fn = nullptr;
@@ -109,12 +115,14 @@ pe_status matmul_map(CUtensorMap* map, CUtensorMapDataType type, int size, const
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     g_encode.store(encode);
   }
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  cuuint32_t box[2] = {128u / size, box_rows};
-  cuuint32_t elem_strides[2] = {1, 1};
-  CUresult r = encode(map, type, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(planes)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch),
+                           static_cast<cuuint64_t>(pitch) * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[3] = {128u / size, box_rows, 1};
+  cuuint32_t elem_strides[3] = {1, 1, 1};
+  CUresult r = encode(map, type, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                      elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PE_OK : PE_ERR_CUDA;
 }
@@ -154,7 +162,7 @@ extern "C" pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_
   if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return PE_ERR_WORKSPACE;
   DeviceStatus* status = nullptr;
-  PE_TRY(status_word(&status));
+  PE_TRY(matmul_status_word(&status));
   const MatmulFp8 p = {static_cast<const uint8_t*>(a),
                        static_cast<const uint8_t*>(b),
                        a_ld,
@@ -175,7 +183,7 @@ extern "C" pe_status pe_matmul_fp8(pe_fp8_type a_type, const void* a, int64_t a_
 extern "C" pe_status pe_read_matmul_status(pe_stream_t stream_) {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   DeviceStatus* word = nullptr;
-  PE_TRY(status_word(&word));
+  PE_TRY(matmul_status_word(&word));
   DeviceStatus st = {};
   PE_CUDA_TRY(cudaMemcpyAsync(&st, word, sizeof(st), cudaMemcpyDeviceToHost, stream));
   PE_CUDA_TRY(cudaMemsetAsync(word, 0, sizeof(st), stream));

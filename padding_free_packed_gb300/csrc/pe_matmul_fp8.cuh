@@ -40,6 +40,13 @@ pe_status matmul_rows(const MatmulFp8& p, int32_t rows, int32_t split, DeviceSta
 // `pitch` bytes apart, boxes of box_rows rows of 128 bytes, 128-byte swizzle.
 pe_status matmul_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base,
                      int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows);
+// The same for `planes` such matrices, one after the other (0: without that dimension).
+pe_status matmul_map_planes(CUtensorMap* map, CUtensorMapDataType type, int size,
+                            const void* base, int64_t rows, int64_t cols, int64_t pitch,
+                            uint32_t box_rows, int32_t planes);
+
+// The address, on the current device, of the status word that every product's waits share.
+pe_status matmul_status_word(DeviceStatus** out);
 
 namespace sm103 {
 
