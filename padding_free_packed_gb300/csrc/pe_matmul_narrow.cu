@@ -5,8 +5,9 @@
 // is narrow (128 rows of b, which is the MMA's M, by kT = 16, 32 or 64 rows of a, its N),
 // several blocks of k are in flight in a CTA, and a cluster of up to 8 CTAs shares the sum
 // over k, joined through distributed shared memory in the order of k (no workspace, no
-// second launch). A CTA's sum stays in tensor memory until its last block; its four warps
-// then copy it to shared memory, and the cluster's CTAs deal out the rows among them: a lane
+// second launch). An accumulator sums four blocks of k, which four warps then add to fp32
+// sums in registers (the tensor cores cut a sum off after every 16 products); at the end they
+// copy them to shared memory, and the cluster's CTAs deal out the rows among them: a lane
 // adds four neighbouring columns, finishes them and writes them.
 // With geglu the tile's rows of b are 64 of the gate's and the same 64 of the up part's.
 //
@@ -23,6 +24,7 @@ using namespace sm103;
 
 constexpr int kThreads = 192;
 constexpr int kMaxSplit = 8;
+constexpr int kChunk = 4;                 // blocks of k that one accumulator sums
 constexpr uint32_t kBBytes = 128 * 128;
 
 // Blocks in flight: two CTAs share an SM.
@@ -39,7 +41,8 @@ struct alignas(1024) Smem {
     float sums[kT][128];                  // this CTA's part, once its loads are done
   };
   uint64_t full[kStages<kT>], empty[kStages<kT>];
-  uint64_t sum_full, drain;
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
   uint32_t tmem_base;
   WaitGuard guard;
 };
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kThreads)
 matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
                      const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ Params p) {
   constexpr int S = kStages<kT>;
-  constexpr uint32_t kTmemCols = kT < 32 ? 32 : kT;
+  constexpr uint32_t kTmemCols = 2 * kT;
   constexpr int32_t kOutCols = kGeglu ? 64 : 128;          // of a tile
   extern __shared__ uint8_t raw[];
   Smem<kT>& s =
@@ -102,7 +105,10 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
-    mbar_init(smem_u32(&s.sum_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.acc_full[i]), 1);
+      mbar_init(smem_u32(&s.acc_empty[i]), 4);
+    }
     mbar_init(smem_u32(&s.drain), 1);
     s.guard.abort = 0;
     s.guard.limit_ns = p.wait_limit_ns;
@@ -168,40 +174,66 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
       const int stage = i % S;
       ok = warp_wait(smem_u32(&s.full[stage]), (i / S) & 1, guard, p.status, kSiteMma);
       if (!ok) break;
+      const int32_t turn = i / kChunk, buf = turn & 1;
+      if (i % kChunk == 0) {
+        ok = warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
+                       kSiteMma);
+        if (!ok) break;
+      }
       tc_fence_after();
       const uint64_t db =
           smem_desc_sw128(smem_u32(s.in.b[stage]), p.b_transposed ? 8192 : 16, 1024);
       const uint64_t da = smem_desc_sw128(smem_u32(s.in.a[stage]), 16, 1024);
 #pragma unroll
       for (int k = 0; k < 4; ++k)          // 16 elements of k each
-        mma_ss_warp(tmem, db + k * step_b, da + k * step_a, p.idesc, i > 0 || k > 0);
+        mma_ss_warp(tmem + buf * kT, db + k * step_b, da + k * step_a, p.idesc,
+                    i % kChunk > 0 || k > 0);
       tc_commit_warp(smem_u32(&s.empty[stage]));
+      if (i % kChunk == kChunk - 1 || i == count - 1) tc_commit_warp(smem_u32(&s.acc_full[buf]));
     }
-    if (ok) tc_commit_warp(smem_u32(&s.sum_full));
     tc_commit_warp(smem_u32(&s.drain));    // no MMA is in flight past this
     mbar_drain_wait(smem_u32(&s.drain), 0);
   } else {
     // ------------------------------------------------------------ sums
-    // The stages may hold the sums once every load has arrived and every MMA has read its
-    // operands, which the last commit says.
-    if (warp_wait(smem_u32(&s.sum_full), 0, guard, p.status, kSiteEpilogue)) {
+    float sum[kT];
+#pragma unroll
+    for (int c = 0; c < kT; ++c) sum[c] = 0.f;
+    bool ok = true;
+    for (int32_t turn = 0; turn * kChunk < count; ++turn) {
+      const int buf = turn & 1;
+      ok = warp_wait(smem_u32(&s.acc_full[buf]), (turn >> 1) & 1, guard, p.status,
+                     kSiteEpilogue);
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t src = tmem + ((uint32_t)(warp * 32) << 16);
+      const uint32_t src = tmem + ((uint32_t)(warp * 32) << 16) + buf * kT;
+      auto hand_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+      };
       if constexpr (kT == 16) {
         uint32_t d[16];
         tmem_ld16(src, d);
+        hand_back();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) s.sums[c][threadIdx.x] = __uint_as_float(d[c]);
+        for (int c = 0; c < 16; ++c) sum[c] += __uint_as_float(d[c]);
       } else {
 #pragma unroll
         for (int h = 0; h < kT; h += 32) {
           uint32_t d[32];
           tmem_ld32(src + h, d);
           tmem_wait_ld(d);
+          if (h + 32 == kT) hand_back();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) s.sums[h + c][threadIdx.x] = __uint_as_float(d[c]);
+          for (int c = 0; c < 32; ++c) sum[h + c] += __uint_as_float(d[c]);
         }
       }
+    }
+    // The stages may hold the sums now: the last commit says that every MMA has read its
+    // operands, and every load has arrived.
+    if (ok) {
+#pragma unroll
+      for (int c = 0; c < kT; ++c) s.sums[c][threadIdx.x] = sum[c];
     }
   }
   tc_fence_before();

@@ -39,6 +39,22 @@ constexpr uint32_t kOperandBytes = kRows * 128;          // 16 KiB
 constexpr uint32_t kPairBytes = 4 * kOperandBytes;       // both CTAs' a and b of one block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBoxBytes = 32 * 128;                 // 32 rows of 128 bytes
+// How rows of out, residual and pre are moved: boxes by TMA or, where rows start anywhere,
+// element by element.
+enum Out { kOutBf16 = 0, kOutFp32 = 1, kOutBf16Anywhere = 2, kOutFp32Anywhere = 3 };
+constexpr bool is_fp32(int out) { return out & 1; }
+constexpr bool by_boxes(int out) { return out < 2; }
+
+constexpr uint32_t kRegsLaunch = 168;
+constexpr uint32_t kRegsLow = 40, kRegsHigh = 232;
+static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
+              "register split exceeds the launch allocation");
+// Blocks of k that one accumulator sums: all of them for results rounded to bf16; for fp32
+// results a few, whose sums are then added in fp32 registers. The tensor cores cut the sum
+// off after every 16 products (1.7e-8 of it a time, always towards zero, measured), which a
+// chain of 11500 products turned into 1.2e-5 of the result; this way it stays at 3e-7.
+constexpr int32_t kChunk = 4;
+constexpr int32_t chunk_of(int out) { return is_fp32(out) ? kChunk : 0x7fffffff; }
 constexpr int kMaxPairs = 80;
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 
@@ -75,10 +91,6 @@ struct Params {
   DeviceStatus* status;
   uint64_t wait_limit_ns;
 };
-
-// How rows of out, residual and pre are moved: bf16 or fp32 boxes by TMA, or, where rows
-// start anywhere, either type element by element.
-enum Out { kOutBf16 = 0, kOutFp32 = 1, kOutAnywhere = 2 };
 
 struct Maps {
   CUtensorMap a, b, out, residual, pre, pre_up;
@@ -192,7 +204,7 @@ struct Boxes {
 // 32 columns of a row, rounded, into the box's 16-byte chunks from `chunk` on.
 template <int kOut>
 __device__ __forceinline__ void put_row(uint32_t row, int chunk, const float (&x)[32]) {
-  if constexpr (kOut == kOutBf16) {
+  if constexpr (!is_fp32(kOut)) {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       store_shared_v4(row ^ ((chunk + g) << 4),
@@ -211,7 +223,7 @@ __device__ __forceinline__ void put_row(uint32_t row, int chunk, const float (&x
 // Adds the residual that lies in the box.
 template <int kOut>
 __device__ __forceinline__ void add_row(uint32_t row, int chunk, float (&x)[32]) {
-  if constexpr (kOut == kOutBf16) {
+  if constexpr (!is_fp32(kOut)) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const uint4 r = load_shared_v4(row ^ ((chunk + g) << 4));
@@ -236,6 +248,7 @@ __device__ __forceinline__ void add_row(uint32_t row, int chunk, float (&x)[32])
 
 // 32 columns of the warp's 32 rows through a box, then row by row, element by element: a
 // row's 32 columns are consecutive. `cols` of them exist.
+template <bool kFp32>
 __device__ __forceinline__ void put_anywhere(const Params& p, uint32_t box, int lane,
                                              const float (&x)[32], const void* residual,
                                              int64_t residual_ld, void* out, int64_t out_ld,
@@ -251,40 +264,38 @@ __device__ __forceinline__ void put_anywhere(const Params& p, uint32_t box, int 
     for (int32_t r = 0; r < 8; ++r) {
       v[r] = load_shared_f32(box + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4);
       if (residual && r0 + r < rows)
-        v[r] += io_get(residual, (int64_t)(row0 + r0 + r) * residual_ld + col0 + lane,
-                       p.e.out_fp32);
+        v[r] += io_get(residual, (int64_t)(row0 + r0 + r) * residual_ld + col0 + lane, kFp32);
     }
 #pragma unroll
     for (int32_t r = 0; r < 8; ++r)
       if (r0 + r < rows)
-        io_put(out, (int64_t)(row0 + r0 + r) * out_ld + col0 + lane, p.e.out_fp32, v[r]);
+        io_put(out, (int64_t)(row0 + r0 + r) * out_ld + col0 + lane, kFp32, v[r]);
   }
 }
 
-// 32 columns of this thread's lane from tensor memory, plus their bias.
-__device__ __forceinline__ void load_z(uint32_t src, const float* bias, float (&z)[32]) {
+// 32 columns of this thread's lane from tensor memory.
+__device__ __forceinline__ void load_acc(uint32_t src, float (&z)[32]) {
   uint32_t r[32];
   tmem_ld32(src, r);
   tmem_wait_ld(r);
 #pragma unroll
+  for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void add_bias(const float* bias, float (&z)[32]) {
+#pragma unroll
   for (int g = 0; g < 8; ++g) {
     const float4 b = *reinterpret_cast<const float4*>(bias + 4 * g);
-    z[4 * g] = __uint_as_float(r[4 * g]) + b.x;
-    z[4 * g + 1] = __uint_as_float(r[4 * g + 1]) + b.y;
-    z[4 * g + 2] = __uint_as_float(r[4 * g + 2]) + b.z;
-    z[4 * g + 3] = __uint_as_float(r[4 * g + 3]) + b.w;
+    z[4 * g] += b.x;
+    z[4 * g + 1] += b.y;
+    z[4 * g + 2] += b.z;
+    z[4 * g + 3] += b.w;
   }
 }
 
 template <int kOut>
-__device__ __forceinline__ void apply_gelu(const Params& p, float (&z)[32]) {
+__device__ __forceinline__ void apply_gelu(float (&z)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if constexpr (kOut == kOutBf16)
-      z[i] = gelu<__nv_bfloat16>(z[i]);
-    else
-      z[i] = matmul_gelu(z[i], kOut == kOutFp32 || p.e.out_fp32);
-  }
+  for (int i = 0; i < 32; ++i) z[i] = is_fp32(kOut) ? gelu_fp32(z[i]) : gelu<__nv_bfloat16>(z[i]);
 }
 
 template <int kOut, bool kGeglu>
@@ -330,6 +341,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
+  if (is_fp32(kOut) && warp < 4) regs_release<kRegsLow>();
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- producer
@@ -388,56 +400,60 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
     const uint64_t desc_b0 = smem_desc_sw128(smem_u32(s.b[0]), p.b_transposed ? 8192 : 16, 1024);
     const uint32_t step_a = p.a_transposed ? 128 : 2, step_b = p.b_transposed ? 128 : 2;
     uint32_t stage = 0, parity = 0;
-    int32_t segment = 0;
+    int32_t turn = 0;                      // of the accumulators
     bool ok = true;
     Walk w;
-    for (bool more = w.start(p, pair, pairs); more && ok; more = w.next(p), ++segment) {
-      const uint32_t buf = segment & 1, d = tmem + buf * kTile;
-      ok = eager_warp_wait(smem_u32(&s.acc_empty[buf]), ((segment >> 1) & 1) ^ 1, guard, p.status,
-                           kSiteMma);
-      if (!ok) break;
-      for (int32_t block = w.first; block < w.last; ++block) {
-        ok = eager_warp_wait(smem_u32(&s.full[stage]), parity, guard, p.status, kSiteMma);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t da = desc_a0 + stage * (kOperandBytes / 16);
-        const uint64_t db = desc_b0 + stage * (kOperandBytes / 16);
+    for (bool more = w.start(p, pair, pairs); more && ok; more = w.next(p)) {
+      for (int32_t block = w.first; block < w.last && ok; ++turn) {
+        const uint32_t buf = turn & 1, d = tmem + buf * kTile;
+        const int32_t first = block;
+        const int32_t end = w.last - first < chunk_of(kOut) ? w.last : first + chunk_of(kOut);
+        ok = eager_warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
+                             kSiteMma);
+        for (; block < end && ok; ++block) {
+          ok = eager_warp_wait(smem_u32(&s.full[stage]), parity, guard, p.status, kSiteMma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = desc_a0 + stage * (kOperandBytes / 16);
+          const uint64_t db = desc_b0 + stage * (kOperandBytes / 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_pair(d, da + k * step_a, db + k * step_b, p.idesc, k > 0 || block > w.first);
-        commit_pair(smem_u32(&s.empty[stage]));
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1;
+          for (int k = 0; k < 4; ++k)
+            mma_pair(d, da + k * step_a, db + k * step_b, p.idesc, k > 0 || block > first);
+          commit_pair(smem_u32(&s.empty[stage]));
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1;
+          }
         }
+        if (ok) commit_pair(smem_u32(&s.acc_full[buf]));
       }
-      if (ok) commit_pair(smem_u32(&s.acc_full[buf]));
     }
     commit_pair(smem_u32(&s.drain));       // no MMA is in flight past this
     mbar_drain_wait(smem_u32(&s.drain), 0);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
+    if constexpr (is_fp32(kOut)) regs_claim<kRegsHigh>();
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const int32_t row_in = (int32_t)rank * kRows + quad * 32;   // this warp's rows in the tile
     const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[0]), 0);
     Boxes boxes = {smem_u32(s.box[warp - 4][0]), smem_u32(&s.residual[warp - 4][0]), 0, lane};
     constexpr int kUnits = kGeglu ? 2 : 4;                      // of 32 columns of out
-    constexpr int kPerBox = kOut == kOutBf16 ? 2 : 1;           // units in a box
-    const bool ahead = kOut != kOutAnywhere && p.e.residual && !p.e.pre;
-    int32_t segment = 0;
+    constexpr int kPerBox = is_fp32(kOut) ? 1 : 2;              // units in a box
+    const bool ahead = by_boxes(kOut) && p.e.residual && !p.e.pre;
+    int32_t turn = 0;                      // of the accumulators
+    bool begins = true;                    // the pair's first segment
     bool ok = true;
     Walk w;
-    for (bool more = w.start(p, pair, pairs); more; more = w.next(p), ++segment) {
+    for (bool more = w.start(p, pair, pairs); more; more = w.next(p), begins = false) {
       const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
       const int32_t row0 = rt * kTile + row_in;
       const int32_t col0 = ct * kOutCols + half * (kOutCols / 2);
       const bool whole = w.first == 0 && w.last == p.blocks;
       const bool stored = whole && row0 < p.e.m && col0 < p.e.n;
-      const uint32_t buf = segment & 1;
       uint32_t loading = 0;                // bit s: slot s's residual is on its way
       if (stored && ok) {
-        if (kOut != kOutAnywhere) {
+        if (by_boxes(kOut)) {
           if (lane == 0) bulk_wait_read();                      // the tile before has left
           __syncwarp();
         }
@@ -463,14 +479,48 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         if (p.e.bias) {
           const int32_t c = kGeglu ? col0 + (i & 63) : col0 + i;
           if (c < p.e.n)
-            v = io_get(p.e.bias, kGeglu && i >= 64 ? (int64_t)p.up_row + c : c, p.e.out_fp32);
+            v = io_get(p.e.bias, kGeglu && i >= 64 ? (int64_t)p.up_row + c : c, is_fp32(kOut));
         }
         bias[i] = v;
       }
       named_barrier(1 + half, 128);
       if (!ok) continue;
-      ok = eager_warp_wait(smem_u32(&s.acc_full[buf]), (segment >> 1) & 1, guard, p.status,
-                           kSiteEpilogue);
+      // Columns of accumulator `buf`: 32 u .. of this half (with geglu u = 2, 3 are up's).
+      auto columns = [&](uint32_t buf, int u) {
+        return lane_base + buf * kTile +
+               (kGeglu ? half * 64 + (u & 1) * 32 + (u >> 1) * 128 : half * 128 + u * 32);
+      };
+      auto hand_back = [&](uint32_t buf) {  // the accumulator has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty + buf * 8);
+      };
+      float sum[is_fp32(kOut) ? kRows : 1];
+      uint32_t buf = turn & 1;
+      if constexpr (is_fp32(kOut)) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
+        for (int32_t block = w.first; block < w.last; block += kChunk, ++turn) {
+          buf = turn & 1;
+          ok = eager_warp_wait(smem_u32(&s.acc_full[buf]), (turn >> 1) & 1, guard, p.status,
+                               kSiteEpilogue);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float z[32];
+            load_acc(columns(buf, u), z);
+            if (u == 3) hand_back(buf);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[32 * u + i] += z[i];
+          }
+        }
+      } else {
+        ok = eager_warp_wait(smem_u32(&s.acc_full[buf]), (turn >> 1) & 1, guard, p.status,
+                             kSiteEpilogue);
+        tc_fence_after();
+        ++turn;
+      }
       if (!ok) {
         if (lane == 0) {
 #pragma unroll
@@ -479,39 +529,35 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         }
         continue;
       }
-      tc_fence_after();
-      const uint32_t acc = lane_base + buf * kTile;
-      // Columns of the accumulator behind columns 32 u .. of this half.
-      const uint32_t z_src = acc + half * (kOutCols / 2), up_src = z_src + kTile / 2;
-      auto hand_back = [&]() {             // the accumulator has been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty + buf * 8);
+      auto load = [&](int u, float (&z)[32]) {
+        if constexpr (is_fp32(kOut)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z[i] = sum[32 * u + i];
+        } else {
+          load_acc(columns(buf, u), z);
+        }
       };
       if (!stored) {
         if (!whole) {
           float4* part =
-              reinterpret_cast<float4*>(
-                  p.parts + (2 * pair + (segment == 0 ? 0 : 1)) * kPartFloats) +
+              reinterpret_cast<float4*>(p.parts + (2 * pair + (begins ? 0 : 1)) * kPartFloats) +
               (rank * 64 + half * 32) * 128 + quad * 32 + lane;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            uint32_t r[32];
-            tmem_ld32(kGeglu && u >= 2 ? up_src + (u - 2) * 32 : z_src + u * 32, r);
-            tmem_wait_ld(r);
+            float z[32];
+            load(u, z);
 #pragma unroll
             for (int g = 0; g < 8; ++g)
               part[(8 * u + g) * 128] =
-                  make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
-                              __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+                  make_float4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]);
           }
         }
-        hand_back();
+        if (!is_fp32(kOut)) hand_back(buf);
         continue;
       }
       int box = 0;                         // of this tile: slots in turn
       auto take = [&]() {                  // waits until the box's slot has been read
-        if (kOut != kOutAnywhere && box >= 2) {
+        if (by_boxes(kOut) && box >= 2) {
           if (lane == 0) bulk_wait_read_but_one();
           __syncwarp();
         }
@@ -531,10 +577,11 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) {
             float z[32];
-            load_z((part ? up_src : z_src) + u * 32, bias + part * 64 + u * 32, z);
+            load(part * 2 + u, z);
+            add_bias(bias + part * 64 + u * 32, z);
             const int32_t col = col0 + u * 32;
-            if constexpr (kOut == kOutAnywhere) {
-              put_anywhere(p, boxes.at(0), lane, z, nullptr, 0, p.e.pre, p.e.pre_ld, row0,
+            if constexpr (!by_boxes(kOut)) {
+              put_anywhere<is_fp32(kOut)>(p, boxes.at(0), lane, z, nullptr, 0, p.e.pre, p.e.pre_ld, row0,
                            (int64_t)part * p.e.n + col, p.e.n - col);
             } else {
               if (u % kPerBox == 0) take();
@@ -549,25 +596,27 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       for (int u = 0; u < kUnits; ++u) {
         const int32_t col = col0 + u * 32;
         float y[32];
-        load_z(z_src + u * 32, bias + u * 32, y);
+        load(u, y);
+        add_bias(bias + u * 32, y);
         if constexpr (kGeglu) {
-          apply_gelu<kOut>(p, y);
+          apply_gelu<kOut>(y);
           float up[32];
-          load_z(up_src + u * 32, bias + 64 + u * 32, up);
+          load(2 + u, up);
+          add_bias(bias + 64 + u * 32, up);
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] *= up[i];
         }
-        if (u == kUnits - 1) hand_back();
+        if (!is_fp32(kOut) && u == kUnits - 1) hand_back(buf);
         if constexpr (!kGeglu) {
           if (p.e.act == PE_ACT_GELU) {
-            apply_gelu<kOut>(p, y);
+            apply_gelu<kOut>(y);
           } else if (p.e.act == PE_ACT_RELU) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
           }
         }
-        if constexpr (kOut == kOutAnywhere) {
-          put_anywhere(p, boxes.at(0), lane, y, p.e.residual, p.e.residual_ld, p.e.out,
+        if constexpr (!by_boxes(kOut)) {
+          put_anywhere<is_fp32(kOut)>(p, boxes.at(0), lane, y, p.e.residual, p.e.residual_ld, p.e.out,
                        p.e.out_ld, row0, col, p.e.n - col);
         } else {
           const int slot = box & 1;
@@ -756,9 +805,25 @@ pe_status launch_tiles(const Maps& maps, const Params& p, int32_t pairs, cudaStr
   const size_t smem = sizeof(Smem) + 1024;
   PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(smem)));
+  if (is_fp32(kOut)) {
+    cudaFuncAttributes attr;
+    PE_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
+    if (static_cast<uint32_t>(attr.numRegs) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
+      return PE_ERR_UNSUPPORTED;
+  }
   PE_TRY(launch_after_previous(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, stream,
                                maps, p));
   return p.shared_tiles ? launch_parts<kGeglu>(p, pairs, stream) : PE_OK;
+}
+
+template <bool kGeglu>
+pe_status launch_out(bool boxes, const Maps& maps, const Params& p, int32_t pairs,
+                     cudaStream_t stream) {
+  if (p.e.out_fp32)
+    return boxes ? launch_tiles<kOutFp32, kGeglu>(maps, p, pairs, stream)
+                 : launch_tiles<kOutFp32Anywhere, kGeglu>(maps, p, pairs, stream);
+  return boxes ? launch_tiles<kOutBf16, kGeglu>(maps, p, pairs, stream)
+               : launch_tiles<kOutBf16Anywhere, kGeglu>(maps, p, pairs, stream);
 }
 
 }  // namespace
@@ -805,14 +870,8 @@ pe_status matmul_tiles(const Matmul& q, bool runs, void* workspace, DeviceStatus
   p.run_blocks = (int32_t)((int64_t)p.tiles * p.blocks / pairs);
   p.run_more = (int32_t)((int64_t)p.tiles * p.blocks % pairs);
   if (!p.shared_tiles && p.tiles < pairs) pairs = p.tiles;
-  if (geglu) {
-    if (!tma) return launch_tiles<kOutAnywhere, true>(maps, p, pairs, stream);
-    return e.out_fp32 ? launch_tiles<kOutFp32, true>(maps, p, pairs, stream)
-                      : launch_tiles<kOutBf16, true>(maps, p, pairs, stream);
-  }
-  if (!tma) return launch_tiles<kOutAnywhere, false>(maps, p, pairs, stream);
-  return e.out_fp32 ? launch_tiles<kOutFp32, false>(maps, p, pairs, stream)
-                    : launch_tiles<kOutBf16, false>(maps, p, pairs, stream);
+  return geglu ? launch_out<true>(tma, maps, p, pairs, stream)
+               : launch_out<false>(tma, maps, p, pairs, stream);
 }
 
 }  // namespace pe
