@@ -27,14 +27,28 @@ __device__ __forceinline__ float normal_fast(float z, float& bell) {
   return z < 0.f ? tail : 1.f - tail;
 }
 
-// T: the type the result is rounded to. fp32 takes CUDA's own function.
+// T: the type the result is rounded to. fp32 takes CUDA's own functions. Infinite z give the
+// limits, 0 and infinity, a slope of 0 and 1.
+template <typename T>
+__device__ __forceinline__ float normal(float z, float& bell) {
+  if constexpr (sizeof(T) == 4) {
+    bell = expf(-0.5f * z * z);
+    return normcdff(z);
+  } else {
+    return normal_fast(z, bell);
+  }
+}
+__device__ __forceinline__ float times_normal(float z, float phi) {
+  return fmaxf(z, -3.402823466e38f) * phi;     // phi carries a NaN
+}
+
 template <typename T>
 __device__ __forceinline__ float gelu(float z) {
   if constexpr (sizeof(T) == 4) {
-    return z * normcdff(z);
+    return times_normal(z, normcdff(z));
   } else {
     float bell;
-    return z * normal_fast(z, bell);
+    return times_normal(z, normal_fast(z, bell));
   }
 }
 
@@ -42,15 +56,10 @@ __device__ __forceinline__ float gelu(float z) {
 template <typename T>
 __device__ __forceinline__ float gelu_slope(float z, float& value) {
   constexpr float kDensity = 0.3989422804014327f;     // 1 / sqrt(2 pi)
-  float phi, bell;
-  if constexpr (sizeof(T) == 4) {
-    phi = normcdff(z);
-    bell = expf(-0.5f * z * z);
-  } else {
-    phi = normal_fast(z, bell);
-  }
-  value = z * phi;
-  return fmaf(z * kDensity, bell, phi);
+  float bell;
+  const float phi = normal<T>(z, bell);
+  value = times_normal(z, phi);
+  return fmaf(fminf(fmaxf(z, -64.f), 64.f) * kDensity, bell, phi);
 }
 
 inline bool activation_ok(int act) { return act >= PE_ACT_NONE && act <= PE_ACT_GEGLU; }

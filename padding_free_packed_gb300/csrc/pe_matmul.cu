@@ -121,15 +121,35 @@ pe_status split(Matmul& p, void* parts, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- the choice
 // Estimated microseconds of every way.
+int64_t tile_count(int64_t m, int64_t n) { return ceil_div(m, 256) * ceil_div(n, 256); }
+
 LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
                        bool a_transposed) {
   constexpr int64_t kSms = 152, kPairs = kSms / 2;
   const int64_t blocks = ceil_div(k, kMatmulBlock) * (fp32 ? kMaxMatmulTerms : 1);
-  const int64_t tiles = ceil_div(m, 256) * ceil_div(n, 256);
-  const double whole = 6 + (double)ceil_div(tiles, kPairs) * (0.28 * (double)blocks + 1);
-  const double runs = 13 + 0.045 * (double)tiles + 0.29 * (double)(tiles * blocks) / kPairs;
-  LinearPlan plan = {0, 1, tiles <= 2 * kPairs && runs < whole};
-  double best = plan.runs ? runs : whole;
+  const int64_t tiles = tile_count(m, n);
+  LinearPlan plan = {0, 1, 1, 1};
+  double best = 5 + (double)ceil_div(tiles, kPairs) * (0.3 * (double)blocks + 0.5);
+  const int64_t doubles = ceil_div(m, 512) * ceil_div(n, 256);
+  const double two = 5 + (double)ceil_div(doubles, kMatmulClusters) * (0.26 * (double)blocks + 0.5);
+  if (two < best) {
+    best = two;
+    plan.pairs = 2;
+  }
+  // Slices of eight blocks at least; a part is written and read once.
+  for (int32_t slices = 2; slices <= 16 && slices * 8 <= blocks && tiles <= 4 * kPairs; ++slices) {
+    const int64_t units = tiles * slices;
+    const double share = units < kPairs ? (double)units / kPairs : 1.0;
+    const double block = share < 0.85 ? 0.26 : 0.3;
+    const double t = 9 + (double)ceil_div(units, kPairs) *
+                             (block * (double)ceil_div(blocks, slices) + 0.5) +
+                     0.1 * (double)units;
+    if (t < best) {
+      best = t;
+      plan.pairs = 1;
+      plan.slices = slices;
+    }
+  }
   constexpr int32_t kRows[3] = {16, 32, 64};
   constexpr double kFixed[3] = {3.0, 3.2, 3.6}, kBlock[3] = {0.2, 0.2, 0.22};
   for (int i = a_transposed ? 2 : 0; i < 3; ++i) {
@@ -142,7 +162,7 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
                      1.2 * shared + (split > 1 ? 0.8 : 0);
     if (t < best) {
       best = t;
-      plan = {kRows[i], (int32_t)split, false};
+      plan = {kRows[i], (int32_t)split, 1, 1};
     }
   }
   return plan;
@@ -168,7 +188,7 @@ extern "C" size_t pe_matmul_workspace_size(pe_dtype dtype, int a_transposed, int
   const bool fp32 = dtype == PE_FP32;
   const LinearPlan plan =
       linear_plan(m, n, k, fp32, activation == PE_ACT_GEGLU, a_transposed != 0);
-  return (plan.runs ? matmul_tiles_workspace() : 0) +
+  return matmul_tiles_workspace(tile_count(m, n), plan.slices) +
          (fp32 ? (size_t)split_bytes(m, n, k, a_transposed != 0, b_transposed != 0) : 0);
 }
 
@@ -235,8 +255,10 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
   DeviceStatus* status = nullptr;
   PE_TRY(matmul_status_word(&status));
   if (fp32)
-    PE_TRY(split(p, static_cast<char*>(workspace) + (plan.runs ? matmul_tiles_workspace() : 0),
+    PE_TRY(split(p,
+                 static_cast<char*>(workspace) +
+                     matmul_tiles_workspace(tile_count(m, n), plan.slices),
                  stream));
   if (plan.rows) return matmul_narrow(p, plan.rows, plan.split, status, stream);
-  return matmul_tiles(p, plan.runs, workspace, status, stream);
+  return matmul_tiles(p, plan.pairs, plan.slices, workspace, status, stream);
 }

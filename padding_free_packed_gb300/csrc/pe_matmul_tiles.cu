@@ -7,11 +7,22 @@
 // epilogue of a tile runs under the next tile's MMAs. An operand stored with k as its rows is
 // loaded in boxes of 64 columns by 64 rows and read by the MMA as it lies there.
 //
-//   warp 0       TMA producer (both CTAs), a ring of kStages blocks
-//   warp 1       MMA issue (first CTA of the pair)
+// With every SM loading, L2 gives each 55 bytes a cycle (measured: a block of 64 takes 600
+// cycles, 512 without loads, 519 with a's alone), 32 KiB of which would be due in the 512
+// cycles of a block's MMAs. So two pairs with neighbouring row tiles form a cluster and share
+// their rows of b: each CTA loads half of what it needs of b and multicasts it to the CTA
+// that needs the same, 24 KiB a block.
+//
+//   warps 0, 2   loads of a and of b (every CTA), a ring of kStages blocks
+//   warp 1       MMA issue (first CTA of each pair)
 //   warps 4-11   epilogue; warps 4-7 the tile's left half, 8-11 its right half: bias, z into
 //                pre, activation, residual (loaded by TMA into the box that the result then
 //                leaves from), rounding, TMA stores of 32 rows x 128 bytes
+//
+// The loads and the MMAs are issued by one thread each, whose instructions take 10 to 20
+// cycles apiece while the epilogue's warps keep the schedulers busy. Their loops over blocks
+// are kept short for that reason, and a and b have a warp each: one thread for both took 530
+// cycles a block without an epilogue, 770 beside geglu's and 960 beside gelu's.
 //
 // With geglu the tile is 128 columns of out: the first CTA loads their gate rows of b, the
 // second their up rows, so that a thread finds both in its row of tensor memory.
@@ -19,10 +30,12 @@
 // fp32 operands come as three bf16 parts each, and six products of parts, the smallest
 // first, are summed in the same accumulator, as six times as many blocks of k.
 //
-// Work: whole tiles in turn, or, where few tiles have long sums, equal runs of consecutive
-// blocks of k (a run may start and end inside a tile); a tile that several pairs share is
-// then summed from their fp32 parts, in the order of k, by a second kernel, which also does
-// the epilogue.
+// Work: whole tiles in turn, or, where few tiles have long sums, slices of k, all tiles of a
+// slice before the next (so that the pairs read the same blocks of k at about the same
+// time); the slices' fp32 sums are then added, in the order of k, by a second kernel, which
+// also does the epilogue.
+#include <type_traits>
+
 #include "pe_matmul.cuh"
 
 namespace pe {
@@ -33,7 +46,7 @@ using namespace sm103;
 
 constexpr int kTile = 256;
 constexpr int kRows = 128;                               // rows of a (and of b) per CTA
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kThreads = 384;
 constexpr uint32_t kOperandBytes = kRows * 128;          // 16 KiB
 constexpr uint32_t kPairBytes = 4 * kOperandBytes;       // both CTAs' a and b of one block
@@ -55,24 +68,42 @@ static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
 // chain of 11500 products turned into 1.2e-5 of the result; this way it stays at 3e-7.
 constexpr int32_t kChunk = 4;
 constexpr int32_t chunk_of(int out) { return is_fp32(out) ? kChunk : 0x7fffffff; }
-constexpr int kMaxPairs = 80;
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 
 struct alignas(1024) Smem {
   uint8_t a[kStages][kOperandBytes];
   uint8_t b[kStages][kOperandBytes];
-  alignas(1024) uint8_t box[8][2][kBoxBytes];  // of each epilogue warp
+  alignas(1024) uint8_t box[8][kBoxBytes];     // of each epilogue warp
   alignas(16) float bias[2][kRows];            // of each half of the tile
   uint64_t full[kStages], empty[kStages];      // full: the first CTA's serve the pair
   uint64_t acc_full[2], acc_empty[2];          // acc_empty: likewise
-  uint64_t residual[8][2];                     // a box's residual has arrived
+  uint64_t residual[8];                        // the box's residual has arrived
   uint64_t drain;
-  int32_t issued[2];                           // blocks each CTA's producer loaded (first CTA)
-  int32_t aborted[2];
+  int32_t loaded[2];                           // blocks of a, of b that this CTA loaded
+  int32_t issued[2][4];                        // the same of every CTA of the cluster, and
+  int32_t aborted[4];                          // whether one of its waits gave up
   uint32_t tmem_base;
   WaitGuard guard;
 };
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory exceeds the per-CTA limit");
+
+// Quotients by a number known at launch, of 0 <= x < 2^31: with 2^(l-1) < d <= 2^l and m =
+// floor(2^(31+l) / d) + 1, x / d is the upper word of x m shifted right by l - 1 (T.
+// Granlund and P. Montgomery, Division by invariant integers using multiplication, 1994).
+// The warps that feed the tensor cores divide between two tiles.
+struct Divisor {
+  uint32_t d, m;
+  int32_t shift;             // -1: d = 1
+
+  __host__ static Divisor of(int32_t d) {
+    int32_t l = 0;
+    while ((1ll << l) < d) ++l;
+    return {(uint32_t)d, d == 1 ? 0u : (uint32_t)((1ull << (31 + l)) / (uint32_t)d + 1), l - 1};
+  }
+  __device__ int32_t quotient(int32_t x) const {
+    return shift < 0 ? x : (int32_t)(__umulhi((uint32_t)x, m) >> shift);
+  }
+};
 
 struct Params {
   MatmulEpilogue e;
@@ -81,13 +112,15 @@ struct Params {
   int32_t terms;
   int32_t a_transposed, b_transposed;
   int32_t up_row;            // geglu: b's first up row
+  int32_t row_units;         // rows of tiles, a cluster's pairs together
   int32_t col_tiles;
-  int32_t tiles;
-  int32_t shared_tiles;      // 1: runs of blocks, partial tiles through `parts`
-  int32_t run_blocks;        // blocks of every pair's run, and
-  int32_t run_more;          // how many pairs get one more
+  int32_t tiles;             // row_units * col_tiles
+  int32_t slices;            // of k; more than one: sums through `parts`
+  int32_t slice_blocks;      // blocks of a slice; the first slices
+  int32_t slice_more;        // have one more
+  Divisor by_band, by_tiles; // quotients by a band's tiles, by all tiles
   uint32_t idesc;
-  float* parts;              // [2 * pairs][2 CTAs][2 halves][32 column groups][128 rows] float4
+  float* parts;              // [slices][tiles][2 CTAs][2 halves][32 column groups][128 rows] float4
   DeviceStatus* status;
   uint64_t wait_limit_ns;
 };
@@ -108,96 +141,106 @@ __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Tile load into this CTA, counted on a barrier of the pair's first CTA.
+// The loads and MMAs below are executed by a whole warp with the same operands, and one lane
+// issues: a warp that runs together keeps them in uniform registers, where these instructions
+// take their operands from; in a branch of one thread each of them first costs several moves.
+
+// Box load into this CTA, counted on a barrier of the pair's first CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                               int32_t x, int32_t y, int32_t z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Both are executed by a whole warp with the same operands; one lane issues.
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync r|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrives once on this barrier in both CTAs when the MMAs issued so far complete.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
+// The same into the CTAs of `mask`, at the same place in each, counted on the barrier of each
+// one's pair.
+__device__ __forceinline__ void tma_load_shared(uint32_t dst, const CUtensorMap* map,
+                                                uint32_t bar, int32_t x, int32_t y, int32_t z,
+                                                uint16_t mask) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}" ::"r"(bar),
-      "h"((uint16_t)3)
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(mask)
       : "memory");
 }
-__device__ __forceinline__ void bulk_wait_read_but_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+// The same box into the L2 cache only.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int32_t x, int32_t y,
+                                             int32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n\t}" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Announces a block's bytes on its barrier.
+__device__ __forceinline__ void expect_pair(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t.reg .b64 st;\n\telect.sync r|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(kPairBytes)
+      : "memory");
+}
+// The four MMAs of a block: operands at the descriptors' low words (the high
+// ones are the same for all), kA and kB units of 16 bytes from 16 elements of k to the next.
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_low, uint32_t a_high,
+                                          uint32_t b_low, uint32_t b_high, uint32_t idesc,
+                                          uint32_t accumulate) {
+#define PE_MMA "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, "
+#define PE_NEXT(i, j)                                                                \
+  "add.u32 a, %1, %" #i ";\n\tadd.u32 b, %3, %" #j ";\n\tmov.b64 da, {a, %2};\n\t" \
+  "mov.b64 db, {b, %4};\n\t"
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a, b, r;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync r|e, 0xffffffff;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t" PE_MMA "p;\n\t" PE_NEXT(7, 8)
+          PE_MMA "t;\n\t" PE_NEXT(9, 10) PE_MMA "t;\n\t" PE_NEXT(11, 12) PE_MMA "t;\n\t}" ::"r"(
+              d_tmem),
+      "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate), "n"(kA),
+      "n"(kB), "n"(2 * kA), "n"(2 * kB), "n"(3 * kA), "n"(3 * kB)
+      : "memory");
+#undef PE_MMA
+#undef PE_NEXT
+}
+// Arrives once on this barrier in the CTAs of `mask` when the MMAs issued so far complete.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+// Tiles are dealt in bands of four rows, down the rows first, so that the clusters at work
+// share operands in L2 both ways.
+constexpr int32_t kBand = 4;
+__device__ __forceinline__ void place(const Params& p, int32_t tile, int32_t& row, int32_t& col) {
+  const int32_t band = p.by_band.quotient(tile), rest = tile - band * (int32_t)p.by_band.d;
+  const int32_t left = p.row_units - band * kBand;
+  col = left >= kBand ? rest / kBand : left == 1 ? rest : left == 2 ? rest / 2 : rest / 3;
+  row = band * kBand + rest - col * (left < kBand ? left : kBand);
 }
 
-// First block of pair `q`'s run: the blocks are dealt evenly, the first pairs get one
-// more each.
-__device__ __forceinline__ int32_t run_start(const Params& p, int32_t q) {
-  return p.run_blocks * q + (q < p.run_more ? q : p.run_more);
-}
-
-// The work of a pair as segments (a tile and a run of its blocks of k), in order.
+// The work of a cluster: units, of a tile and a slice of its blocks of k, slice by slice.
 struct Walk {
-  int32_t tile, first, last;      // last: one past the segment's last block
-  int32_t stride;
-  int32_t left;                   // blocks after this segment (shared tiles)
+  int32_t unit, tile;
+  int32_t first, last;            // last: one past the unit's last block
 
-  // The pair's first segment; false when it has none.
-  __device__ bool start(const Params& p, int32_t pair, int32_t pairs) {
-    if (p.shared_tiles) {
-      const int32_t lo = run_start(p, pair), hi = run_start(p, pair + 1);
-      if (lo >= hi) return false;
-      tile = lo / p.blocks;
-      first = lo - tile * p.blocks;
-      const int32_t room = hi - lo;
-      last = room < p.blocks - first ? first + room : p.blocks;
-      left = room - (last - first);
-      return true;
-    }
-    stride = pairs;
-    tile = pair;
+  __device__ bool at(const Params& p, int32_t u) {
+    unit = tile = u;
     first = 0;
     last = p.blocks;
-    return tile < p.tiles;
-  }
-  __device__ bool next(const Params& p) {
-    first = 0;
-    if (p.shared_tiles) {
-      if (left <= 0) return false;
-      ++tile;
-      last = left < p.blocks ? left : p.blocks;
-      left -= last;
-      return true;
+    if (p.slices > 1) {
+      const int32_t slice = p.by_tiles.quotient(u);
+      tile = u - slice * p.tiles;
+      first = slice * p.slice_blocks + (slice < p.slice_more ? slice : p.slice_more);
+      last = first + p.slice_blocks + (slice < p.slice_more ? 1 : 0);
     }
-    tile += stride;
-    return tile < p.tiles;
-  }
-};
-
-// An epilogue warp's boxes: two in turn. A box is filled by the warp's threads (or first by
-// a load of the residual) and leaves by a TMA store of its own bulk group.
-struct Boxes {
-  uint32_t base;                  // of this warp's two boxes
-  uint32_t bars;                  // their barriers
-  uint32_t phases;                // bit s: parity of slot s's next arrival
-  int lane;
-
-  __device__ uint32_t at(int slot) const { return base + slot * kBoxBytes; }
-  // This thread's row of a box.
-  __device__ uint32_t row(int slot) const { return at(slot) + lane * 128 + ((lane & 7) << 4); }
-  __device__ void load(int slot, const CUtensorMap* map, int32_t x, int32_t y) const {
-    mbar_arrive_expect_tx(bars + slot * 8, kBoxBytes);
-    tma_load_2d(at(slot), map, bars + slot * 8, x, y);
+    return u < p.tiles * p.slices;
   }
 };
 
@@ -281,45 +324,52 @@ __device__ __forceinline__ void load_acc(uint32_t src, float (&z)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(r[i]);
 }
+// Two columns an instruction, here and in gelu: every instruction of the epilogue takes an
+// issue slot from the warps that feed the tensor cores.
 __device__ __forceinline__ void add_bias(const float* bias, float (&z)[32]) {
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
     const float4 b = *reinterpret_cast<const float4*>(bias + 4 * g);
-    z[4 * g] += b.x;
-    z[4 * g + 1] += b.y;
-    z[4 * g + 2] += b.z;
-    z[4 * g + 3] += b.w;
+    f2_split(fadd2(f2(z[4 * g], z[4 * g + 1]), f2(b.x, b.y)), z[4 * g], z[4 * g + 1]);
+    f2_split(fadd2(f2(z[4 * g + 2], z[4 * g + 3]), f2(b.z, b.w)), z[4 * g + 2], z[4 * g + 3]);
   }
 }
 
 template <int kOut>
 __device__ __forceinline__ void apply_gelu(float (&z)[32]) {
+  if constexpr (is_fp32(kOut)) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) z[i] = is_fp32(kOut) ? gelu_fp32(z[i]) : gelu<__nv_bfloat16>(z[i]);
+    for (int i = 0; i < 32; ++i) z[i] = gelu_fp32(z[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) gelu_pair(z[i], z[i + 1]);
+  }
 }
 
-template <int kOut, bool kGeglu>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int kOut, bool kGeglu, int kPairs>
+__global__ void __launch_bounds__(kThreads, 1)
 matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int32_t cta = (int32_t)cluster_rank();            // in the cluster
+  const int32_t rank = cta & 1, pair = cta >> 1;          // in the pair; of the cluster's pairs
+  const int32_t cluster = blockIdx.x / (2 * kPairs), clusters = gridDim.x / (2 * kPairs);
+  constexpr uint16_t kAll = (1 << 2 * kPairs) - 1;
   volatile WaitGuard* guard = &s.guard;
   constexpr int32_t kOutCols = kGeglu ? kTile / 2 : kTile;   // of a tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), kPairs);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.acc_full[i]), 1);
       mbar_init(smem_u32(&s.acc_empty[i]), 16);
     }
-    for (int i = 0; i < 16; ++i) mbar_init(smem_u32(&s.residual[i >> 1][i & 1]), 1);
-    mbar_init(smem_u32(&s.drain), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&s.residual[i]), 1);
+    mbar_init(smem_u32(&s.drain), kPairs);
     s.guard.abort = 0;
     s.guard.limit_ns = p.wait_limit_ns;
     fence_mbarrier_init();
@@ -337,45 +387,67 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
   tc_fence_before();
   __syncthreads();
   griddep_wait();                          // what the kernel before this one wrote is read below
-  cluster_sync();                          // barriers of both CTAs exist before any arrival
+  cluster_sync();                          // every CTA's barriers exist before any arrival
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
   if (is_fp32(kOut) && warp < 4) regs_release<kRegsLow>();
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- producer
-      const uint32_t full0 = peer_address(smem_u32(&s.full[0]), 0);
-      int32_t issued = 0, stage = 0;
-      uint32_t parity = 1;
+  if (warp == 0 || warp == 2) {
+    // ---------------------------------------------------------- loads
+    auto load = [&](auto of_b, auto is_transposed) {
+      constexpr bool kB = decltype(of_b)::value, kTransposed = decltype(is_transposed)::value;
+      const CUtensorMap* map = kB ? &maps.b : &maps.a;
+      const uint32_t to0 = smem_u32(kB ? s.b[0] : s.a[0]) +
+                           (kB && kPairs == 2 ? pair * (kOperandBytes / 2) : 0);
+      const uint32_t full0 = peer_address(smem_u32(&s.full[0]), (uint32_t)(cta & ~1));
+      const uint32_t full_own = smem_u32(&s.full[0]), empty0 = smem_u32(&s.empty[0]);
+      // This CTA's place in a tile's rows of the operand, and the CTAs that need the same
+      // rows of b.
+      const int32_t in_tile = kB && kPairs == 2 ? pair * 64 : 0;
+      const uint16_t sharers = (uint16_t)(5 << rank);
+      const int32_t x_end = p.term_blocks * kMatmulBlock;
+      int32_t issued = 0;
+      uint32_t stage = 0, parity = 1;
       bool ok = true;
       Walk w;
-      for (bool more = w.start(p, pair, pairs); more && ok; more = w.next(p)) {
-        const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
-        const int32_t row = rt * kTile + (int32_t)rank * kRows;
-        const int32_t col = kGeglu ? ct * kOutCols + (rank ? p.up_row : 0)
-                                   : ct * kTile + (int32_t)rank * kRows;
-        int32_t term = w.first / p.term_blocks;
+      int32_t next_row, next_col;                      // of tiles
+      bool more = w.at(p, cluster);
+      place(p, w.tile, next_row, next_col);
+      for (; more && ok; more = w.at(p, w.unit + clusters)) {
+        const int32_t at = in_tile + (!kB      ? (next_row * kPairs + pair) * kTile + rank * kRows
+                                      : kGeglu ? next_col * kOutCols + (rank ? p.up_row : 0)
+                                               : next_col * kTile + rank * kRows);
+        int32_t term = p.terms == 1 ? 0 : w.first / p.term_blocks;
         int32_t x = (w.first - term * p.term_blocks) * kMatmulBlock;
-        const int32_t x_end = p.term_blocks * kMatmulBlock;
-        for (int32_t block = w.first; block < w.last; ++block) {
-          ok = eager_wait(smem_u32(&s.empty[stage]), parity, guard, p.status, kSiteProducer);
+        int32_t z = kB ? term_b(term, p.terms) : term_a(term, p.terms);
+        // The rows of a that this CTA's next tile reads, which the clusters on its row of
+        // tiles share out, go to L2 under this tile: from HBM a block takes longer than
+        // the ring is deep (169151 x 1024 x 1024 222 us without, 217 with; with residual
+        // 253, 243).
+        Walk next;
+        const bool ahead = next.at(p, w.unit + clusters) && p.slices == 1;
+        place(p, next.tile, next_row, next_col);
+        const int32_t ahead_at = (next_row * kPairs + pair) * kTile + rank * kRows;
+        int32_t until = !kB && !kTransposed && ahead ? next_col : 0x7fffffff;
+        for (int32_t left = w.last - w.first; left > 0; --left) {
+          ok = eager_warp_wait(empty0 + stage * 8, parity, guard, p.status, kSiteProducer);
           if (!ok) break;
-          const uint32_t bar = full0 + stage * 8;
-          const uint32_t sa = smem_u32(s.a[stage]), sb = smem_u32(s.b[stage]);
-          const int32_t pa = term_a(term, p.terms), pb = term_b(term, p.terms);
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), kPairBytes);
-          if (p.a_transposed) {
-            tma_load_pair(sa, &maps.a, bar, row, x, pa);
-            tma_load_pair(sa + kOperandBytes / 2, &maps.a, bar, row + 64, x, pa);
+          const uint32_t bar = full0 + stage * 8, to = to0 + stage * kOperandBytes;
+          if (!kB && rank == 0) expect_pair(full_own + stage * 8);
+          if constexpr (kB && kPairs == 2) {           // one of two boxes, for two pairs
+            tma_load_shared(to, map, bar, kTransposed ? at : x, kTransposed ? x : at, z,
+                            sharers);
+          } else if constexpr (kTransposed) {          // 64 columns by 64 rows a box
+            tma_load_pair(to, map, bar, at, x, z);
+            tma_load_pair(to + kOperandBytes / 2, map, bar, at + 64, x, z);
           } else {
-            tma_load_pair(sa, &maps.a, bar, x, row, pa);
+            tma_load_pair(to, map, bar, x, at, z);
           }
-          if (p.b_transposed) {
-            tma_load_pair(sb, &maps.b, bar, col, x, pb);
-            tma_load_pair(sb + kOperandBytes / 2, &maps.b, bar, col + 64, x, pb);
-          } else {
-            tma_load_pair(sb, &maps.b, bar, x, col, pb);
+          if constexpr (!kB && !kTransposed) {
+            if (until-- == 0) {
+              tma_prefetch(map, x, ahead_at, z);
+              until = p.col_tiles - 1;
+            }
           }
           ++issued;
           if (++stage == kStages) {
@@ -386,87 +458,118 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
           if (x == x_end) {
             x = 0;
             ++term;
+            z = kB ? term_b(term, p.terms) : term_a(term, p.terms);
           }
         }
       }
-      store_cluster_i32(peer_address(smem_u32(&s.issued[rank]), 0), issued);
+      if (lane == 0) s.loaded[kB] = issued;
+    };
+    if (warp == 0) {
+      if (p.a_transposed)
+        load(std::false_type(), std::true_type());
+      else
+        load(std::false_type(), std::false_type());
+    } else {
+      if (p.b_transposed)
+        load(std::true_type(), std::true_type());
+      else
+        load(std::true_type(), std::false_type());
     }
-    __syncwarp();
   } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------------------ MMA issue
-    // 16 elements of k: 32 bytes along rows of k, or 16 rows of 128 bytes; an operand's next
-    // 64 columns, where k runs along its rows, are the stage's second half.
-    const uint64_t desc_a0 = smem_desc_sw128(smem_u32(s.a[0]), p.a_transposed ? 8192 : 16, 1024);
-    const uint64_t desc_b0 = smem_desc_sw128(smem_u32(s.b[0]), p.b_transposed ? 8192 : 16, 1024);
-    const uint32_t step_a = p.a_transposed ? 128 : 2, step_b = p.b_transposed ? 128 : 2;
-    uint32_t stage = 0, parity = 0;
-    int32_t turn = 0;                      // of the accumulators
-    bool ok = true;
-    Walk w;
-    for (bool more = w.start(p, pair, pairs); more && ok; more = w.next(p)) {
-      for (int32_t block = w.first; block < w.last && ok; ++turn) {
-        const uint32_t buf = turn & 1, d = tmem + buf * kTile;
-        const int32_t first = block;
-        const int32_t end = w.last - first < chunk_of(kOut) ? w.last : first + chunk_of(kOut);
-        ok = eager_warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
-                             kSiteMma);
-        for (; block < end && ok; ++block) {
-          ok = eager_warp_wait(smem_u32(&s.full[stage]), parity, guard, p.status, kSiteMma);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t da = desc_a0 + stage * (kOperandBytes / 16);
-          const uint64_t db = desc_b0 + stage * (kOperandBytes / 16);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_pair(d, da + k * step_a, db + k * step_b, p.idesc, k > 0 || block > first);
-          commit_pair(smem_u32(&s.empty[stage]));
-          if (++stage == kStages) {
-            stage = 0;
-            parity ^= 1;
+    // ---------------------------------------------------------- MMA issue
+    // 16 elements of k: 32 bytes along rows of k, or 16 rows of 128 bytes; an operand's
+    // next 64 columns, where k runs along its rows, are the stage's second half.
+    auto issue = [&](auto a_is_transposed, auto b_is_transposed) {
+      constexpr bool kAT = decltype(a_is_transposed)::value;
+      constexpr bool kBT = decltype(b_is_transposed)::value;
+      const uint64_t desc_a = smem_desc_sw128(smem_u32(s.a[0]), kAT ? 8192 : 16, 1024);
+      const uint64_t desc_b = smem_desc_sw128(smem_u32(s.b[0]), kBT ? 8192 : 16, 1024);
+      const uint16_t both = (uint16_t)(3 << (cta & ~1));   // this pair's CTAs
+      const uint32_t full0 = smem_u32(&s.full[0]), empty0 = smem_u32(&s.empty[0]);
+      uint32_t stage = 0, parity = 0;
+      int32_t turn = 0;                  // of the accumulators
+      bool ok = true;
+      Walk w;
+      for (bool more = w.at(p, cluster); more && ok; more = w.at(p, w.unit + clusters)) {
+        for (int32_t block = w.first; block < w.last && ok; ++turn) {
+          const uint32_t buf = turn & 1, d = tmem + buf * kTile;
+          const int32_t end = w.last - block < chunk_of(kOut) ? w.last : block + chunk_of(kOut);
+          uint32_t accumulate = 0;
+          ok = eager_warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
+                          kSiteMma);
+          for (; block < end && ok; ++block) {
+            ok = eager_warp_wait(full0 + stage * 8, parity, guard, p.status, kSiteMma);
+            if (!ok) break;
+            tc_fence_after();
+            mma_block<kAT ? 128 : 2, kBT ? 128 : 2>(
+                d, (uint32_t)desc_a + stage * (kOperandBytes / 16), (uint32_t)(desc_a >> 32),
+                (uint32_t)desc_b + stage * (kOperandBytes / 16), (uint32_t)(desc_b >> 32),
+                p.idesc, accumulate);
+            commit_pair(empty0 + stage * 8, kAll);
+            accumulate = 1;
+            if (++stage == kStages) {
+              stage = 0;
+              parity ^= 1;
+            }
           }
+          if (ok) commit_pair(smem_u32(&s.acc_full[buf]), both);
         }
-        if (ok) commit_pair(smem_u32(&s.acc_full[buf]));
       }
+    };
+    if (p.a_transposed) {
+      if (p.b_transposed)
+        issue(std::true_type(), std::true_type());
+      else
+        issue(std::true_type(), std::false_type());
+    } else {
+      if (p.b_transposed)
+        issue(std::false_type(), std::true_type());
+      else
+        issue(std::false_type(), std::false_type());
     }
-    commit_pair(smem_u32(&s.drain));       // no MMA is in flight past this
-    mbar_drain_wait(smem_u32(&s.drain), 0);
+    commit_pair(smem_u32(&s.drain), kAll);   // waited for below: no MMA in flight past that
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     if constexpr (is_fp32(kOut)) regs_claim<kRegsHigh>();
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const int32_t row_in = (int32_t)rank * kRows + quad * 32;   // this warp's rows in the tile
-    const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[0]), 0);
-    Boxes boxes = {smem_u32(s.box[warp - 4][0]), smem_u32(&s.residual[warp - 4][0]), 0, lane};
+    const int32_t row_in = rank * kRows + quad * 32;            // this warp's rows in the tile
+    const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[0]), (uint32_t)(cta & ~1));
+    // This warp's box, this thread's row of it, and the barrier that counts its residuals.
+    const uint32_t box = smem_u32(s.box[warp - 4]);
+    const uint32_t box_row = box + lane * 128 + ((lane & 7) << 4);
+    const uint32_t box_bar = smem_u32(&s.residual[warp - 4]);
+    uint32_t box_parity = 0;
     constexpr int kUnits = kGeglu ? 2 : 4;                      // of 32 columns of out
     constexpr int kPerBox = is_fp32(kOut) ? 1 : 2;              // units in a box
     const bool ahead = by_boxes(kOut) && p.e.residual && !p.e.pre;
     int32_t turn = 0;                      // of the accumulators
-    bool begins = true;                    // the pair's first segment
     bool ok = true;
     Walk w;
-    for (bool more = w.start(p, pair, pairs); more; more = w.next(p), begins = false) {
-      const int32_t rt = w.tile / p.col_tiles, ct = w.tile - rt * p.col_tiles;
-      const int32_t row0 = rt * kTile + row_in;
-      const int32_t col0 = ct * kOutCols + half * (kOutCols / 2);
-      const bool whole = w.first == 0 && w.last == p.blocks;
+    for (bool more = w.at(p, cluster); more; more = w.at(p, w.unit + clusters)) {
+      int32_t tile_row, tile_col;
+      place(p, w.tile, tile_row, tile_col);
+      const int32_t row0 = (tile_row * kPairs + pair) * kTile + row_in;
+      const int32_t col0 = tile_col * kOutCols + half * (kOutCols / 2);
+      const bool whole = kPairs == 2 || p.slices == 1;
       const bool stored = whole && row0 < p.e.m && col0 < p.e.n;
-      uint32_t loading = 0;                // bit s: slot s's residual is on its way
-      if (stored && ok) {
+      bool loading = false;                // the box's residual is on its way
+      auto load_residual = [&](int32_t col) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(box_bar, kBoxBytes);
+          tma_load_2d(box, &maps.residual, box_bar, col, row0);
+        }
+        loading = true;
+      };
+      auto take = [&]() {                  // the box that left before has been read
         if (by_boxes(kOut)) {
-          if (lane == 0) bulk_wait_read();                      // the tile before has left
+          if (lane == 0) bulk_wait_read();
           __syncwarp();
         }
-        if (ahead) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int32_t col = col0 + b * kPerBox * 32;
-            if (b * kPerBox < kUnits && col < p.e.n) {
-              if (lane == 0) boxes.load(b, &maps.residual, col, row0);
-              loading |= 1u << b;
-            }
-          }
-        }
+      };
+      if (stored && ok && ahead) {
+        take();
+        load_residual(col0);
       }
       // The bias of this half's 128 columns of the accumulator: with geglu 64 of the gate's,
       // then 64 of the up part's. The half's warps meet here for every segment, after a wait
@@ -522,11 +625,8 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         ++turn;
       }
       if (!ok) {
-        if (lane == 0) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            if (loading >> b & 1) mbar_drain_wait(boxes.bars + b * 8, boxes.phases >> b & 1);
-        }
+        if (loading && lane == 0) mbar_drain_wait(box_bar, box_parity);
+        box_parity ^= loading ? 1u : 0u;
         continue;
       }
       auto load = [&](int u, float (&z)[32]) {
@@ -540,7 +640,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       if (!stored) {
         if (!whole) {
           float4* part =
-              reinterpret_cast<float4*>(p.parts + (2 * pair + (begins ? 0 : 1)) * kPartFloats) +
+              reinterpret_cast<float4*>(p.parts + (int64_t)w.unit * kPartFloats) +
               (rank * 64 + half * 32) * 128 + quad * 32 + lane;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -555,44 +655,38 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         if (!is_fp32(kOut)) hand_back(buf);
         continue;
       }
-      int box = 0;                         // of this tile: slots in turn
-      auto take = [&]() {                  // waits until the box's slot has been read
-        if (by_boxes(kOut) && box >= 2) {
-          if (lane == 0) bulk_wait_read_but_one();
-          __syncwarp();
-        }
-      };
-      auto leave = [&](const CUtensorMap* map, int32_t col, int32_t cols) {
+      auto leave = [&](const CUtensorMap* map, int32_t col) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if (col < cols) tma_store_2d(map, boxes.at(box & 1), col, row0);
-          bulk_commit();                   // a group for every box, so that take() counts them
+        if (lane == 0 && col < p.e.n) {
+          tma_store_2d(map, box, col, row0);
+          bulk_commit();
         }
-        ++box;
       };
+      // Loops over the accumulator's columns stay loops where the sums are not in registers:
+      // unrolled, their code pushed the MMA warp's out of the instruction cache.
       if (p.e.pre) {                       // z, before anything else
-#pragma unroll
+#pragma unroll(is_fp32(kOut) ? 2 : 1)
         for (int part = 0; part < (kGeglu ? 2 : 1); ++part) {
-#pragma unroll
+#pragma unroll(is_fp32(kOut) ? 4 : 1)
           for (int u = 0; u < kUnits; ++u) {
             float z[32];
             load(part * 2 + u, z);
             add_bias(bias + part * 64 + u * 32, z);
             const int32_t col = col0 + u * 32;
             if constexpr (!by_boxes(kOut)) {
-              put_anywhere<is_fp32(kOut)>(p, boxes.at(0), lane, z, nullptr, 0, p.e.pre, p.e.pre_ld, row0,
+              put_anywhere<is_fp32(kOut)>(p, box, lane, z, nullptr, 0, p.e.pre, p.e.pre_ld, row0,
                            (int64_t)part * p.e.n + col, p.e.n - col);
             } else {
               if (u % kPerBox == 0) take();
-              put_row<kOut>(boxes.row(box & 1), u % kPerBox * 4, z);
+              put_row<kOut>(box_row, u % kPerBox * 4, z);
               if (u % kPerBox == kPerBox - 1)
-                leave(part ? &maps.pre_up : &maps.pre, col0 + u / kPerBox * kPerBox * 32, p.e.n);
+                leave(part ? &maps.pre_up : &maps.pre, col0 + u / kPerBox * kPerBox * 32);
             }
           }
         }
       }
-#pragma unroll
+#pragma unroll(is_fp32(kOut) ? 4 : 1)
       for (int u = 0; u < kUnits; ++u) {
         const int32_t col = col0 + u * 32;
         float y[32];
@@ -616,37 +710,27 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
           }
         }
         if constexpr (!by_boxes(kOut)) {
-          put_anywhere<is_fp32(kOut)>(p, boxes.at(0), lane, y, p.e.residual, p.e.residual_ld, p.e.out,
-                       p.e.out_ld, row0, col, p.e.n - col);
+          put_anywhere<is_fp32(kOut)>(p, box, lane, y, p.e.residual, p.e.residual_ld, p.e.out,
+                                      p.e.out_ld, row0, col, p.e.n - col);
         } else {
-          const int slot = box & 1;
           if (u % kPerBox == 0) {
-            take();
-            const int32_t box_col = col;
-            if (p.e.residual && box_col < p.e.n) {
-              if (!(loading >> slot & 1) && lane == 0)
-                boxes.load(slot, &maps.residual, box_col, row0);
-              loading &= ~(1u << slot);
-              ok = eager_warp_wait(boxes.bars + slot * 8, boxes.phases >> slot & 1, guard,
-                                   p.status, kSiteResidual);
-              boxes.phases ^= 1u << slot;
+            if (!loading) take();
+            if (p.e.residual && col < p.e.n) {
+              if (!loading) load_residual(col);
+              ok = eager_warp_wait(box_bar, box_parity, guard, p.status, kSiteResidual);
               if (!ok) break;
+              loading = false;
+              box_parity ^= 1;
             }
           }
-          if (p.e.residual) add_row<kOut>(boxes.row(slot), u % kPerBox * 4, y);
-          put_row<kOut>(boxes.row(slot), u % kPerBox * 4, y);
-          if (u % kPerBox == kPerBox - 1)
-            leave(&maps.out, col0 + u / kPerBox * kPerBox * 32, p.e.n);
+          if (p.e.residual) add_row<kOut>(box_row, u % kPerBox * 4, y);
+          put_row<kOut>(box_row, u % kPerBox * 4, y);
+          if (u % kPerBox == kPerBox - 1) leave(&maps.out, col0 + u / kPerBox * kPerBox * 32);
         }
       }
       if (!ok) {                           // the residual did not come in time
-        if (lane == 0) {
-          // This slot's arrival was counted above; the other's may be on its way too.
-          const int slot = box & 1;
-          mbar_drain_wait(boxes.bars + slot * 8, (boxes.phases >> slot & 1) ^ 1);
-          if (loading >> (slot ^ 1) & 1)
-            mbar_drain_wait(boxes.bars + (slot ^ 1) * 8, boxes.phases >> (slot ^ 1) & 1);
-        }
+        if (lane == 0) mbar_drain_wait(box_bar, box_parity);
+        box_parity ^= 1;
       }
     }
     bulk_wait_all();
@@ -654,27 +738,46 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) store_cluster_i32(peer_address(smem_u32(&s.aborted[rank]), 0),
-                                          s.guard.abort);
+  if (threadIdx.x == 0) {
+    for (uint32_t to = 0; to < 2 * kPairs; ++to) {
+      for (int i = 0; i < 2; ++i)
+        store_cluster_i32(peer_address(smem_u32(&s.issued[i][cta]), to), s.loaded[i]);
+      store_cluster_i32(peer_address(smem_u32(&s.aborted[cta]), to), s.guard.abort);
+    }
+  }
   __syncthreads();
   cluster_sync();
-  // The issuing warp's last commits arrive in both CTAs: the second stays until they,
-  // and so every arrival before them, have reached its barriers.
-  if (rank == 1 && threadIdx.x == 0) mbar_drain_wait(smem_u32(&s.drain), 0);
-  if (rank == 0 && threadIdx.x == 0 && (s.aborted[0] || s.aborted[1])) {
-    // Both producers have stopped. Blocks that only one CTA loaded are put right
-    // on their barrier, then every load that may be in flight is waited for.
-    const int32_t n0 = s.issued[0], n1 = s.issued[1];
-    const int32_t both = n0 < n1 ? n0 : n1, any = n0 < n1 ? n1 : n0;
-    for (int32_t i = both; i < any; ++i) {
-      const uint32_t bar = smem_u32(&s.full[i % kStages]);
-      if (n0 > n1)
-        mbar_complete_tx(bar, kPairBytes / 2);
-      else
-        mbar_arrive_expect_tx(bar, kPairBytes / 2);
+  if (threadIdx.x == 0) {
+    // The issuing warps' last commits arrive in every CTA, which stays until they, and so
+    // every arrival before them, have reached its barriers.
+    mbar_drain_wait(smem_u32(&s.drain), 0);
+    bool aborted = false;
+    int32_t fewest = s.loaded[0], most = s.loaded[0];
+    for (int i = 0; i < 2 * kPairs; ++i) {
+      aborted |= s.aborted[i] != 0;
+      for (int j = 0; j < 2; ++j) {
+        fewest = s.issued[j][i] < fewest ? s.issued[j][i] : fewest;
+        most = s.issued[j][i] > most ? s.issued[j][i] : most;
+      }
     }
-    for (int32_t i = any > kStages ? any - kStages : 0; i < any; ++i)
-      mbar_drain_wait(smem_u32(&s.full[i % kStages]), (i / kStages) & 1);
+    if (rank == 0 && aborted) {
+      // All loading warps have stopped. Blocks that only some of them loaded are put right
+      // on this pair's barrier, then every load that may be in flight is waited for.
+      for (int32_t i = fewest; i < most; ++i) {
+        uint32_t bytes = 0;                // into the pair's CTAs
+        for (int j = 0; j < 2 * kPairs; ++j) {
+          if (j >> 1 == pair && s.issued[0][j] > i) bytes += kOperandBytes;
+          if (s.issued[1][j] > i) bytes += kOperandBytes / kPairs;
+        }
+        const uint32_t bar = smem_u32(&s.full[i % kStages]);
+        if (s.loaded[0] <= i)              // nothing was expected yet
+          mbar_arrive_expect_tx(bar, bytes);
+        else if (bytes < kPairBytes)
+          mbar_complete_tx(bar, kPairBytes - bytes);
+      }
+      for (int32_t i = most > kStages ? most - kStages : 0; i < most; ++i)
+        mbar_drain_wait(smem_u32(&s.full[i % kStages]), (i / kStages) & 1);
+    }
   }
   __syncthreads();
   cluster_sync();
@@ -686,63 +789,49 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
   }
 }
 
-// Sums the parts of every tile that several pairs share, in the order of k, and finishes
-// them; without blocks of k, finishes zeros. One block per 32 rows x 128 columns of the
-// accumulator (64 of the gate, 64 of the up part with geglu); parts are column-group-major.
+// Adds the slices' sums of every tile, in the order of k, and finishes them; without slices,
+// finishes zeros. One block per 32 rows x 128 columns of the accumulator (64 of the gate, 64
+// of the up part with geglu); parts are column-group-major.
 template <bool kGeglu>
 __global__ void __launch_bounds__(256)
-matmul_parts_kernel(const __grid_constant__ Params p, int32_t pairs) {
+matmul_parts_kernel(const __grid_constant__ Params p) {
   constexpr int32_t kOutCols = kGeglu ? kTile / 2 : kTile;
   __shared__ float tile[32][132];
   griddep_wait();                                        // before any block may leave
   const int piece = blockIdx.x & 15;                     // 2 CTAs x 4 row quarters x 2 halves
   const int32_t t = blockIdx.x >> 4;
   const int rank = piece >> 3, quad = (piece >> 1) & 3, half = piece & 1;
-  const int32_t rt = t / p.col_tiles, ct = t - rt * p.col_tiles;
+  int32_t rt, ct;
+  place(p, t, rt, ct);
   const int32_t row0 = rt * kTile + rank * kRows + quad * 32;
   const int32_t col0 = ct * kOutCols + half * (kOutCols / 2);
   if (row0 >= p.e.m || col0 >= p.e.n) return;
   const int row = threadIdx.x & 31, g0 = threadIdx.x >> 5;
   float4 sum[4] = {};
-  if (p.blocks) {
-    const int32_t lo = t * p.blocks, hi = lo + p.blocks; // the tile's blocks
-    // Pair q holds block `lo`: run_start(q) <= lo < run_start(q + 1).
-    const int32_t long_end = p.run_more * (p.run_blocks + 1);
-    int32_t q = lo < long_end ? lo / (p.run_blocks + 1)
-                              : p.run_more + (lo - long_end) / p.run_blocks;
-    if (run_start(p, q + 1) >= hi) return;               // one pair wrote the whole tile
-    const float4* parts = reinterpret_cast<const float4*>(p.parts) +
-                          (rank * 64 + half * 32) * 128 + quad * 32 + row + g0 * 128;
-    // Four parts in flight, added in the order of k. A pair's part of the tile is its
-    // first segment unless its run began before the tile.
-    constexpr int kAhead = 4;
-    while (q < pairs && run_start(p, q) < hi) {
-      float4 v[kAhead][4];
-      bool in[kAhead];
+  const float4* parts = reinterpret_cast<const float4*>(p.parts + (int64_t)t * kPartFloats) +
+                        (rank * 64 + half * 32) * 128 + quad * 32 + row + g0 * 128;
+  constexpr int kAhead = 4;                              // parts in flight
+  for (int32_t q = 0; q < p.slices; q += kAhead) {
+    float4 v[kAhead][4];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int32_t start = run_start(p, q + j);
-        in[j] = q + j < pairs && start < hi;
-        const int64_t slot = 2 * (q + j) + (start >= lo ? 0 : 1);
-        if (in[j]) {
+    for (int j = 0; j < kAhead; ++j) {
+      if (q + j < p.slices) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[j][i] = parts[slot * (int64_t)(kPartFloats / 4) + 8 * i * 128];
+        for (int i = 0; i < 4; ++i)
+          v[j][i] = parts[(int64_t)(q + j) * p.tiles * (int64_t)(kPartFloats / 4) + 8 * i * 128];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (q + j < p.slices) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i].x += v[j][i].x;
+          sum[i].y += v[j][i].y;
+          sum[i].z += v[j][i].z;
+          sum[i].w += v[j][i].w;
         }
       }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (in[j]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum[i].x += v[j][i].x;
-            sum[i].y += v[j][i].y;
-            sum[i].z += v[j][i].z;
-            sum[i].w += v[j][i].w;
-          }
-        }
-      }
-      q += kAhead;
     }
   }
 #pragma unroll
@@ -762,12 +851,7 @@ matmul_parts_kernel(const __grid_constant__ Params p, int32_t pairs) {
 }
 
 // ---------------------------------------------------------------- host side
-int32_t pair_count() {
-  const int32_t n = device_sm_count() / 2;
-  return n < kMaxPairs ? n : kMaxPairs;
-}
-
-Params base_params(const Matmul& q) {
+Params base_params(const Matmul& q, int pairs) {
   Params p = {};
   p.e = q.e;
   p.term_blocks = (int32_t)ceil_div(q.k, kMatmulBlock);
@@ -777,31 +861,33 @@ Params base_params(const Matmul& q) {
   p.b_transposed = q.b.transposed ? 1 : 0;
   const bool geglu = q.e.act == PE_ACT_GEGLU;
   p.up_row = geglu ? q.e.n : 0;
+  p.row_units = (int32_t)ceil_div(q.m, kTile * pairs);
   p.col_tiles = (int32_t)ceil_div(q.e.n, geglu ? kTile / 2 : kTile);
-  p.tiles = (int32_t)(ceil_div(q.m, kTile) * p.col_tiles);
+  p.tiles = p.row_units * p.col_tiles;
+  p.by_band = Divisor::of(kBand * p.col_tiles);
+  p.by_tiles = Divisor::of(p.tiles);
   p.idesc = idesc_bf16(256, 256, q.a.transposed, q.b.transposed);
   p.wait_limit_ns = wait_limit_ns();
   return p;
 }
 
 template <bool kGeglu>
-pe_status launch_parts(const Params& p, int32_t pairs, cudaStream_t stream) {
+pe_status launch_parts(const Params& p, cudaStream_t stream) {
   return launch_after_previous(matmul_parts_kernel<kGeglu>, dim3((unsigned)(16 * p.tiles)),
-                               dim3(256), 0, stream, p, pairs);
+                               dim3(256), 0, stream, p);
 }
 
 pe_status operand_map(CUtensorMap* map, const MatmulOperand& x, int32_t rows, int32_t k,
-                      int32_t planes) {
-  if (x.transposed)
-    return matmul_map_planes(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x.base, k, rows, x.ld * 2,
-                             64, planes);
-  return matmul_map_planes(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x.base, rows, k, x.ld * 2,
-                           kRows, planes);
+                      int32_t planes, uint32_t box_rows) {
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return x.transposed
+             ? matmul_map_planes(map, bf16, 2, x.base, k, rows, x.ld * 2, 64, planes)
+             : matmul_map_planes(map, bf16, 2, x.base, rows, k, x.ld * 2, box_rows, planes);
 }
 
-template <int kOut, bool kGeglu>
-pe_status launch_tiles(const Maps& maps, const Params& p, int32_t pairs, cudaStream_t stream) {
-  const auto kernel = matmul_tiles_kernel<kOut, kGeglu>;
+template <int kOut, bool kGeglu, int kPairs>
+pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) {
+  const auto kernel = matmul_tiles_kernel<kOut, kGeglu, kPairs>;
   const size_t smem = sizeof(Smem) + 1024;
   PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(smem)));
@@ -811,36 +897,52 @@ pe_status launch_tiles(const Maps& maps, const Params& p, int32_t pairs, cudaStr
     if (static_cast<uint32_t>(attr.numRegs) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
       return PE_ERR_UNSUPPORTED;
   }
-  PE_TRY(launch_after_previous(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, stream,
-                               maps, p));
-  return p.shared_tiles ? launch_parts<kGeglu>(p, pairs, stream) : PE_OK;
+  // Clusters that fit at a time: each takes as many of one GPC's SMs as it has CTAs.
+  const int64_t work = (int64_t)p.tiles * p.slices;
+  const int64_t fit = kPairs == 2 ? kMatmulClusters : device_sm_count() / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * kPairs * (work < fit ? work : fit)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * kPairs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  PE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, maps, p));
+  return PE_OK;
 }
 
-template <bool kGeglu>
-pe_status launch_out(bool boxes, const Maps& maps, const Params& p, int32_t pairs,
-                     cudaStream_t stream) {
+template <bool kGeglu, int kPairs>
+pe_status launch_out(bool boxes, const Maps& maps, const Params& p, cudaStream_t stream) {
   if (p.e.out_fp32)
-    return boxes ? launch_tiles<kOutFp32, kGeglu>(maps, p, pairs, stream)
-                 : launch_tiles<kOutFp32Anywhere, kGeglu>(maps, p, pairs, stream);
-  return boxes ? launch_tiles<kOutBf16, kGeglu>(maps, p, pairs, stream)
-               : launch_tiles<kOutBf16Anywhere, kGeglu>(maps, p, pairs, stream);
+    return boxes ? launch_kernel<kOutFp32, kGeglu, kPairs>(maps, p, stream)
+                 : launch_kernel<kOutFp32Anywhere, kGeglu, kPairs>(maps, p, stream);
+  return boxes ? launch_kernel<kOutBf16, kGeglu, kPairs>(maps, p, stream)
+               : launch_kernel<kOutBf16Anywhere, kGeglu, kPairs>(maps, p, stream);
 }
 
 }  // namespace
 
-size_t matmul_tiles_workspace() { return 2 * kMaxPairs * kPartFloats * sizeof(float); }
-
-pe_status matmul_no_sum(const Matmul& q, cudaStream_t stream) {
-  const Params p = base_params(q);
-  return q.e.act == PE_ACT_GEGLU ? launch_parts<true>(p, 0, stream)
-                                 : launch_parts<false>(p, 0, stream);
+size_t matmul_tiles_workspace(int64_t tiles, int32_t slices) {
+  return slices > 1 ? (size_t)tiles * (size_t)slices * kPartFloats * sizeof(float) : 0;
 }
 
-pe_status matmul_tiles(const Matmul& q, bool runs, void* workspace, DeviceStatus* status,
-                       cudaStream_t stream) {
+pe_status matmul_no_sum(const Matmul& q, cudaStream_t stream) {
+  const Params p = base_params(q, 1);
+  return q.e.act == PE_ACT_GEGLU ? launch_parts<true>(p, stream) : launch_parts<false>(p, stream);
+}
+
+pe_status matmul_tiles(const Matmul& q, int32_t pairs, int32_t slices, void* workspace,
+                       DeviceStatus* status, cudaStream_t stream) {
   Maps maps;
-  PE_TRY(operand_map(&maps.a, q.a, q.m, q.k, q.planes));
-  PE_TRY(operand_map(&maps.b, q.b, q.n, q.k, q.planes));
+  PE_TRY(operand_map(&maps.a, q.a, q.m, q.k, q.planes, kRows));
+  PE_TRY(operand_map(&maps.b, q.b, q.n, q.k, q.planes, kRows / pairs));
   const MatmulEpilogue& e = q.e;
   const bool geglu = e.act == PE_ACT_GEGLU;
   const int size = e.out_fp32 ? 4 : 2;
@@ -862,16 +964,19 @@ pe_status matmul_tiles(const Matmul& q, bool runs, void* workspace, DeviceStatus
     PE_TRY(map(&maps.pre, e.pre, e.pre_ld));
     PE_TRY(map(&maps.pre_up, e.pre ? pre_up : nullptr, e.pre_ld));
   }
-  Params p = base_params(q);
+  Params p = base_params(q, pairs);
+  p.slices = slices;
+  p.slice_blocks = p.blocks / slices;
+  p.slice_more = p.blocks % slices;
   p.status = status;
   p.parts = static_cast<float*>(workspace);
-  int32_t pairs = pair_count();
-  p.shared_tiles = runs ? 1 : 0;
-  p.run_blocks = (int32_t)((int64_t)p.tiles * p.blocks / pairs);
-  p.run_more = (int32_t)((int64_t)p.tiles * p.blocks % pairs);
-  if (!p.shared_tiles && p.tiles < pairs) pairs = p.tiles;
-  return geglu ? launch_out<true>(tma, maps, p, pairs, stream)
-               : launch_out<false>(tma, maps, p, pairs, stream);
+  if (pairs == 2)
+    return geglu ? launch_out<true, 2>(tma, maps, p, stream)
+                 : launch_out<false, 2>(tma, maps, p, stream);
+  PE_TRY((geglu ? launch_out<true, 1>(tma, maps, p, stream)
+                : launch_out<false, 1>(tma, maps, p, stream)));
+  if (slices == 1) return PE_OK;
+  return geglu ? launch_parts<true>(p, stream) : launch_parts<false>(p, stream);
 }
 
 }  // namespace pe

@@ -207,6 +207,26 @@ def test_infinities_and_nan_stay_in_their_rows(m, dtype):
     assert torch.equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("m", [2, 3000])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_activations_of_far_and_infinite_sums(m, dtype):
+    """The bias is what goes into the activation: gelu and relu at their limits."""
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([-inf, inf, nan, -1e30, 1e30, -70.0, 70.0, -0.0], device=DEV).to(dtype)
+    a, b = torch.zeros(m, 64, dtype=dtype, device=DEV), torch.zeros(8, 64, dtype=dtype, device=DEV)
+    got = pe.pe_matmul(a, b, bias=z, activation="gelu")
+    assert got.nan_to_num(7.0, inf, -inf).double().tolist() == [
+        [0.0, inf, 7.0, 0.0, float(z[4]), 0.0, 70.0, 0.0]] * m
+    got = pe.pe_matmul(a, b, bias=z, activation="relu")
+    assert got.nan_to_num(7.0, inf, -inf).double().tolist() == [
+        [0.0, inf, 7.0, 0.0, float(z[4]), 0.0, 70.0, 0.0]] * m
+    up = torch.cat([z, torch.ones(8, device=DEV, dtype=dtype)])
+    b = torch.zeros(16, 64, dtype=dtype, device=DEV)
+    got = pe.pe_matmul(a, b, bias=up, activation="geglu")
+    assert got.nan_to_num(7.0, inf, -inf).double().tolist() == [
+        [0.0, inf, 7.0, 0.0, float(z[4]), 0.0, 70.0, 0.0]] * m
+
+
 def test_fp32_numbers_of_all_sizes():
     """Near the largest number, and products far below one another."""
     big = torch.tensor([[3.4028234663852886e38, 1.0, 2.0 ** -60, -3.4e38]], device=DEV)

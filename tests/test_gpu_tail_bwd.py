@@ -172,6 +172,14 @@ def test_activation_bwd_far_arguments(act, dtype):
     dy = torch.ones_like(z)
     dz, _ = pe.pe_activation_bwd(dy, z, "gelu")
     assert dz.tolist() == [[0.0, 0.0, 0.5, 0.5, 1.0, 1.0]]
+    inf = float("inf")
+    z = torch.tensor([[-inf, inf, float("nan")] * 2], device=DEV).to(dtype)
+    dz, _ = pe.pe_activation_bwd(torch.ones(1, 6 if act == "gelu" else 3, device=DEV).to(dtype), z,
+                                 act)
+    if act == "gelu":
+        assert dz[0, :2].tolist() == [0.0, 1.0] and bool(dz[0, 2].isnan())
+    else:                                       # gate and up are both (-inf, inf, nan)
+        assert dz[0, 3:5].tolist() == [0.0, inf] and bool(dz[0, 5].isnan())
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
