@@ -3,7 +3,7 @@
 // gelu'(z) = Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi).
 #pragma once
 
-#include "pe_common.cuh"
+#include "pe_sm103.cuh"
 
 namespace pe {
 
@@ -61,6 +61,54 @@ __device__ __forceinline__ float gelu_slope(float z, float& value) {
   value = times_normal(z, phi);
   return fmaf(fminf(fmaxf(z, -64.f), 64.f) * kDensity, bell, phi);
 }
+
+// The same for results rounded to bf16, two numbers at a time in paired arithmetic. With a =
+// |z| and q = Phi(-a),
+//   gelu = max(z, 0) - a q,    gelu' = m for z < 0, 1 - m otherwise, m = q - a bell / sqrt(2 pi),
+// which keeps both tails as exact as normal_fast without computing two. a is cut off at 64,
+// where q is long zero: infinities give the limits, and a NaN stays one.
+struct GeluPair {
+  uint64_t a, q, bell;
+
+  __device__ __forceinline__ GeluPair(float z0, float z1) {
+    using namespace sm103;
+    auto cut = [](float z) {
+      float r;
+      asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(z)), "f"(64.f));
+      return r;
+    };
+    a = f2(cut(z0), cut(z1));
+    float d0, d1, e0, e1, t0, t1;
+    f2_split(ffma2(a, both(0.5f * 0.70710678f), both(1.f)), d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(d1));
+    f2_split(fmul2(fmul2(a, a), both(-0.5f * kLog2e)), e0, e1);
+    bell = f2(ex2(e0), ex2(e1));
+    const uint64_t t = f2(t0, t1);
+    uint64_t p = ffma2(both(0.5f * 0.08912372f), t, both(0.5f * -0.35997975f));
+    p = ffma2(p, t, both(0.5f * 0.39377043f));
+    p = ffma2(p, t, both(0.5f * 0.0346651f));
+    p = ffma2(p, t, both(0.5f * 0.28271717f));
+    p = ffma2(p, t, both(0.5f * 0.27735412f));
+    p = ffma2(p, t, both(0.5f * 0.28234804f));
+    q = fmul2(fmul2(p, t), bell);
+  }
+  static __device__ __forceinline__ uint64_t both(float x) { return sm103::f2(x, x); }
+  static __device__ __forceinline__ uint64_t minus(uint64_t x) {
+    return x ^ 0x8000000080000000ull;
+  }
+  __device__ __forceinline__ uint64_t value(float z0, float z1) const {
+    return sm103::ffma2(minus(a), q, sm103::f2(fmaxf(z0, 0.f), fmaxf(z1, 0.f)));
+  }
+  __device__ __forceinline__ uint64_t slope(float z0, float z1) const {
+    using namespace sm103;
+    const uint64_t m = ffma2(fmul2(minus(a), both(0.3989422804014327f)), bell, q);
+    float m0, m1, n0, n1;
+    f2_split(m, m0, m1);
+    f2_split(fadd2(both(1.f), minus(m)), n0, n1);
+    return f2(z0 < 0.f ? m0 : n0, z1 < 0.f ? m1 : n1);
+  }
+};
 
 inline bool activation_ok(int act) { return act >= PE_ACT_NONE && act <= PE_ACT_GEGLU; }
 

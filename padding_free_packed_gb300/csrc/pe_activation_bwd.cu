@@ -33,6 +33,7 @@ template <typename T, int V, int kAct, int kRows>
 __global__ void __launch_bounds__(kThreads)
 activation_bwd_kernel(const Args<T> a) {
   constexpr int kParts = kAct == PE_ACT_GEGLU ? 2 : 1;
+  constexpr bool kPaired = kAct >= PE_ACT_GELU && sizeof(T) == 2 && V > 1;
   __shared__ float sums[kRowLanes][kParts][kLanes * V];
   const int x = threadIdx.x % kLanes, y = threadIdx.x / kLanes;
   const int32_t F = a.features, c = (blockIdx.x * kLanes + x) * V;
@@ -62,8 +63,23 @@ activation_bwd_kernel(const Args<T> a) {
         const int64_t r = r0 + u * step;
         if (r < a.rows) {
           float d[kParts][V];
+          if constexpr (kPaired) {
+            using namespace sm103;
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
+            for (int j = 0; j < V / 2; ++j) {
+              const float z0 = z[u][0].get(2 * j), z1 = z[u][0].get(2 * j + 1);
+              const GeluPair at(z0, z1);
+              const uint64_t g = dy[u].pair(j), slope = at.slope(z0, z1);
+              if constexpr (kAct == PE_ACT_GEGLU) {
+                f2_split(fmul2(fmul2(g, z[u][1].pair(j)), slope), d[0][2 * j], d[0][2 * j + 1]);
+                f2_split(fmul2(g, at.value(z0, z1)), d[1][2 * j], d[1][2 * j + 1]);
+              } else {
+                f2_split(fmul2(g, slope), d[0][2 * j], d[0][2 * j + 1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int v = 0; v < (kPaired ? 0 : V); ++v) {
             const float g = dy[u].get(v);
             if constexpr (kAct == PE_ACT_GEGLU) {
               float value;
@@ -94,6 +110,7 @@ activation_bwd_kernel(const Args<T> a) {
     }
   }
   if (!a.part) return;
+  griddep_launch_dependents();                 // the second kernel may come to wait for this one
 #pragma unroll
   for (int p = 0; p < kParts; ++p)
 #pragma unroll
@@ -113,7 +130,9 @@ activation_bwd_kernel(const Args<T> a) {
 
 template <typename T, int V, int kAct>
 pe_status launch(const Args<T>& a, float* dbias, cudaStream_t stream) {
-  constexpr int kRows = V * sizeof(T) == 16 ? 2 : 4;
+  // 6 to 8 loads of a thread in flight, with narrow ones more.
+  constexpr int kRows = (kAct == PE_ACT_NONE ? 8 : kAct == PE_ACT_GEGLU ? 2 : 4) *
+                        (kAct != PE_ACT_NONE && V * sizeof(T) < 16 ? 2 : 1);
   constexpr int kParts = kAct == PE_ACT_GEGLU ? 2 : 1;
   const int64_t strips = ceil_div(a.features, kLanes * V);
   int64_t lines = ceil_div(a.rows, kRowLanes);

@@ -24,7 +24,7 @@ struct Draw {
   Keys keys;
   uint64_t offset;
   const uint64_t* device_offset;     // added to offset, or null
-  uint64_t threshold;                // kept iff word >= threshold; p < 1, so up to 2^32
+  uint32_t most_dropped;             // kept iff word > most_dropped (all are where p = 0)
   float scale;
 };
 
@@ -54,14 +54,14 @@ struct Args {
 };
 
 // V consecutive elements (a multiple of 4, or 1) a thread and step, kSteps steps in flight.
-template <typename T, int V, int kSteps>
+// kAll: p = 0, no numbers are drawn.
+template <typename T, int V, int kSteps, bool kAll>
 __global__ void __launch_bounds__(kThreads)
 dropout_kernel(const Args<T> a) {
   uint64_t offset = a.d.offset;
   if (a.d.device_offset) offset += *a.d.device_offset;
   const uint32_t o0 = (uint32_t)offset, o1 = (uint32_t)(offset >> 32);
-  const bool none_kept = a.d.threshold > 0xffffffffull;
-  const uint32_t threshold = (uint32_t)a.d.threshold;
+  const uint32_t dropped = a.d.most_dropped;
   const int64_t units = a.count / V, stride = (int64_t)gridDim.x * kThreads;
   for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < units;
        i0 += kSteps * stride) {
@@ -79,23 +79,37 @@ dropout_kernel(const Args<T> a) {
       const int64_t i = i0 + s * stride;
       if (i < units) {
         float o[V];
-#pragma unroll
-        for (int v = 0; v < V; v += 4) {
-          uint32_t w[4];
-          philox(a.d.keys, (uint64_t)(i * V + v) >> 2, o0, o1, w);
-          if constexpr (V == 1) {
+        if constexpr (V == 1) {
+          o[0] = x[s].get(0) * a.d.scale;
+          if constexpr (!kAll) {
+            uint32_t w[4];
+            philox(a.d.keys, (uint64_t)i >> 2, o0, o1, w);
             const int at = (int)(i & 3);
             const uint32_t word = at == 0 ? w[0] : at == 1 ? w[1] : at == 2 ? w[2] : w[3];
-            o[0] = word >= threshold && !none_kept ? x[s].get(0) * a.d.scale : 0.f;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4 && v + j < V; ++j)
-              o[v + j] = w[j] >= threshold && !none_kept ? x[s].get(v + j) * a.d.scale : 0.f;
+            if (word <= dropped) o[0] = 0.f;
           }
-        }
-        if (a.res) {
+          if (a.res) o[0] += r[s].get(0);
+        } else {
+          const uint64_t scale = sm103::f2(a.d.scale, a.d.scale);
 #pragma unroll
-          for (int v = 0; v < V; ++v) o[v] += r[s].get(v);
+          for (int v = 0; v < V; v += 4) {
+#pragma unroll
+            for (int j = v; j < v + 4; j += 2)
+              sm103::f2_split(sm103::fmul2(x[s].pair(j / 2), scale), o[j], o[j + 1]);
+            if constexpr (!kAll) {
+              uint32_t w[4];
+              philox(a.d.keys, (uint64_t)(i * V + v) >> 2, o0, o1, w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (w[j] <= dropped) o[v + j] = 0.f;
+            }
+          }
+          if (a.res) {
+#pragma unroll
+            for (int j = 0; j < V; j += 2)
+              sm103::f2_split(sm103::fadd2(sm103::f2(o[j], o[j + 1]), r[s].pair(j / 2)), o[j],
+                              o[j + 1]);
+          }
         }
         Vec<T, V> out;
         out.put(o);
@@ -106,11 +120,14 @@ dropout_kernel(const Args<T> a) {
   if constexpr (V > 1) {               // the last count % V elements, one a thread
     const int64_t e = units * V + threadIdx.x;
     if (blockIdx.x == 0 && e < a.count) {
-      uint32_t w[4];
-      philox(a.d.keys, (uint64_t)e >> 2, o0, o1, w);
-      const int at = (int)(e & 3);
-      const uint32_t word = at == 0 ? w[0] : at == 1 ? w[1] : at == 2 ? w[2] : w[3];
-      float o = word >= threshold && !none_kept ? to_f32(a.x[e]) * a.d.scale : 0.f;
+      float o = to_f32(a.x[e]) * a.d.scale;
+      if constexpr (!kAll) {
+        uint32_t w[4];
+        philox(a.d.keys, (uint64_t)e >> 2, o0, o1, w);
+        const int at = (int)(e & 3);
+        const uint32_t word = at == 0 ? w[0] : at == 1 ? w[1] : at == 2 ? w[2] : w[3];
+        if (word <= dropped) o = 0.f;
+      }
       if (a.res) o += to_f32(a.res[e]);
       a.y[e] = from_f32<T>(o);
     }
@@ -118,23 +135,26 @@ dropout_kernel(const Args<T> a) {
 }
 
 template <typename T, int V, int kSteps>
-pe_status launch(const Args<T>& a, cudaStream_t stream) {
+pe_status launch(const Args<T>& a, bool all, cudaStream_t stream) {
   int64_t blocks = ceil_div(ceil_div(a.count, V), kThreads);
   const int64_t most = (int64_t)device_sm_count() * 8;
   if (blocks > most) blocks = most;
-  dropout_kernel<T, V, kSteps><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  if (all)
+    dropout_kernel<T, V, kSteps, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  else
+    dropout_kernel<T, V, kSteps, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   PE_CUDA_TRY(cudaGetLastError());
   return PE_OK;
 }
 
 template <typename T>
 pe_status run(const void* x, const void* res, int64_t count, void* y, const Draw& d,
-              cudaStream_t stream) {
+              bool all, cudaStream_t stream) {
   const Args<T> a = {static_cast<const T*>(x), static_cast<const T*>(res), count,
                      static_cast<T*>(y), d};
   constexpr int V = 16 / sizeof(T);
-  if (aligned(x, 16) && aligned(y, 16) && aligned(res, 16)) return launch<T, V, 2>(a, stream);
-  return launch<T, 1, 4>(a, stream);
+  if (aligned(x, 16) && aligned(y, 16) && aligned(res, 16)) return launch<T, V, 2>(a, all, stream);
+  return launch<T, 1, 4>(a, all, stream);
 }
 
 }  // namespace
@@ -162,8 +182,10 @@ extern "C" pe_status pe_dropout(pe_dtype dtype, const void* x, const void* resid
   }
   d.offset = offset;
   d.device_offset = device_offset;
-  d.threshold = (uint64_t)ceil(p * 4294967296.0);
+  // word >= p 2^32 <=> word > ceil(p 2^32) - 1, a number below 2^32 for p > 0.
+  const bool all = p == 0.0;
+  d.most_dropped = all ? 0u : (uint32_t)((uint64_t)ceil(p * 4294967296.0) - 1);
   d.scale = (float)(1.0 / (1.0 - p));
-  if (dtype == PE_FP32) return run<float>(x, residual, count, y, d, stream);
-  return run<__nv_bfloat16>(x, residual, count, y, d, stream);
+  if (dtype == PE_FP32) return run<float>(x, residual, count, y, d, all, stream);
+  return run<__nv_bfloat16>(x, residual, count, y, d, all, stream);
 }

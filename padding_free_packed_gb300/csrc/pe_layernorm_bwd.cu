@@ -20,7 +20,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int32_t kMaxChannels = 16384;
 constexpr int32_t kWide = 4096;                 // wider rows: one block of 1024 threads a row
-constexpr int kMaxBlocks = 456, kMaxWideBlocks = 152;
+constexpr int kMaxBlocks = 608, kMaxWideBlocks = 152;
 
 template <typename T>
 struct Args {
@@ -58,9 +58,17 @@ __device__ __forceinline__ void group_sum(float (&x)[kSums], float* red, int gro
   }
 }
 
+// Blocks an SM that the registers are to allow: more of them spill, fewer leave too few rows
+// in flight (169151 x 1024 bf16, 16 channels a thread: 1 block 284 us, 2 blocks 220, 3 blocks
+// 495; 90487 x 512 fp32, 8 channels: 2 blocks 116 us, 3 blocks 184).
+template <int V, int kIter, int kGroup>
+constexpr int kMinBlocks =
+    V == 8 ? (kIter > 1 ? 2 : kGroup == 96 ? 4 : 3) : V * kIter > 8 ? 1 : 2;
+
 // kGroup threads a row, each with kIter vectors of V channels, the same for all of its rows.
 template <typename T, int V, int kIter, int kGroup>
-__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads / kGroup * kGroup)
+__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads / kGroup * kGroup,
+                                  kGroup > kThreads ? 1 : kMinBlocks<V, kIter, kGroup>)
 layernorm_bwd_kernel(const Args<T> a) {
   constexpr bool kIsWide = kGroup > kThreads;
   constexpr int kGroups = kIsWide ? 1 : kThreads / kGroup;
@@ -71,13 +79,28 @@ layernorm_bwd_kernel(const Args<T> a) {
   const int64_t step = (int64_t)gridDim.x * kGroups;
   int64_t t = (int64_t)blockIdx.x * kGroups + group;
 
+  // A thread's channels in pairs: half as many instructions, which is what bounds rows in
+  // flight here. Single channels (rows that start anywhere) go one at a time.
+  constexpr bool kPaired = V > 1 && !kIsWide;
   constexpr int kKept = kIsWide ? 1 : kIter * V;
-  float dw[kKept], db[kKept];
+  float dw[kPaired ? 1 : kKept], db[kPaired ? 1 : kKept];
+  uint64_t dw2[kPaired ? kKept / 2 : 1], db2[kPaired ? kKept / 2 : 1];
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < (kPaired ? 1 : kKept); ++i) dw[i] = db[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < (kPaired ? kKept / 2 : 1); ++i) dw2[i] = db2[i] = 0ull;
   if constexpr (kIsWide) {
     for (int32_t c = threadIdx.x; c < 2 * a.C; c += kBlock) sums[c] = 0.f;
     __syncthreads();
+  }
+  Vec<T, V> wv[kPaired ? kIter : 1];             // the weight of this thread's channels
+  if constexpr (kPaired) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      wv[it].zero();
+      if (c < a.C) wv[it] = load_vec<T, V>(a.w + c);
+    }
   }
 
   Vec<T, V> dyv[kIter], hv[kIter], rv[kIter];
@@ -97,72 +120,147 @@ layernorm_bwd_kernel(const Args<T> a) {
   load(t);
   int phase = 0;
   for (; t < a.N; t += step) {
-    Vec<T, V> dyn[kIter], hn[kIter], rn[kIter];
+    if constexpr (kPaired) {
+      using namespace sm103;
+      Vec<T, V> dyn[kIter], hn[kIter], rn[kIter];
+      uint64_t total = 0ull;
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      dyn[it] = dyv[it];
-      hn[it] = hv[it];
-      if constexpr (!kIsWide) rn[it] = rv[it];
-    }
-    if constexpr (!kIsWide) load(t + step);
-    float first[1] = {0.f};
+      for (int it = 0; it < kIter; ++it) {
+        dyn[it] = dyv[it];
+        hn[it] = hv[it];
+        rn[it] = rv[it];
 #pragma unroll
-    for (int it = 0; it < kIter; ++it)
-#pragma unroll
-      for (int v = 0; v < V; ++v) first[0] += hn[it].get(v);
-    group_sum<1, kGroup>(first, red[phase], group);
-    const float mean = first[0] * a.inv_c;
-    // Squares of h - mean, and sums of g and g (h - mean).
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int32_t c = (it * kGroup + g) * V;
-      if (c < a.C) {
-        const Vec<T, V> wv = load_vec<T, V>(a.w + c);    // from the caches, here and below
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float d = hn[it].get(v) - mean, gv = dyn[it].get(v) * wv.get(v);
-          s[0] = fmaf(d, d, s[0]);
-          s[1] += gv;
-          s[2] = fmaf(gv, d, s[2]);
-        }
+        for (int j = 0; j < V / 2; ++j) total = fadd2(total, hn[it].pair(j));
       }
-    }
-    group_sum<3, kGroup>(s, red[phase] + 32, group);
-    phase ^= 1;
-    const float rstd = rsqrtf(fmaf(s[0], a.inv_c, a.eps));
-    const float mean_g = s[1] * a.inv_c;
-    const float along = rstd * (s[2] * a.inv_c) * rstd;      // mean(g n) rstd
+      load(t + step);
+      float first[1], other;
+      f2_split(total, first[0], other);
+      first[0] += other;
+      group_sum<1, kGroup>(first, red[phase], group);
+      const float mean = first[0] * a.inv_c;
+      // Squares of d = h - mean, and the sums of g and g d.
+      uint64_t s0 = 0ull, s1 = 0ull, s2 = 0ull;
+      const uint64_t minus_mean = f2(-mean, -mean);
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const int32_t c = (it * kGroup + g) * V;
-      if (c < a.C) {
-        const Vec<T, V> wv = load_vec<T, V>(a.w + c);
-        if constexpr (kIsWide) {
-          if (a.dres) rn[it] = load_vec<T, V>(a.dres + t * a.C + c);
-        }
-        float dx[V];
+      for (int it = 0; it < kIter; ++it) {
+        if ((it * kGroup + g) * V < a.C) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float dy = dyn[it].get(v), d = hn[it].get(v) - mean;
-          dx[v] = rstd * (fmaf(dy, wv.get(v), -mean_g) - d * along);
-          if (a.dres) dx[v] += rn[it].get(v);
-          if constexpr (kIsWide) {
-            sums[c + v] = fmaf(dy, d * rstd, sums[c + v]);
-            sums[a.C + c + v] += dy;
-          } else {
-            dw[it * V + v] = fmaf(dy, d * rstd, dw[it * V + v]);
-            db[it * V + v] += dy;
+          for (int j = 0; j < V / 2; ++j) {
+            const uint64_t d = fadd2(hn[it].pair(j), minus_mean);
+            const uint64_t gv = fmul2(dyn[it].pair(j), wv[it].pair(j));
+            s0 = ffma2(d, d, s0);
+            s1 = fadd2(s1, gv);
+            s2 = ffma2(gv, d, s2);
           }
         }
-        Vec<T, V> o;
-        o.put(dx);
-        store_vec<T, V>(a.dx + t * a.C + c, o);
       }
+      float s[3], t0, t1, t2;
+      f2_split(s0, s[0], t0);
+      f2_split(s1, s[1], t1);
+      f2_split(s2, s[2], t2);
+      s[0] += t0;
+      s[1] += t1;
+      s[2] += t2;
+      group_sum<3, kGroup>(s, red[phase] + 32, group);
+      phase ^= 1;
+      const float rstd = rsqrtf(fmaf(s[0], a.inv_c, a.eps));
+      const float mean_g = s[1] * a.inv_c, along = rstd * (s[2] * a.inv_c) * rstd;
+      const uint64_t rstd2 = f2(rstd, rstd), minus_g = f2(-mean_g, -mean_g);
+      const uint64_t minus_along = f2(-along, -along);      // -mean(g n) rstd
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int32_t c = (it * kGroup + g) * V;
+        if (c < a.C) {
+          Vec<T, V> o;
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            const int e = it * (V / 2) + j;
+            const uint64_t dy = dyn[it].pair(j), d = fadd2(hn[it].pair(j), minus_mean);
+            uint64_t x = ffma2(d, minus_along, ffma2(dy, wv[it].pair(j), minus_g));
+            x = a.dres ? ffma2(x, rstd2, rn[it].pair(j)) : fmul2(x, rstd2);
+            o.put_pair(j, x);
+            dw2[e] = ffma2(dy, fmul2(d, rstd2), dw2[e]);
+            db2[e] = fadd2(db2[e], dy);
+          }
+          store_vec<T, V>(a.dx + t * a.C + c, o);
+        }
+      }
+    } else {
+      Vec<T, V> dyn[kIter], hn[kIter], rn[kIter];
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        dyn[it] = dyv[it];
+        hn[it] = hv[it];
+        if constexpr (!kIsWide) rn[it] = rv[it];
+      }
+      if constexpr (!kIsWide) load(t + step);
+      float first[1] = {0.f};
+#pragma unroll
+      for (int it = 0; it < kIter; ++it)
+#pragma unroll
+        for (int v = 0; v < V; ++v) first[0] += hn[it].get(v);
+      group_sum<1, kGroup>(first, red[phase], group);
+      const float mean = first[0] * a.inv_c;
+      float s[3] = {0.f, 0.f, 0.f};            // as above
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int32_t c = (it * kGroup + g) * V;
+        if (c < a.C) {
+          const Vec<T, V> w = load_vec<T, V>(a.w + c);   // from the caches, here and below
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float d = hn[it].get(v) - mean, gv = dyn[it].get(v) * w.get(v);
+            s[0] = fmaf(d, d, s[0]);
+            s[1] += gv;
+            s[2] = fmaf(gv, d, s[2]);
+          }
+        }
+      }
+      group_sum<3, kGroup>(s, red[phase] + 32, group);
+      phase ^= 1;
+      const float rstd = rsqrtf(fmaf(s[0], a.inv_c, a.eps));
+      const float mean_g = s[1] * a.inv_c, along = rstd * (s[2] * a.inv_c) * rstd;
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int32_t c = (it * kGroup + g) * V;
+        if (c < a.C) {
+          const Vec<T, V> w = load_vec<T, V>(a.w + c);
+          if constexpr (kIsWide) {
+            if (a.dres) rn[it] = load_vec<T, V>(a.dres + t * a.C + c);
+          }
+          float dx[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float dy = dyn[it].get(v), d = hn[it].get(v) - mean;
+            dx[v] = rstd * (fmaf(dy, w.get(v), -mean_g) - d * along);
+            if (a.dres) dx[v] += rn[it].get(v);
+            if constexpr (kIsWide) {
+              sums[c + v] = fmaf(dy, d * rstd, sums[c + v]);
+              sums[a.C + c + v] += dy;
+            } else {
+              dw[it * V + v] = fmaf(dy, d * rstd, dw[it * V + v]);
+              db[it * V + v] += dy;
+            }
+          }
+          Vec<T, V> o;
+          o.put(dx);
+          store_vec<T, V>(a.dx + t * a.C + c, o);
+        }
+      }
+      if constexpr (kIsWide) load(t + step);
     }
-    if constexpr (kIsWide) load(t + step);
   }
+  auto kept = [&](bool bias, int i) {            // this thread's sum i
+    if constexpr (kPaired) {
+      float lo, hi;
+      sm103::f2_split(bias ? db2[i / 2] : dw2[i / 2], lo, hi);
+      return i % 2 ? hi : lo;
+    } else {
+      return bias ? db[i] : dw[i];
+    }
+  };
 
+  griddep_launch_dependents();               // the second kernel may come to wait for this one
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
   if constexpr (kIsWide) {
     __syncthreads();
@@ -174,8 +272,8 @@ layernorm_bwd_kernel(const Args<T> a) {
       for (int v = 0; v < V; ++v) {
         const int32_t c = (it * kGroup + g) * V + v;
         if (c < a.C) {
-          part[c] = dw[it * V + v];
-          part[a.C + c] = db[it * V + v];
+          part[c] = kept(false, it * V + v);
+          part[a.C + c] = kept(true, it * V + v);
         }
       }
   } else {
@@ -187,7 +285,7 @@ layernorm_bwd_kernel(const Args<T> a) {
     for (int which = 0; which < 2; ++which) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kIter * V; ++i) mine[i * kLine + g] = which ? db[i] : dw[i];
+      for (int i = 0; i < kIter * V; ++i) mine[i * kLine + g] = kept(which, i);
       __syncthreads();
       for (int32_t c = threadIdx.x; c < a.C; c += kBlock) {
         const int vec = c / V, i = vec / kGroup * V + c % V;
@@ -200,28 +298,43 @@ layernorm_bwd_kernel(const Args<T> a) {
   }
 }
 
+// Blocks of a kernel that an SM holds at a time.
+template <typename K>
+int resident_blocks(K kernel, int threads, size_t smem) {
+  int blocks = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) != cudaSuccess)
+    return 0;
+  return blocks;
+}
+
 template <typename T, int V, int kIter, int kGroup>
 pe_status launch(const Args<T>& a, float* dweight, float* dbias, cudaStream_t stream) {
   constexpr bool wide = kGroup > kThreads;
   constexpr int kGroups = wide ? 1 : kThreads / kGroup;
   static_assert(!wide || kIter * kGroup * V >= kMaxChannels, "a block holds the widest row");
-  int64_t blocks = ceil_div(a.N, kGroups);
-  const int64_t most = wide ? kMaxWideBlocks : kMaxBlocks;
-  if (blocks > most) blocks = most;
+  const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup>;
   const size_t smem = wide ? 2 * (size_t)a.C * sizeof(float)
                       : kGroups > 1 ? (size_t)kGroups * kIter * V * (kGroup + 1) * sizeof(float)
                                     : 0;
-  const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup>;
   if (wide)
     PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      2 * kMaxChannels * (int)sizeof(float)));
+  // As many blocks as the device holds at a time: a block more would run alone at the end.
+  static const int resident = resident_blocks(kernel, kGroup * kGroups, wide ? 2 * kMaxChannels * sizeof(float) : smem);
+  if (resident < 1) return PE_ERR_CUDA;
+  int64_t blocks = ceil_div(a.N, kGroups), most = (int64_t)resident * device_sm_count();
+  if (most > (wide ? kMaxWideBlocks : kMaxBlocks)) most = wide ? kMaxWideBlocks : kMaxBlocks;
+  if (blocks > most) blocks = most;
   kernel<<<(unsigned)blocks, kGroup * kGroups, smem, stream>>>(a);
   PE_CUDA_TRY(cudaGetLastError());
   return launch_sum_parts(a.part, (int32_t)blocks, a.C, dweight, a.C, dbias, stream);
 }
 
 // The form for V neighbouring channels per access: vectors a thread and threads a row, by the
-// row's width.
+// row's width. 16 channels a thread of bf16, 8 of fp32 (which take twice the registers); with
+// the residual's gradient:
+//   bf16 32299 x 768    16 channels of 64 threads 43.2 us, 8 of 96 41.6, 24 of 32 51
+//   bf16 169151 x 1024  16 of 64 220 us, 8 of 128 236;   90487 x 512  16 of 32 64, 8 of 64 68
 template <typename T, int V>
 pe_status launch_rows(const Args<T>& a, float* dweight, float* dbias, cudaStream_t stream) {
   const int32_t C = a.C;
@@ -229,6 +342,7 @@ pe_status launch_rows(const Args<T>& a, float* dweight, float* dbias, cudaStream
   if constexpr (V == 8) {
     if (C <= 256) return launch<T, V, 1, 32>(a, dweight, dbias, stream);
     if (C <= 512) return launch<T, V, 2, 32>(a, dweight, dbias, stream);
+    if (C <= 768) return launch<T, V, 1, 96>(a, dweight, dbias, stream);
     if (C <= 1024) return launch<T, V, 2, 64>(a, dweight, dbias, stream);
     if (C <= 2048) return launch<T, V, 2, 128>(a, dweight, dbias, stream);
     return launch<T, V, 2, 256>(a, dweight, dbias, stream);

@@ -113,30 +113,6 @@ __device__ __forceinline__ void io_put(void* p, int64_t at, int32_t fp32, float 
     static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
 }
 
-// gelu<__nv_bfloat16> of two numbers, in paired arithmetic: z Phi(z) = max(z, 0) - |z| q with
-// q = Phi(-|z|), which needs no choice between the tails and keeps both as exact. |z| is cut
-// off at 64, where q is long zero: infinities give infinity and zero, a NaN comes through max.
-__device__ __forceinline__ void gelu_pair(float& z0, float& z1) {
-  const float a0 = fminf(fabsf(z0), 64.f), a1 = fminf(fabsf(z1), 64.f);
-  const uint64_t a = f2(a0, a1);
-  float d0, d1, e0, e1, t0, t1;
-  f2_split(ffma2(a, f2(0.5f * 0.70710678f, 0.5f * 0.70710678f), f2(1.f, 1.f)), d0, d1);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(d0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(d1));
-  f2_split(fmul2(fmul2(a, a), f2(-0.5f * kLog2e, -0.5f * kLog2e)), e0, e1);
-  const uint64_t t = f2(t0, t1);
-  // Half of the polynomial of normal_fast, whose tail is 1/2 P(t) t exp(-z^2 / 2).
-  auto twice = [](float c) { return f2(0.5f * c, 0.5f * c); };
-  uint64_t p = ffma2(twice(0.08912372f), t, twice(-0.35997975f));
-  p = ffma2(p, t, twice(0.39377043f));
-  p = ffma2(p, t, twice(0.0346651f));
-  p = ffma2(p, t, twice(0.28271717f));
-  p = ffma2(p, t, twice(0.27735412f));
-  p = ffma2(p, t, twice(0.28234804f));
-  const uint64_t q = fmul2(fmul2(p, t), f2(ex2(e0), ex2(e1)));
-  f2_split(ffma2(f2(-a0, -a1), q, f2(max_nan(z0, 0.f), max_nan(z1, 0.f))), z0, z1);
-}
-
 // gelu where the result is rounded to fp32; out of line, as it is long.
 static __device__ __noinline__ float gelu_fp32(float z) { return gelu<float>(z); }
 

@@ -66,7 +66,7 @@ static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
 // results a few, whose sums are then added in fp32 registers. The tensor cores cut the sum
 // off after every 16 products (1.7e-8 of it a time, always towards zero, measured), which a
 // chain of 11500 products turned into 1.2e-5 of the result; this way it stays at 3e-7.
-constexpr int32_t kChunk = 4;
+constexpr int32_t kChunk = 8;
 constexpr int32_t chunk_of(int out) { return is_fp32(out) ? kChunk : 0x7fffffff; }
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 
@@ -342,7 +342,8 @@ __device__ __forceinline__ void apply_gelu(float (&z)[32]) {
     for (int i = 0; i < 32; ++i) z[i] = gelu_fp32(z[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) gelu_pair(z[i], z[i + 1]);
+    for (int i = 0; i < 32; i += 2)
+      f2_split(GeluPair(z[i], z[i + 1]).value(z[i], z[i + 1]), z[i], z[i + 1]);
   }
 }
 

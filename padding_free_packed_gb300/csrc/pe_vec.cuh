@@ -3,6 +3,7 @@
 #pragma once
 
 #include "pe_common.cuh"
+#include "pe_sm103.cuh"
 
 namespace pe {
 
@@ -16,6 +17,8 @@ template <int V>
 struct alignas(4 * V) Vec<float, V> {
   float w[V];
   __device__ float get(int v) const { return w[v]; }
+  __device__ uint64_t pair(int j) const { return sm103::f2(w[2 * j], w[2 * j + 1]); }
+  __device__ void put_pair(int j, uint64_t x) { sm103::f2_split(x, w[2 * j], w[2 * j + 1]); }
   __device__ void zero() {
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = 0.f;
@@ -34,6 +37,13 @@ struct alignas(2 * V) Vec<__nv_bfloat16, V> {
   uint32_t w[V / 2];
   __device__ float get(int v) const {
     return __uint_as_float(v & 1 ? w[v >> 1] & 0xffff0000u : w[v >> 1] << 16);
+  }
+  // Elements 2 j and 2 j + 1 for paired fp32 arithmetic, and back, rounded.
+  __device__ uint64_t pair(int j) const { return sm103::f2(get(2 * j), get(2 * j + 1)); }
+  __device__ void put_pair(int j, uint64_t x) {
+    float lo, hi;
+    sm103::f2_split(x, lo, hi);
+    w[j] = sm103::pack_bf16x2(lo, hi);
   }
   __device__ void zero() {
 #pragma unroll
