@@ -54,6 +54,7 @@ split_kernel(const SplitOperand a, const SplitOperand b, unsigned a_blocks) {
   const int64_t blocks = second ? gridDim.x - a_blocks : a_blocks;
   const int64_t groups = o.part_ld / 8, total = o.rows * groups;
   griddep_wait();
+  griddep_launch_dependents();             // the product may come to wait for this kernel
   for (int64_t i = block * kSplitThreads + threadIdx.x; i < total; i += blocks * kSplitThreads) {
     const int64_t row = i / groups;
     const int64_t c = (i - row * groups) * 8;
@@ -120,29 +121,46 @@ pe_status split(Matmul& p, void* parts, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- the choice
-// Estimated microseconds of every way.
 int64_t tile_count(int64_t m, int64_t n) { return ceil_div(m, 256) * ceil_div(n, 256); }
 
+// Estimated microseconds of every way, from times measured on a GB300 (m x n x k, bf16; T:
+// rows of a per CTA, S: split; tiles: on pairs, on clusters of two pairs):
+//   1 x 2304 x 768     T16 S1 6.8, S2 5.9, S4 5.2, S8 5.7   T64 S4 5.4      tiles 8.4
+//   1 x 768 x 2304     T16 S1 13.6, S4 6.9, S8 6.5          T64 S8 6.5      tiles 14.7
+//   64 x 768 x 768     T16 S4 5.7   T32 S4 5.9              T64 S2 6.9      tiles 8.9
+//   128 x 2304 x 768   T16 S2 7.7   T32 S2 6.3, S4 7.0      T64 S4 6.6      tiles 9.1
+//   320 x 1001 x 1140  T16 S1 10.9  T32 S1 9.7              T64 S2 8.4
+//   320 x 2304 x 768   T16 S1 14.1  T32 S1 8.1, S2 12.7     T64 S1 8.6      tiles 9.3
+//   640 x 2304 x 768                T32 S1 14.5             T64 S1 9.4      tiles 9.5
+//   2500 x 768 x 768                T32 S1 15.7             T64 S1 9.8      tiles 9.5
+//   20000 x 64 x 768                T32 S1 24.9             T64 S1 18.3     tiles 13.3, 17.6
+// A narrow CTA takes 0.28 for each block of k beside its start and its rows, half as much
+// again where two share an SM, and what is left over after 304 takes a second turn. A tile takes 0.26 for each block
+// with up to 136 SMs at work or with two pairs a cluster (which hold 144), 0.27 with all, and
+// 0.5 between two. Slices pay for parts that are written and read:
+//   2304 x 768 x 32299 to fp32, 27 tiles   1: 142, 2: 84, 4: 92, 5: 82, 8: 85, 12: 101
+//   768 x 768 x 32299, 9 tiles             1: 142, 2: 79, 4: 47, 6: 39, 8: 37, 9: 52, 16: 43
+//   1024 x 1024 x 169151, 16 tiles         2: 361, 4: 212, 5: 331, 8: 220, 9: 208, 12: 230
 LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
                        bool a_transposed) {
   constexpr int64_t kSms = 152, kPairs = kSms / 2;
   const int64_t blocks = ceil_div(k, kMatmulBlock) * (fp32 ? kMaxMatmulTerms : 1);
   const int64_t tiles = tile_count(m, n);
   LinearPlan plan = {0, 1, 1, 1};
-  double best = 5 + (double)ceil_div(tiles, kPairs) * (0.3 * (double)blocks + 0.5);
+  double best = 5.5 + (double)ceil_div(tiles, kPairs) *
+                          ((tiles <= 68 ? 0.26 : 0.27) * (double)blocks + 0.5);
   const int64_t doubles = ceil_div(m, 512) * ceil_div(n, 256);
-  const double two = 5 + (double)ceil_div(doubles, kMatmulClusters) * (0.26 * (double)blocks + 0.5);
+  const double two =
+      5.5 + (double)ceil_div(doubles, kMatmulClusters) * (0.26 * (double)blocks + 0.5);
   if (two < best) {
     best = two;
     plan.pairs = 2;
   }
-  // Slices of eight blocks at least; a part is written and read once.
+  // Slices of eight blocks at least.
   for (int32_t slices = 2; slices <= 16 && slices * 8 <= blocks && tiles <= 4 * kPairs; ++slices) {
     const int64_t units = tiles * slices;
-    const double share = units < kPairs ? (double)units / kPairs : 1.0;
-    const double block = share < 0.85 ? 0.26 : 0.3;
     const double t = 9 + (double)ceil_div(units, kPairs) *
-                             (block * (double)ceil_div(blocks, slices) + 0.5) +
+                             ((units <= 68 ? 0.26 : 0.27) * (double)ceil_div(blocks, slices) + 0.5) +
                      0.1 * (double)units;
     if (t < best) {
       best = t;
@@ -151,18 +169,23 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
     }
   }
   constexpr int32_t kRows[3] = {16, 32, 64};
-  constexpr double kFixed[3] = {3.0, 3.2, 3.6}, kBlock[3] = {0.2, 0.2, 0.22};
+  constexpr double kStart[3] = {3.6, 4.2, 5.1};
+  const int64_t col_tiles = ceil_div(geglu ? n / 2 : n, geglu ? 64 : 128);
   for (int i = a_transposed ? 2 : 0; i < 3; ++i) {
-    const int64_t ctas = ceil_div(m, kRows[i]) * ceil_div(geglu ? n / 2 : n, geglu ? 64 : 128);
+    const int64_t ctas = ceil_div(m, kRows[i]) * col_tiles;
     if (ctas > 8 * kSms || ceil_div(m, kRows[i]) > 65535) continue;
-    int64_t split = kSms / ctas < blocks / 2 ? kSms / ctas : blocks / 2;
-    split = blocks < 7 || split < 1 ? 1 : split > 8 ? 8 : split;
-    const double shared = (double)ceil_div(ctas * split, kSms) - 1;
-    const double t = kFixed[i] + kBlock[i] * (double)ceil_div(blocks, split) * (1 + 0.6 * shared) +
-                     1.2 * shared + (split > 1 ? 0.8 : 0);
-    if (t < best) {
-      best = t;
-      plan = {kRows[i], (int32_t)split, 1, 1};
+    for (int32_t split = 1; split <= 8 && (split == 1 || split * 2 <= blocks);
+         split += split < 2 ? 1 : 2) {
+      const int64_t units = ctas * split;
+      const bool shared = units > kSms;
+      double t = kStart[i] + (shared ? 0.42 : 0.28) * (double)ceil_div(blocks, split);
+      if (split > 1) t += 0.6 + 0.13 * split;
+      if (shared) t += split > 1 ? 1.5 : 0.2;
+      t += (double)(ceil_div(units, 2 * kSms) - 1) * (t - 2);
+      if (t < best) {
+        best = t;
+        plan = {kRows[i], split, 1, 1};
+      }
     }
   }
   return plan;

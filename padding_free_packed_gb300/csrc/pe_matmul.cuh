@@ -116,33 +116,30 @@ __device__ __forceinline__ void io_put(void* p, int64_t at, int32_t fp32, float 
 // gelu where the result is rounded to fp32; out of line, as it is long.
 static __device__ __noinline__ float gelu_fp32(float z) { return gelu<float>(z); }
 
-__device__ __forceinline__ float matmul_gelu(float z, int32_t out_fp32) {
-  return out_fp32 ? gelu_fp32(z) : gelu<__nv_bfloat16>(z);
-}
+// Four neighbouring columns of out from their sums (with geglu: gate and up), `count` of them
+// inside the matrix; the columns' bias is read once for all rows.
+template <int kAct>
+struct Finish4 {
+  static constexpr bool kGeglu = kAct == PE_ACT_GEGLU;
+  const MatmulEpilogue& e;
+  int32_t col, count;
+  bool four;                 // accesses of four elements
+  float bias[4], up_bias[4];
 
-// Four neighbouring columns of out from their sums (with geglu: gate and up), `left` of them
-// inside the matrix.
-__device__ __forceinline__ void finish4(const MatmulEpilogue& e, int64_t row, int32_t col,
-                                        int32_t left, const float (&sum)[4],
-                                        const float (&up_sum)[4]) {
-  const bool geglu = e.act == PE_ACT_GEGLU;
-  const int32_t count = left < 4 ? left : 4;
-  float z[4], u[4], y[4];
+  __device__ Finish4(const MatmulEpilogue& epilogue, int32_t first) : e(epilogue), col(first) {
+    count = e.n - col < 4 ? e.n - col : 4;
+    four = e.by_four && count == 4;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    z[j] = sum[j];
-    u[j] = up_sum[j];
-    if (e.bias && j < count) {
-      z[j] += io_get(e.bias, col + j, e.out_fp32);
-      if (geglu) u[j] += io_get(e.bias, (int64_t)e.n + col + j, e.out_fp32);
+    for (int j = 0; j < 4; ++j) {
+      bias[j] = up_bias[j] = 0.f;
+      if (e.bias && j < count) {
+        bias[j] = io_get(e.bias, col + j, e.out_fp32);
+        if (kGeglu) up_bias[j] = io_get(e.bias, (int64_t)e.n + col + j, e.out_fp32);
+      }
     }
-    y[j] = e.act == PE_ACT_RELU ? (z[j] < 0.f ? 0.f : z[j])
-           : e.act >= PE_ACT_GELU ? matmul_gelu(z[j], e.out_fp32)
-                                  : z[j];
-    if (geglu) y[j] *= u[j];
   }
-  auto put = [&](void* p, int64_t at, const float (&v)[4], bool four) {
-    if (four) {
+  __device__ void put(void* p, int64_t at, const float (&v)[4], bool by_four) const {
+    if (by_four) {
       if (e.out_fp32)
         *reinterpret_cast<float4*>(static_cast<float*>(p) + at) =
             make_float4(v[0], v[1], v[2], v[3]);
@@ -154,19 +151,61 @@ __device__ __forceinline__ void finish4(const MatmulEpilogue& e, int64_t row, in
       for (int j = 0; j < 4; ++j)
         if (j < count) io_put(p, at + j, e.out_fp32, v[j]);
     }
-  };
-  const bool four = e.by_four && count == 4;
-  if (e.pre) {
-    put(e.pre, row * e.pre_ld + col, z, four);
-    if (geglu) put(e.pre, row * e.pre_ld + e.n + col, u, four && e.n % 4 == 0);
   }
-  if (e.residual) {
+  // The residual of a row, to be read ahead of the sums.
+  __device__ void residual(int64_t row, float (&r)[4]) const {
+    const int64_t at = row * e.residual_ld + col;
+    if (four) {
+      if (e.out_fp32) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + at);
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(
+            static_cast<const __nv_bfloat16*>(e.residual) + at);
+        r[0] = __uint_as_float(v.x << 16), r[1] = __uint_as_float(v.x & 0xffff0000u);
+        r[2] = __uint_as_float(v.y << 16), r[3] = __uint_as_float(v.y & 0xffff0000u);
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < count) y[j] += io_get(e.residual, row * e.residual_ld + col + j, e.out_fp32);
+      for (int j = 0; j < 4; ++j) r[j] = j < count ? io_get(e.residual, at + j, e.out_fp32) : 0.f;
+    }
   }
-  put(e.out, row * e.out_ld + col, y, four);
-}
+  __device__ void row(int64_t row, const float4& sum, const float4& up_sum,
+                      const float (&r)[4]) const {
+    const float z[4] = {sum.x + bias[0], sum.y + bias[1], sum.z + bias[2], sum.w + bias[3]};
+    const float u[4] = {up_sum.x + up_bias[0], up_sum.y + up_bias[1], up_sum.z + up_bias[2],
+                        up_sum.w + up_bias[3]};
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = z[j];
+    if constexpr (kAct == PE_ACT_RELU) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = z[j] < 0.f ? 0.f : z[j];
+    } else if constexpr (kAct >= PE_ACT_GELU) {
+      if (e.out_fp32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = gelu_fp32(z[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+          f2_split(GeluPair(z[j], z[j + 1]).value(z[j], z[j + 1]), y[j], y[j + 1]);
+      }
+      if constexpr (kGeglu) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] *= u[j];
+      }
+    }
+    if (e.residual) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] += r[j];
+    }
+    if (e.pre) {
+      put(e.pre, row * e.pre_ld + col, z, four);
+      if (kGeglu) put(e.pre, row * e.pre_ld + e.n + col, u, four && e.n % 4 == 0);
+    }
+    put(e.out, row * e.out_ld + col, y, four);
+  }
+};
 
 }  // namespace sm103
 }  // namespace pe

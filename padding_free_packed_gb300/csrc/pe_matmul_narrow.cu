@@ -8,12 +8,15 @@
 // second launch). An accumulator sums four blocks of k, which four warps then add to fp32
 // sums in registers (the tensor cores cut a sum off after every 16 products); at the end they
 // copy them to shared memory, and the cluster's CTAs deal out the rows among them: a lane
-// adds four neighbouring columns, finishes them and writes them.
+// adds four neighbouring columns, finishes them and writes them. That part is one warp a
+// scheduler or two, so it is bound by its instructions, not by memory: the activation is a
+// template's, and all eight warps take part.
 // With geglu the tile's rows of b are 64 of the gate's and the same 64 of the up part's.
 //
-//   warps 0-3   sums to shared memory; join and epilogue
+//   warps 0-3   sums to shared memory
 //   warp 4      TMA producer
 //   warp 5      MMA issue
+//   all         join and epilogue
 #include "pe_matmul.cuh"
 
 namespace pe {
@@ -22,14 +25,14 @@ namespace {
 
 using namespace sm103;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kMaxSplit = 8;
 constexpr int kChunk = 4;                 // blocks of k that one accumulator sums
 constexpr uint32_t kBBytes = 128 * 128;
 
 // Blocks in flight: two CTAs share an SM.
 template <int kT>
-constexpr int kStages = kT == 64 ? 4 : 5;
+constexpr int kStages = kT == 64 ? 4 : kT == 32 ? 5 : 6;
 
 template <int kT>
 struct alignas(1024) Smem {
@@ -83,11 +86,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-template <int kT, bool kGeglu>
-__global__ void __launch_bounds__(kThreads)
+template <int kT, int kAct>
+__global__ void __launch_bounds__(kThreads, 2)
 matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
                      const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ Params p) {
   constexpr int S = kStages<kT>;
+  constexpr bool kGeglu = kAct == PE_ACT_GEGLU;
   constexpr uint32_t kTmemCols = 2 * kT;
   constexpr int32_t kOutCols = kGeglu ? 64 : 128;          // of a tile
   extern __shared__ uint8_t raw[];
@@ -193,7 +197,7 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
     }
     tc_commit_warp(smem_u32(&s.drain));    // no MMA is in flight past this
     mbar_drain_wait(smem_u32(&s.drain), 0);
-  } else {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ sums
     float sum[kT];
 #pragma unroll
@@ -236,51 +240,70 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
       for (int c = 0; c < kT; ++c) s.sums[c][threadIdx.x] = sum[c];
     }
   }
+  griddep_launch_dependents();             // the next kernel may come to wait for this one
   tc_fence_before();
   if (p.split == 1)
     __syncthreads();
   else
     cluster_sync();
   // ---------------------------------------------------------------- join and epilogue
-  if (warp < 4) {
-    constexpr int kLanes = kOutCols / 4;                   // of a row
-    constexpr int kRowsWarp = 32 / kLanes;                 // rows of a warp at a time
-    const int at = 4 * (lane % kLanes);
-    const int32_t col = col0 + at;
+  constexpr int kLanes = kOutCols / 4;                     // of a row
+  constexpr int kRowsWarp = 32 / kLanes;                   // rows of a warp at a time
+  constexpr int kFlight = 4;                               // of them in flight
+  const int at = 4 * (lane % kLanes);
+  const int32_t col = col0 + at;
+  if (col < p.e.n) {
+    const Finish4<kAct> finish(p.e, col);
     const int32_t rank = p.split == 1 ? 0 : (int32_t)cluster_rank();
     const int32_t rows = p.e.m - row0 < kT ? p.e.m - row0 : kT;
-    const int32_t step = 4 * kRowsWarp * p.split;
-    for (int32_t c = (rank * 4 + warp) * kRowsWarp + lane / kLanes; c < rows; c += step) {
-      if (col >= p.e.n) break;
-      float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-      auto add = [&](float (&to)[4], const float4& v) {
-        to[0] += v.x;
-        to[1] += v.y;
-        to[2] += v.z;
-        to[3] += v.w;
-      };
-      if (p.split == 1) {
-        add(z, *reinterpret_cast<const float4*>(&s.sums[c][at]));
-        if constexpr (kGeglu) add(u, *reinterpret_cast<const float4*>(&s.sums[c][64 + at]));
-      } else {
-        const uint32_t from = smem_u32(&s.sums[c][at]);
-        float4 v[kMaxSplit], w[kGeglu ? kMaxSplit : 1];
+    const int32_t step = 8 * kRowsWarp * p.split;
+    for (int32_t c0 = (rank * 8 + warp) * kRowsWarp + lane / kLanes; c0 < rows;
+         c0 += kFlight * step) {
+      float residual[kFlight][4];
+      float4 z[kFlight], u[kFlight];
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) {              // all parts in flight
-          if (r < p.split) {
-            v[r] = load_cluster_f32x4(peer_address(from, r));
-            if constexpr (kGeglu) w[r] = load_cluster_f32x4(peer_address(from + 256, r));
+      for (int i = 0; i < kFlight; ++i) {
+        const int32_t c = c0 + i * step;
+        z[i] = u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < rows && p.e.residual) finish.residual(row0 + c, residual[i]);
+      }
+      // The cluster's parts in the order of k, those of all rows in flight.
+#pragma unroll 2
+      for (int32_t r = 0; r < p.split; ++r) {
+        float4 v[kFlight], w[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int32_t c = c0 + i * step;
+          if (c < rows) {
+            if (p.split == 1) {
+              v[i] = *reinterpret_cast<const float4*>(&s.sums[c][at]);
+              if constexpr (kGeglu) w[i] = *reinterpret_cast<const float4*>(&s.sums[c][64 + at]);
+            } else {
+              const uint32_t there = peer_address(smem_u32(&s.sums[c][at]), r);
+              v[i] = load_cluster_f32x4(there);
+              if constexpr (kGeglu) w[i] = load_cluster_f32x4(there + 256);
+            }
           }
         }
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) {
-          if (r < p.split) {
-            add(z, v[r]);
-            if constexpr (kGeglu) add(u, w[r]);
+        for (int i = 0; i < kFlight; ++i) {
+          if (c0 + i * step < rows) {
+            z[i].x += v[i].x;
+            z[i].y += v[i].y;
+            z[i].z += v[i].z;
+            z[i].w += v[i].w;
+            if constexpr (kGeglu) {
+              u[i].x += w[i].x;
+              u[i].y += w[i].y;
+              u[i].z += w[i].z;
+              u[i].w += w[i].w;
+            }
           }
         }
       }
-      finish4(p.e, row0 + c, col, p.e.n - col, z, u);
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i)
+        if (c0 + i * step < rows) finish.row(row0 + c0 + i * step, z[i], u[i], residual[i]);
     }
   }
   if (p.split > 1) cluster_sync();         // the sums have been read by the whole cluster
@@ -290,8 +313,9 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
   }
 }
 
-template <int kT, bool kGeglu>
+template <int kT, int kAct>
 pe_status launch(const Matmul& q, int32_t split, DeviceStatus* status, cudaStream_t stream) {
+  constexpr bool kGeglu = kAct == PE_ACT_GEGLU;
   CUtensorMap ma, mb;
   auto map = [&](CUtensorMap* to, const MatmulOperand& x, int32_t rows, uint32_t box) {
     const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -315,7 +339,7 @@ pe_status launch(const Matmul& q, int32_t split, DeviceStatus* status, cudaStrea
   p.wait_limit_ns = wait_limit_ns();
   const size_t smem = sizeof(Smem<kT>) + 1024;
   static_assert(2 * (sizeof(Smem<kT>) + 2048) <= 227 * 1024, "two CTAs share an SM");
-  const auto kernel = matmul_narrow_kernel<kT, kGeglu>;
+  const auto kernel = matmul_narrow_kernel<kT, kAct>;
   PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(smem)));
   cudaLaunchConfig_t cfg = {};
@@ -339,8 +363,12 @@ pe_status launch(const Matmul& q, int32_t split, DeviceStatus* status, cudaStrea
 
 template <int kT>
 pe_status launch_rows(const Matmul& q, int32_t split, DeviceStatus* status, cudaStream_t stream) {
-  return q.e.act == PE_ACT_GEGLU ? launch<kT, true>(q, split, status, stream)
-                                 : launch<kT, false>(q, split, status, stream);
+  switch (q.e.act) {
+    case PE_ACT_GEGLU: return launch<kT, PE_ACT_GEGLU>(q, split, status, stream);
+    case PE_ACT_GELU: return launch<kT, PE_ACT_GELU>(q, split, status, stream);
+    case PE_ACT_RELU: return launch<kT, PE_ACT_RELU>(q, split, status, stream);
+    default: return launch<kT, PE_ACT_NONE>(q, split, status, stream);
+  }
 }
 
 }  // namespace

@@ -52,11 +52,11 @@ constexpr uint32_t kOperandBytes = kRows * 128;          // 16 KiB
 constexpr uint32_t kPairBytes = 4 * kOperandBytes;       // both CTAs' a and b of one block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBoxBytes = 32 * 128;                 // 32 rows of 128 bytes
-// How rows of out, residual and pre are moved: boxes by TMA or, where rows start anywhere,
-// element by element.
+// How rows of out, residual and pre move between a warp's box and memory: by TMA or, where
+// rows start anywhere, by the warp's lanes.
 enum Out { kOutBf16 = 0, kOutFp32 = 1, kOutBf16Anywhere = 2, kOutFp32Anywhere = 3 };
 constexpr bool is_fp32(int out) { return out & 1; }
-constexpr bool by_boxes(int out) { return out < 2; }
+constexpr bool by_tma(int out) { return out < 2; }
 
 constexpr uint32_t kRegsLaunch = 168;
 constexpr uint32_t kRegsLow = 40, kRegsHigh = 232;
@@ -289,30 +289,76 @@ __device__ __forceinline__ void add_row(uint32_t row, int chunk, float (&x)[32])
   }
 }
 
-// 32 columns of the warp's 32 rows through a box, then row by row, element by element: a
-// row's 32 columns are consecutive. `cols` of them exist.
+// A box to rows that start anywhere: a row's 128 bytes are 32 consecutive words, one a lane.
+// Where a bf16 row starts in the middle of a word, lane l writes columns 2 l - 1 and 2 l in
+// one word, and the first and last columns go alone. `rows` and `cols` of the box exist.
 template <bool kFp32>
-__device__ __forceinline__ void put_anywhere(const Params& p, uint32_t box, int lane,
-                                             const float (&x)[32], const void* residual,
-                                             int64_t residual_ld, void* out, int64_t out_ld,
-                                             int32_t row0, int64_t col0, int32_t cols) {
-  __syncwarp();
-  put_row<kOutFp32>(box + lane * 128 + ((lane & 7) << 4), 0, x);
-  __syncwarp();
-  const int32_t rows = lane < cols ? p.e.m - row0 : 0;
+__device__ __forceinline__ void box_to_rows(uint32_t box, int lane, void* out, int64_t ld,
+                                            int64_t row0, int64_t col0, int32_t rows,
+                                            int32_t cols) {
+  if (cols <= 0) return;
 #pragma unroll 1
-  for (int32_t r0 = 0; r0 < 32; r0 += 8) {               // eight reads in flight
-    float v[8];
+  for (int r0 = 0; r0 < 32 && r0 < rows; r0 += 8) {
+    uint32_t w[8];
 #pragma unroll
-    for (int32_t r = 0; r < 8; ++r) {
-      v[r] = load_shared_f32(box + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4);
-      if (residual && r0 + r < rows)
-        v[r] += io_get(residual, (int64_t)(row0 + r0 + r) * residual_ld + col0 + lane, kFp32);
+    for (int i = 0; i < 8; ++i)
+      w[i] = __float_as_uint(
+          load_shared_f32(box + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4) + (lane & 3) * 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i >= rows) break;
+      const int64_t at = (row0 + r0 + i) * ld + col0;
+      if constexpr (kFp32) {
+        if (lane < cols) static_cast<uint32_t*>(out)[at + lane] = w[i];
+      } else {
+        uint16_t* to = static_cast<uint16_t*>(out) + at;
+        const int shift = (int)(reinterpret_cast<uintptr_t>(to) >> 1 & 1);   // the warp's
+        const uint32_t before = __shfl_up_sync(0xffffffffu, w[i], 1);
+        const uint32_t word = shift ? (before >> 16) | (w[i] << 16) : w[i];
+        const int32_t c = 2 * lane - shift;              // the word's first column
+        if (c >= 0 && c + 1 < cols) {
+          *reinterpret_cast<uint32_t*>(to + c) = word;
+        } else {
+          if (c >= 0 && c < cols) to[c] = (uint16_t)word;
+          if (c < 0) to[0] = (uint16_t)(word >> 16);
+        }
+        if (shift && lane == 31 && cols > 63) to[63] = (uint16_t)(w[i] >> 16);
+      }
+    }
+  }
+}
+// The same the other way: the residual's rows into a box.
+template <bool kFp32>
+__device__ __forceinline__ void rows_to_box(uint32_t box, int lane, const void* in, int64_t ld,
+                                            int64_t row0, int64_t col0, int32_t rows,
+                                            int32_t cols) {
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32 && r0 < rows; r0 += 8) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = 0;
+      if (r0 + i < rows) {
+        const int64_t at = (row0 + r0 + i) * ld + col0;
+        if constexpr (kFp32) {
+          if (lane < cols) w[i] = static_cast<const uint32_t*>(in)[at + lane];
+        } else {
+          const uint16_t* from = static_cast<const uint16_t*>(in) + at + 2 * lane;
+          if (2 * lane + 1 < cols && (reinterpret_cast<uintptr_t>(from) & 2) == 0) {
+            w[i] = *reinterpret_cast<const uint32_t*>(from);
+          } else {
+            if (2 * lane < cols) w[i] = from[0];
+            if (2 * lane + 1 < cols) w[i] |= (uint32_t)from[1] << 16;
+          }
+        }
+      }
     }
 #pragma unroll
-    for (int32_t r = 0; r < 8; ++r)
-      if (r0 + r < rows)
-        io_put(out, (int64_t)(row0 + r0 + r) * out_ld + col0 + lane, kFp32, v[r]);
+    for (int i = 0; i < 8; ++i)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(box + (r0 + i) * 128 +
+                                                   (((lane >> 2) ^ i) << 4) + (lane & 3) * 4),
+                   "r"(w[i])
+                   : "memory");
   }
 }
 
@@ -543,7 +589,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
     uint32_t box_parity = 0;
     constexpr int kUnits = kGeglu ? 2 : 4;                      // of 32 columns of out
     constexpr int kPerBox = is_fp32(kOut) ? 1 : 2;              // units in a box
-    const bool ahead = by_boxes(kOut) && p.e.residual && !p.e.pre;
+    const bool ahead = by_tma(kOut) && p.e.residual && !p.e.pre;
     int32_t turn = 0;                      // of the accumulators
     bool ok = true;
     Walk w;
@@ -563,10 +609,8 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         loading = true;
       };
       auto take = [&]() {                  // the box that left before has been read
-        if (by_boxes(kOut)) {
-          if (lane == 0) bulk_wait_read();
-          __syncwarp();
-        }
+        if (by_tma(kOut) && lane == 0) bulk_wait_read();
+        __syncwarp();
       };
       if (stored && ok && ahead) {
         take();
@@ -656,12 +700,19 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         if (!is_fp32(kOut)) hand_back(buf);
         continue;
       }
-      auto leave = [&](const CUtensorMap* map, int32_t col) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && col < p.e.n) {
-          tma_store_2d(map, box, col, row0);
-          bulk_commit();
+      // The box to columns `col` .. of a tensor (its map; its address and rows, of p.e.n
+      // columns from there on).
+      auto leave = [&](const CUtensorMap* map, void* to, int64_t ld, int32_t col) {
+        if constexpr (by_tma(kOut)) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && col < p.e.n) {
+            tma_store_2d(map, box, col, row0);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          box_to_rows<is_fp32(kOut)>(box, lane, to, ld, row0, col, p.e.m - row0, p.e.n - col);
         }
       };
       // Loops over the accumulator's columns stay loops where the sums are not in registers:
@@ -674,16 +725,12 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
             float z[32];
             load(part * 2 + u, z);
             add_bias(bias + part * 64 + u * 32, z);
-            const int32_t col = col0 + u * 32;
-            if constexpr (!by_boxes(kOut)) {
-              put_anywhere<is_fp32(kOut)>(p, box, lane, z, nullptr, 0, p.e.pre, p.e.pre_ld, row0,
-                           (int64_t)part * p.e.n + col, p.e.n - col);
-            } else {
-              if (u % kPerBox == 0) take();
-              put_row<kOut>(box_row, u % kPerBox * 4, z);
-              if (u % kPerBox == kPerBox - 1)
-                leave(part ? &maps.pre_up : &maps.pre, col0 + u / kPerBox * kPerBox * 32);
-            }
+            if (u % kPerBox == 0) take();
+            put_row<kOut>(box_row, u % kPerBox * 4, z);
+            if (u % kPerBox == kPerBox - 1)
+              leave(part ? &maps.pre_up : &maps.pre,
+                    static_cast<char*>(p.e.pre) + (int64_t)part * p.e.n * (is_fp32(kOut) ? 4 : 2),
+                    p.e.pre_ld, col0 + u / kPerBox * kPerBox * 32);
           }
         }
       }
@@ -710,24 +757,26 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
             for (int i = 0; i < 32; ++i) y[i] = y[i] < 0.f ? 0.f : y[i];
           }
         }
-        if constexpr (!by_boxes(kOut)) {
-          put_anywhere<is_fp32(kOut)>(p, box, lane, y, p.e.residual, p.e.residual_ld, p.e.out,
-                                      p.e.out_ld, row0, col, p.e.n - col);
-        } else {
-          if (u % kPerBox == 0) {
-            if (!loading) take();
-            if (p.e.residual && col < p.e.n) {
+        if (u % kPerBox == 0) {
+          if (!loading) take();
+          if (p.e.residual && col < p.e.n) {
+            if constexpr (by_tma(kOut)) {
               if (!loading) load_residual(col);
               ok = eager_warp_wait(box_bar, box_parity, guard, p.status, kSiteResidual);
               if (!ok) break;
               loading = false;
               box_parity ^= 1;
+            } else {
+              rows_to_box<is_fp32(kOut)>(box, lane, p.e.residual, p.e.residual_ld, row0, col,
+                                         p.e.m - row0, p.e.n - col);
+              __syncwarp();
             }
           }
-          if (p.e.residual) add_row<kOut>(box_row, u % kPerBox * 4, y);
-          put_row<kOut>(box_row, u % kPerBox * 4, y);
-          if (u % kPerBox == kPerBox - 1) leave(&maps.out, col0 + u / kPerBox * kPerBox * 32);
         }
+        if (p.e.residual) add_row<kOut>(box_row, u % kPerBox * 4, y);
+        put_row<kOut>(box_row, u % kPerBox * 4, y);
+        if (u % kPerBox == kPerBox - 1)
+          leave(&maps.out, p.e.out, p.e.out_ld, col0 + u / kPerBox * kPerBox * 32);
       }
       if (!ok) {                           // the residual did not come in time
         if (lane == 0) mbar_drain_wait(box_bar, box_parity);
@@ -737,6 +786,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
     bulk_wait_all();
   }
 
+  griddep_launch_dependents();             // the next kernel may come to wait for this one
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -793,9 +843,10 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
 // Adds the slices' sums of every tile, in the order of k, and finishes them; without slices,
 // finishes zeros. One block per 32 rows x 128 columns of the accumulator (64 of the gate, 64
 // of the up part with geglu); parts are column-group-major.
-template <bool kGeglu>
+template <int kAct>
 __global__ void __launch_bounds__(256)
 matmul_parts_kernel(const __grid_constant__ Params p) {
+  constexpr bool kGeglu = kAct == PE_ACT_GEGLU;
   constexpr int32_t kOutCols = kGeglu ? kTile / 2 : kTile;
   __shared__ float tile[32][132];
   griddep_wait();                                        // before any block may leave
@@ -838,15 +889,26 @@ matmul_parts_kernel(const __grid_constant__ Params p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(&tile[row][4 * (g0 + 8 * i)]) = sum[i];
   __syncthreads();
-  // Four columns of out a thread.
-  constexpr int kGroups = kGeglu ? 16 : 32;
-  for (int e = threadIdx.x; e < 32 * kGroups; e += 256) {
-    const int r = e / kGroups, c = 4 * (e % kGroups);
-    if (row0 + r < p.e.m && col0 + c < p.e.n) {
-      const float4 z = *reinterpret_cast<const float4*>(&tile[r][c]);
-      const float4 u = *reinterpret_cast<const float4*>(&tile[r][kGeglu ? c + 64 : c]);
-      const float zs[4] = {z.x, z.y, z.z, z.w}, us[4] = {u.x, u.y, u.z, u.w};
-      finish4(p.e, row0 + r, col0 + c, p.e.n - col0 - c, zs, us);
+  // Four columns of out a thread, the same in all of its rows.
+  constexpr int kGroups = kGeglu ? 16 : 32, kStep = 256 / kGroups;
+  const int c = 4 * (threadIdx.x % kGroups);
+  if (col0 + c >= p.e.n) return;
+  const Finish4<kAct> finish(p.e, col0 + c);
+  constexpr int kFlight = 4;
+  for (int r0 = threadIdx.x / kGroups; r0 < 32; r0 += kFlight * kStep) {
+    float residual[kFlight][4];
+    if (p.e.residual) {
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i)
+        if (r0 + i * kStep < 32 && row0 + r0 + i * kStep < p.e.m)
+          finish.residual(row0 + r0 + i * kStep, residual[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int r = r0 + i * kStep;
+      if (r < 32 && row0 + r < p.e.m)
+        finish.row(row0 + r, *reinterpret_cast<const float4*>(&tile[r][c]),
+                   *reinterpret_cast<const float4*>(&tile[r][kGeglu ? c + 64 : c]), residual[i]);
     }
   }
 }
@@ -872,10 +934,12 @@ Params base_params(const Matmul& q, int pairs) {
   return p;
 }
 
-template <bool kGeglu>
 pe_status launch_parts(const Params& p, cudaStream_t stream) {
-  return launch_after_previous(matmul_parts_kernel<kGeglu>, dim3((unsigned)(16 * p.tiles)),
-                               dim3(256), 0, stream, p);
+  const auto kernel = p.e.act == PE_ACT_GEGLU  ? matmul_parts_kernel<PE_ACT_GEGLU>
+                      : p.e.act == PE_ACT_GELU ? matmul_parts_kernel<PE_ACT_GELU>
+                      : p.e.act == PE_ACT_RELU ? matmul_parts_kernel<PE_ACT_RELU>
+                                               : matmul_parts_kernel<PE_ACT_NONE>;
+  return launch_after_previous(kernel, dim3((unsigned)(16 * p.tiles)), dim3(256), 0, stream, p);
 }
 
 pe_status operand_map(CUtensorMap* map, const MatmulOperand& x, int32_t rows, int32_t k,
@@ -935,8 +999,7 @@ size_t matmul_tiles_workspace(int64_t tiles, int32_t slices) {
 }
 
 pe_status matmul_no_sum(const Matmul& q, cudaStream_t stream) {
-  const Params p = base_params(q, 1);
-  return q.e.act == PE_ACT_GEGLU ? launch_parts<true>(p, stream) : launch_parts<false>(p, stream);
+  return launch_parts(base_params(q, 1), stream);
 }
 
 pe_status matmul_tiles(const Matmul& q, int32_t pairs, int32_t slices, void* workspace,
@@ -976,8 +1039,7 @@ pe_status matmul_tiles(const Matmul& q, int32_t pairs, int32_t slices, void* wor
                  : launch_out<false, 2>(tma, maps, p, stream);
   PE_TRY((geglu ? launch_out<true, 1>(tma, maps, p, stream)
                 : launch_out<false, 1>(tma, maps, p, stream)));
-  if (slices == 1) return PE_OK;
-  return geglu ? launch_parts<true>(p, stream) : launch_parts<false>(p, stream);
+  return slices == 1 ? PE_OK : launch_parts(p, stream);
 }
 
 }  // namespace pe
