@@ -399,8 +399,8 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  * nothing allocated, nothing read back, capturable in a CUDA graph. Tensors are
  * contiguous unless a stride is given. Results are bitwise the same in every
  * run. Workspaces are device memory, 16-byte aligned, of the size that the
- * *_workspace_size call gives, else PE_ERR_WORKSPACE; two calls that may run at
- * the same time need one each.
+ * *_workspace_size call gives (or NULL where that is 0), else PE_ERR_WORKSPACE;
+ * two calls that may run at the same time need one each.
  * ------------------------------------------------------------------------ */
 
 /* The dense products of a layer, with what follows them in the same pass:
@@ -454,7 +454,7 @@ pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int a_transpose
  * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
  * finite and > 0, NULL required pointers; PE_ERR_UNSUPPORTED for other dtypes or
  * devices and more than 16384 channels. */
-size_t pe_layernorm_bwd_workspace_size(int32_t channels);
+size_t pe_layernorm_bwd_workspace_size(int64_t num_tokens, int32_t channels);
 pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void* h, const void* weight,
                            const void* dresidual, int64_t num_tokens, int32_t channels, float eps,
                            void* dx, float* dweight, float* dbias, void* workspace,
@@ -473,7 +473,7 @@ pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void* h, const 
  * activation, NULL required pointers or ones that have to be NULL, dz = dy with
  * PE_ACT_GEGLU; PE_ERR_OVERFLOW for 2^30 - 1024 features or more;
  * PE_ERR_UNSUPPORTED for other dtypes or devices. */
-size_t pe_activation_bwd_workspace_size(pe_activation activation, int32_t features);
+size_t pe_activation_bwd_workspace_size(pe_activation activation, int64_t rows, int32_t features);
 pe_status pe_activation_bwd(pe_dtype dtype, pe_activation activation, const void* dy,
                             const void* pre, int64_t rows, int32_t features, void* dz,
                             float* dbias, void* workspace, size_t workspace_bytes,

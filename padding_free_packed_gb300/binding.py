@@ -9,6 +9,7 @@ fallback: if libpe.so is missing or the device is not sm_103a the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -137,12 +138,12 @@ def load_library(path: str = LIB_PATH):
     lib.pe_matmul_fp8.argtypes = [c.c_int, vp, i64, vp, c.c_int, vp, i64, vp, i64, i64, i64,
                                   c.c_int, vp, vp, sz, vp]
     lib.pe_matmul_fp8.restype = c.c_int
-    lib.pe_layernorm_bwd_workspace_size.argtypes = [i32]
+    lib.pe_layernorm_bwd_workspace_size.argtypes = [i64, i32]
     lib.pe_layernorm_bwd_workspace_size.restype = sz
     lib.pe_layernorm_bwd.argtypes = [c.c_int, vp, vp, vp, vp, i64, i32, c.c_float, vp, vp, vp, vp,
                                      sz, vp]
     lib.pe_layernorm_bwd.restype = c.c_int
-    lib.pe_activation_bwd_workspace_size.argtypes = [c.c_int, i32]
+    lib.pe_activation_bwd_workspace_size.argtypes = [c.c_int, i64, i32]
     lib.pe_activation_bwd_workspace_size.restype = sz
     lib.pe_activation_bwd.argtypes = [c.c_int, c.c_int, vp, vp, i64, i32, vp, vp, vp, sz, vp]
     lib.pe_activation_bwd.restype = c.c_int
@@ -621,6 +622,12 @@ def _output(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Te
     return t
 
 
+def _like(t: torch.Tensor | None, name: str, like: torch.Tensor) -> torch.Tensor:
+    """The caller's output tensor after a check, or a new one like the contiguous `like`."""
+    return torch.empty_like(like) if t is None else _output(t, name, like.shape, like.dtype,
+                                                            like.device)
+
+
 def _two_dims(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
@@ -864,6 +871,11 @@ def _row_tensor(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     return ld if rows > 1 else cols
 
 
+@functools.lru_cache(maxsize=4096)
+def _matmul_workspace(*sizes) -> int:
+    return load_library().pe_matmul_workspace_size(*sizes)
+
+
 def pe_matmul(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None,
               activation="none", residual: torch.Tensor | None = None, dtype=None, out=None,
               pre=None, a_transposed: bool = False, b_transposed: bool = False, workspace=None):
@@ -874,7 +886,6 @@ def pe_matmul(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None
     N], a b^T + bias is also written there. bias, residual and pre are in out's dtype. out
     may be residual; out, residual and pre may be parts of wider matrices. bf16 operands
     whose rows do not start at multiples of 16 bytes are copied first."""
-    lib = load_library()
     act = _activation_code(activation)
     a, a_ld = _operand(a, "a")
     b, b_ld = _operand(b, "b")
@@ -901,7 +912,7 @@ def pe_matmul(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None
         residual_ld = _row_tensor(residual, "residual", (m, wide), out.dtype, dev)
     if pre is not None:
         pre_ld = _row_tensor(pre, "pre", (m, n), out.dtype, dev)
-    need = lib.pe_matmul_workspace_size(code, a_transposed, b_transposed, m, n, k, act)
+    need = _matmul_workspace(code, bool(a_transposed), bool(b_transposed), m, n, k, act)
     ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
     _call("pe_matmul", dev, code, a.data_ptr(), a_ld, a_transposed, b.data_ptr(), b_ld,
           b_transposed, m, n, k, _ptr(bias), act, _ptr(residual), residual_ld, out_code,
@@ -922,13 +933,14 @@ def pe_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
     weight = _norm_weight(weight, h, c)
     if dresidual is not None:
         dresidual = _input(dresidual, "dresidual", h, h.shape)
-    dx = _output(out, "out", h.shape, h.dtype, h.device)
-    sums = torch.empty((2, c), dtype=torch.float32, device=h.device)
-    dweight, dbias = sums[0], sums[1]
-    ws, ws_bytes = _workspace_for(workspace, lib.pe_layernorm_bwd_workspace_size(c), h.device)
-    _call("pe_layernorm_bwd", h.device, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
+    dev = h.device
+    dx = _like(out, "out", h)
+    dweight, dbias = torch.empty((2, c), dtype=torch.float32, device=dev).unbind()
+    need = lib.pe_layernorm_bwd_workspace_size(n, c)
+    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
+    _call("pe_layernorm_bwd", dev, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
           weight.data_ptr(), _ptr(dresidual), n, c, float(eps), dx.data_ptr(),
-          dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), ws_bytes)
+          dweight.data_ptr(), dbias.data_ptr(), _ptr(ws), ws_bytes)
     return dx, dweight, dbias
 
 
@@ -952,13 +964,15 @@ def pe_activation_bwd(dy: torch.Tensor, pre: torch.Tensor | None, activation="no
         if pre is None:
             raise ValueError("pre is what went into the activation")
         pre = _input(pre, "pre", dy, (n, wide))
-        dz = _output(out, "out", (n, wide), dy.dtype, dy.device)
-    dbias = torch.empty(wide, dtype=torch.float32, device=dy.device) if need_dbias else None
-    ws, ws_bytes = None, 0
+        dz = _like(out, "out", pre)
+    dev = dy.device
+    dbias, ws, ws_bytes = None, None, 0
     if need_dbias:
-        ws, ws_bytes = _workspace_for(workspace, lib.pe_activation_bwd_workspace_size(act, f),
-                                      dy.device)
-    _call("pe_activation_bwd", dy.device, _dtype_code(dy.dtype), act, dy.data_ptr(), _ptr(pre), n,
+        dbias = torch.empty(wide, dtype=torch.float32, device=dev)
+        need = lib.pe_activation_bwd_workspace_size(act, n, f)
+        if need:
+            ws, ws_bytes = _workspace_for(workspace, need, dev)
+    _call("pe_activation_bwd", dev, _dtype_code(dy.dtype), act, dy.data_ptr(), _ptr(pre), n,
           f, _ptr(dz), _ptr(dbias), _ptr(ws), ws_bytes)
     return (dy if act == 0 else dz), dbias
 
@@ -980,7 +994,7 @@ def pe_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
             raise ValueError(f"device_offset must be one int64 on {x.device}")
     if not (0 <= seed < 2 ** 64 and 0 <= offset < 2 ** 64):
         raise ValueError("seed and offset must be from 0 to 2**64 - 1")
-    y = _output(out, "out", x.shape, x.dtype, x.device)
+    y = _like(out, "out", x)
     _call("pe_dropout", x.device, _dtype_code(x.dtype), x.data_ptr(), _ptr(residual), x.numel(),
           float(p), int(seed), int(offset), _ptr(device_offset), y.data_ptr())
     return y
@@ -1002,6 +1016,19 @@ def _rope_rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> 
     return t
 
 
+def _rope_target(out: torch.Tensor | None, name: str, src: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(src.shape, dtype=src.dtype, device=src.device)
+    if out.shape != src.shape:
+        raise ValueError(f"{name} must have shape {tuple(src.shape)}")
+    return _rope_rows(out, name, src)
+
+
+@functools.lru_cache(maxsize=256)
+def _int32_array(numbers: tuple):
+    return (ctypes.c_int32 * len(numbers))(*(int(x) for x in numbers))
+
+
 def pe_rope_axes(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, sections,
                  theta: float, per_axis: bool = False, inverse: bool = False, out_q=None,
                  out_k=None):
@@ -1011,37 +1038,29 @@ def pe_rope_axes(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     axis's s. `inverse` turns back (the backward). q and k may be views whose tokens lie
     further apart, such as parts of one buffer of q, k and v. Returns (q, k) turned, in new
     contiguous tensors or in out_q and out_k (q and k themselves, for in place)."""
-    load_library()
     q = _rope_rows(q, "q")
-    sections = [int(s) for s in sections]
     n, hq, d = q.shape
+    dev = q.device
+    sections = tuple(sections)
+    axes = len(sections)
+    if positions.dtype is not torch.int32 or positions.shape != (axes, n) or (
+            positions.device != dev):
+        raise ValueError(f"positions must be int32 of shape {(axes, n)} on {dev}")
+    if not positions.is_contiguous():
+        positions = positions.contiguous()
+    out_q = _rope_target(out_q, "out_q", q)
+    hk = k_step = out_k_step = 0
     if k is not None:
         k = _rope_rows(k, "k", q)
+        hk = k.shape[1]
         if k.shape[0] != n or k.shape[2] != d:
             raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
-    if positions.dtype != torch.int32 or positions.shape != (len(sections), n) or (
-            positions.device != q.device):
-        raise ValueError(f"positions must be int32 of shape {(len(sections), n)} on {q.device}")
-    positions = positions.contiguous()
-
-    def target(out, src, name):
-        if src is None:
-            if out is not None:
-                raise ValueError(f"{name} needs its input")
-            return None
-        if out is None:
-            return torch.empty(src.shape, dtype=src.dtype, device=src.device)
-        if out.shape != src.shape:
-            raise ValueError(f"{name} must have shape {tuple(src.shape)}")
-        return _rope_rows(out, name, src)
-
-    def rows(t):                                 # heads and their stride from token to token
-        return (0, 0) if t is None else (t.shape[1], max(t.stride(0), t.shape[1] * d))
-
-    out_q, out_k = target(out_q, q, "out_q"), target(out_k, k, "out_k")
-    (_, q_step), (hk, k_step) = rows(q), rows(k)
-    _call("pe_rope_axes", q.device, _dtype_code(q.dtype), q.data_ptr(), q_step,
-          out_q.data_ptr(), rows(out_q)[1], hq, _ptr(k), k_step, _ptr(out_k), rows(out_k)[1], hk,
-          positions.data_ptr(), (ctypes.c_int32 * len(sections))(*sections), len(sections), n, d,
-          float(theta), int(bool(per_axis)), int(bool(inverse)))
+        out_k = _rope_target(out_k, "out_k", k)
+        k_step, out_k_step = max(k.stride(0), hk * d), max(out_k.stride(0), hk * d)
+    elif out_k is not None:
+        raise ValueError("out_k needs k")
+    _call("pe_rope_axes", dev, _dtype_code(q.dtype), q.data_ptr(), max(q.stride(0), hq * d),
+          out_q.data_ptr(), max(out_q.stride(0), hq * d), hq, _ptr(k), k_step, _ptr(out_k),
+          out_k_step, hk, positions.data_ptr(), _int32_array(sections), axes, n, d, float(theta),
+          int(bool(per_axis)), int(bool(inverse)))
     return out_q, out_k

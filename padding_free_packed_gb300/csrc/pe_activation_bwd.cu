@@ -26,7 +26,13 @@ struct Args {
   int32_t features;
   T* dz;
   float* part;           // [gridDim.y][columns of z], or null
+  float* dbias;          // few rows: written by the strip's cluster of gridDim.y blocks
 };
+
+// Rows that a cluster of eight blocks takes for each strip of columns, 16 for each of a
+// block's threads (1001 x 333 gelu fp32: one launch 5.5 us, two 8.3).
+constexpr int64_t kFewRows = 16 * kClusterLines * kRowLanes;
+
 
 // V neighbouring columns per access, kRows rows of a thread in flight.
 template <typename T, int V, int kAct, int kRows>
@@ -109,33 +115,58 @@ activation_bwd_kernel(const Args<T> a) {
       }
     }
   }
-  if (!a.part) return;
+  if (!a.part && !a.dbias) return;
   griddep_launch_dependents();                 // the second kernel may come to wait for this one
 #pragma unroll
   for (int p = 0; p < kParts; ++p)
 #pragma unroll
     for (int v = 0; v < V; ++v) sums[y][p][x * V + v] = sum[p][v];
   __syncthreads();
+  __shared__ float line[kParts * kLanes * V];  // this block's sums of the strip's columns
   for (int e = threadIdx.x; e < kParts * kLanes * V; e += kThreads) {
     const int p = e / (kLanes * V), at = e % (kLanes * V);
     const int32_t col = blockIdx.x * kLanes * V + at;
-    if (col < F) {
-      float total = 0.f;
+    float total = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRowLanes; ++i) total += sums[i][p][at];
+    for (int i = 0; i < kRowLanes; ++i) total += sums[i][p][at];
+    if (!a.part)
+      line[e] = total;
+    else if (col < F)
       a.part[(int64_t)blockIdx.y * ld + (int64_t)p * F + col] = total;
-    }
   }
+  if (a.part) return;
+  // The strip's gate columns, then its up columns.
+  const int32_t first = blockIdx.x * kLanes * V;
+  const int32_t wide = F - first < kLanes * V ? F - first : kLanes * V;
+  sm103::cluster_sync();                       // every block's line is complete
+  const uint32_t here = sm103::smem_u32(line), blocks = gridDim.y;
+  for (int e = (int)(blockIdx.y * kThreads + threadIdx.x); e < kParts * kLanes * V;
+       e += (int)blocks * kThreads) {
+    const int p = e / (kLanes * V), at = e % (kLanes * V);
+    float total = 0.f;
+    for (uint32_t b = 0; b < blocks; ++b)
+      total += sm103::load_cluster_f32(sm103::peer_address(here + 4 * e, b));
+    if (at < wide) a.dbias[(int64_t)p * F + first + at] = total;
+  }
+  sm103::cluster_sync();                       // the lines have been read
 }
 
 template <typename T, int V, int kAct>
-pe_status launch(const Args<T>& a, float* dbias, cudaStream_t stream) {
+pe_status launch(const Args<T>& a, cudaStream_t stream) {
   // 6 to 8 loads of a thread in flight, with narrow ones more.
   constexpr int kRows = (kAct == PE_ACT_NONE ? 8 : kAct == PE_ACT_GEGLU ? 2 : 4) *
                         (kAct != PE_ACT_NONE && V * sizeof(T) < 16 ? 2 : 1);
   constexpr int kParts = kAct == PE_ACT_GEGLU ? 2 : 1;
   const int64_t strips = ceil_div(a.features, kLanes * V);
   int64_t lines = ceil_div(a.rows, kRowLanes);
+  if (a.dbias && a.rows <= kFewRows) {
+    if (lines > kClusterLines) lines = kClusterLines;
+    Args<T> few = a;
+    few.part = nullptr;
+    return launch_clusters(activation_bwd_kernel<T, V, kAct, kRows>,
+                           dim3((unsigned)strips, (unsigned)lines), dim3(1, (unsigned)lines),
+                           kThreads, 0, stream, few);
+  }
   const int64_t most = ceil_div((int64_t)device_sm_count() * 8, strips);
   if (lines > most) lines = most;
   if (lines > kMaxBlocks) lines = kMaxBlocks;
@@ -143,16 +174,16 @@ pe_status launch(const Args<T>& a, float* dbias, cudaStream_t stream) {
       <<<dim3((unsigned)strips, (unsigned)lines), kThreads, 0, stream>>>(a);
   PE_CUDA_TRY(cudaGetLastError());
   if (!a.part) return PE_OK;
-  return launch_sum_parts(a.part, (int32_t)lines, kParts * a.features, dbias, 0, nullptr, stream);
+  return launch_sum_parts(a.part, (int32_t)lines, kParts * a.features, a.dbias, 0, nullptr, stream);
 }
 
 template <typename T, int V>
-pe_status launch_act(int act, const Args<T>& a, float* dbias, cudaStream_t stream) {
+pe_status launch_act(int act, const Args<T>& a, cudaStream_t stream) {
   switch (act) {
-    case PE_ACT_GEGLU: return launch<T, V, PE_ACT_GEGLU>(a, dbias, stream);
-    case PE_ACT_GELU: return launch<T, V, PE_ACT_GELU>(a, dbias, stream);
-    case PE_ACT_RELU: return launch<T, V, PE_ACT_RELU>(a, dbias, stream);
-    default: return launch<T, V, PE_ACT_NONE>(a, dbias, stream);
+    case PE_ACT_GEGLU: return launch<T, V, PE_ACT_GEGLU>(a, stream);
+    case PE_ACT_GELU: return launch<T, V, PE_ACT_GELU>(a, stream);
+    case PE_ACT_RELU: return launch<T, V, PE_ACT_RELU>(a, stream);
+    default: return launch<T, V, PE_ACT_NONE>(a, stream);
   }
 }
 
@@ -164,13 +195,14 @@ pe_status run(int act, const void* dy, const void* z, int64_t rows, int32_t feat
                      rows,
                      features,
                      static_cast<T*>(dz),
-                     dbias ? static_cast<float*>(workspace) : nullptr};
+                     dbias ? static_cast<float*>(workspace) : nullptr,
+                     dbias};
   constexpr int V = 16 / sizeof(T);
-  if (vectors<V>(features, a.dy, a.z, a.dz)) return launch_act<T, V>(act, a, dbias, stream);
+  if (vectors<V>(features, a.dy, a.z, a.dz)) return launch_act<T, V>(act, a, stream);
   if (V > 4 && vectors<4>(features, a.dy, a.z, a.dz))
-    return launch_act<T, 4>(act, a, dbias, stream);
-  if (vectors<2>(features, a.dy, a.z, a.dz)) return launch_act<T, 2>(act, a, dbias, stream);
-  return launch_act<T, 1>(act, a, dbias, stream);
+    return launch_act<T, 4>(act, a, stream);
+  if (vectors<2>(features, a.dy, a.z, a.dz)) return launch_act<T, 2>(act, a, stream);
+  return launch_act<T, 1>(act, a, stream);
 }
 
 // Columns of z are counted in int32, up to a block's past the last one.
@@ -182,8 +214,10 @@ constexpr int32_t kMaxFeatures = (1 << 30) - 1024;
 
 using namespace pe;
 
-extern "C" size_t pe_activation_bwd_workspace_size(pe_activation activation, int32_t features) {
-  if (!activation_ok(activation) || features < 1 || features > kMaxFeatures) return 0;
+extern "C" size_t pe_activation_bwd_workspace_size(pe_activation activation, int64_t rows,
+                                                   int32_t features) {
+  if (!activation_ok(activation) || rows <= kFewRows || features < 1 || features > kMaxFeatures)
+    return 0;
   return (size_t)kMaxBlocks * (size_t)features * (activation == PE_ACT_GEGLU ? 2 : 1) *
          sizeof(float);
 }
@@ -200,8 +234,9 @@ extern "C" pe_status pe_activation_bwd(pe_dtype dtype, pe_activation activation,
   if (rows > 0) {
     if (!dy || (activation != PE_ACT_NONE && (!pre || !dz))) return PE_ERR_INVALID_ARG;
     if (activation == PE_ACT_GEGLU && dz == dy) return PE_ERR_INVALID_ARG;
-    if (dbias && (!workspace || !aligned(workspace, 16) ||
-                  workspace_bytes < pe_activation_bwd_workspace_size(activation, features)))
+    const size_t need =
+        dbias ? pe_activation_bwd_workspace_size(activation, rows, features) : 0;
+    if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
       return PE_ERR_WORKSPACE;
   }
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pe.h"
 
 namespace pe {
@@ -221,6 +223,38 @@ pe_status launch_after_previous(void (*kernel)(KArgs...), dim3 grid, dim3 block,
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return PE_ERR_CUDA;
+  return PE_OK;
+}
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; `done`, one for
+// each kernel, remembers the devices (the runtime call takes microseconds).
+template <typename K>
+pe_status allow_shared_memory(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int device = 0;
+  PE_CUDA_TRY(cudaGetDevice(&device));
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (done.load() & bit) return PE_OK;
+  PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(bit);
+  return PE_OK;
+}
+
+// Launches `grid` in clusters (of eight blocks at most, the portable size).
+template <typename... KArgs, typename... Args>
+pe_status launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 cluster, unsigned threads,
+                          size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster.x;
+  attr[0].val.clusterDim.y = cluster.y;
+  attr[0].val.clusterDim.z = cluster.z;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return PE_ERR_CUDA;

@@ -33,7 +33,10 @@ struct Args {
   float inv_c;           // 1 / C
   float eps;
   T* dx;
-  float* part;           // [gridDim.x][2 C]: this block's sums for the weight, the bias
+  float* part;           // [gridDim.x][2 C]: this block's sums for the weight, the bias, or
+                         // null: one cluster, which writes the gradients itself
+  float* dweight;
+  float* dbias;
 };
 
 // Sums of kSums numbers a thread over the kGroup threads of a row, the same in all of them.
@@ -261,7 +264,8 @@ layernorm_bwd_kernel(const Args<T> a) {
   };
 
   griddep_launch_dependents();               // the second kernel may come to wait for this one
-  float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
+  constexpr int kOwnSums = kGroups > 1 ? kGroups * kKept * (kGroup + 1) : 0;
+  float* part = a.part ? a.part + (int64_t)blockIdx.x * 2 * a.C : sums + kOwnSums;
   if constexpr (kIsWide) {
     __syncthreads();
     for (int32_t c = threadIdx.x; c < 2 * a.C; c += kBlock) part[c] = sums[c];
@@ -296,6 +300,16 @@ layernorm_bwd_kernel(const Args<T> a) {
       }
     }
   }
+  if constexpr (!kIsWide) {
+    if (!a.part)
+      sum_lines_of_cluster(part, (int32_t)gridDim.x, a.C, a.dweight, a.C, a.dbias);
+  }
+}
+
+// Rows that one cluster takes: 16 for each group of threads of its eight blocks, of which a
+// block has as many as this in every form (320 x 500 fp32: one launch 5.2 us, two 6.3).
+int64_t few_rows(int32_t C) {
+  return C > kWide ? 0 : 16 * kClusterLines * (C <= 256 ? 8 : C <= 512 ? 4 : C <= 1024 ? 2 : 1);
 }
 
 // Blocks of a kernel that an SM holds at a time.
@@ -308,26 +322,40 @@ int resident_blocks(K kernel, int threads, size_t smem) {
 }
 
 template <typename T, int V, int kIter, int kGroup>
-pe_status launch(const Args<T>& a, float* dweight, float* dbias, cudaStream_t stream) {
+pe_status launch(const Args<T>& a, cudaStream_t stream) {
   constexpr bool wide = kGroup > kThreads;
   constexpr int kGroups = wide ? 1 : kThreads / kGroup;
   static_assert(!wide || kIter * kGroup * V >= kMaxChannels, "a block holds the widest row");
+  size_t smem = wide ? 2 * (size_t)a.C * sizeof(float)
+                : kGroups > 1 ? (size_t)kGroups * kIter * V * (kGroup + 1) * sizeof(float)
+                              : 0;
   const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup>;
-  const size_t smem = wide ? 2 * (size_t)a.C * sizeof(float)
-                      : kGroups > 1 ? (size_t)kGroups * kIter * V * (kGroup + 1) * sizeof(float)
-                                    : 0;
-  if (wide)
-    PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     2 * kMaxChannels * (int)sizeof(float)));
+  if (a.N <= few_rows(a.C)) {
+    smem += 2 * (size_t)a.C * sizeof(float);
+    static_assert(wide || kGroups * kIter * V * (kGroup + 1) + 2 * kWide <= 56 * 256,
+                  "the sums and a line fit the opt-in below");
+    static std::atomic<uint64_t> done{0};
+    PE_TRY(allow_shared_memory(kernel, 56 << 10, done));
+    Args<T> few = a;
+    few.part = nullptr;
+    const int64_t need = ceil_div(a.N, kGroups);
+    const dim3 blocks((unsigned)(need < kClusterLines ? need : kClusterLines));
+    return launch_clusters(kernel, blocks, blocks, kGroup * kGroups, smem, stream, few);
+  }
+  if (wide) {
+    static std::atomic<uint64_t> done{0};
+    PE_TRY(allow_shared_memory(kernel, 2 * kMaxChannels * (int)sizeof(float), done));
+  }
   // As many blocks as the device holds at a time: a block more would run alone at the end.
-  static const int resident = resident_blocks(kernel, kGroup * kGroups, wide ? 2 * kMaxChannels * sizeof(float) : smem);
+  static const int resident =
+      resident_blocks(kernel, kGroup * kGroups, wide ? 2 * kMaxChannels * sizeof(float) : smem);
   if (resident < 1) return PE_ERR_CUDA;
   int64_t blocks = ceil_div(a.N, kGroups), most = (int64_t)resident * device_sm_count();
   if (most > (wide ? kMaxWideBlocks : kMaxBlocks)) most = wide ? kMaxWideBlocks : kMaxBlocks;
   if (blocks > most) blocks = most;
   kernel<<<(unsigned)blocks, kGroup * kGroups, smem, stream>>>(a);
   PE_CUDA_TRY(cudaGetLastError());
-  return launch_sum_parts(a.part, (int32_t)blocks, a.C, dweight, a.C, dbias, stream);
+  return launch_sum_parts(a.part, (int32_t)blocks, a.C, a.dweight, a.C, a.dbias, stream);
 }
 
 // The form for V neighbouring channels per access: vectors a thread and threads a row, by the
@@ -336,23 +364,23 @@ pe_status launch(const Args<T>& a, float* dweight, float* dbias, cudaStream_t st
 //   bf16 32299 x 768    16 channels of 64 threads 43.2 us, 8 of 96 41.6, 24 of 32 51
 //   bf16 169151 x 1024  16 of 64 220 us, 8 of 128 236;   90487 x 512  16 of 32 64, 8 of 64 68
 template <typename T, int V>
-pe_status launch_rows(const Args<T>& a, float* dweight, float* dbias, cudaStream_t stream) {
+pe_status launch_rows(const Args<T>& a, cudaStream_t stream) {
   const int32_t C = a.C;
-  if (C > kWide) return launch<T, V, 16 / V, 1024>(a, dweight, dbias, stream);
+  if (C > kWide) return launch<T, V, 16 / V, 1024>(a, stream);
   if constexpr (V == 8) {
-    if (C <= 256) return launch<T, V, 1, 32>(a, dweight, dbias, stream);
-    if (C <= 512) return launch<T, V, 2, 32>(a, dweight, dbias, stream);
-    if (C <= 768) return launch<T, V, 1, 96>(a, dweight, dbias, stream);
-    if (C <= 1024) return launch<T, V, 2, 64>(a, dweight, dbias, stream);
-    if (C <= 2048) return launch<T, V, 2, 128>(a, dweight, dbias, stream);
-    return launch<T, V, 2, 256>(a, dweight, dbias, stream);
+    if (C <= 256) return launch<T, V, 1, 32>(a, stream);
+    if (C <= 512) return launch<T, V, 2, 32>(a, stream);
+    if (C <= 768) return launch<T, V, 1, 96>(a, stream);
+    if (C <= 1024) return launch<T, V, 2, 64>(a, stream);
+    if (C <= 2048) return launch<T, V, 2, 128>(a, stream);
+    return launch<T, V, 2, 256>(a, stream);
   } else {
     constexpr int kIter = 8 / V;               // eight channels a thread
-    if (C <= 256) return launch<T, V, kIter, 32>(a, dweight, dbias, stream);
-    if (C <= 512) return launch<T, V, kIter, 64>(a, dweight, dbias, stream);
-    if (C <= 1024) return launch<T, V, kIter, 128>(a, dweight, dbias, stream);
-    if (C <= 2048) return launch<T, V, kIter, 256>(a, dweight, dbias, stream);
-    return launch<T, V, 2 * kIter, 256>(a, dweight, dbias, stream);
+    if (C <= 256) return launch<T, V, kIter, 32>(a, stream);
+    if (C <= 512) return launch<T, V, kIter, 64>(a, stream);
+    if (C <= 1024) return launch<T, V, kIter, 128>(a, stream);
+    if (C <= 2048) return launch<T, V, kIter, 256>(a, stream);
+    return launch<T, V, 2 * kIter, 256>(a, stream);
   }
 }
 
@@ -369,15 +397,17 @@ pe_status run(const void* dy, const void* h, const void* w, const void* dres, in
                      1.f / (float)C,
                      eps,
                      static_cast<T*>(dx),
-                     static_cast<float*>(ws)};
+                     static_cast<float*>(ws),
+                     dweight,
+                     dbias};
   constexpr int V = 16 / sizeof(T);
   if (vectors<V>(C, a.dy, a.w, a.h, a.dx, a.dres))
-    return launch_rows<T, V>(a, dweight, dbias, stream);
+    return launch_rows<T, V>(a, stream);
   if (V > 4 && vectors<4>(C, a.dy, a.w, a.h, a.dx, a.dres))
-    return launch_rows<T, 4>(a, dweight, dbias, stream);
+    return launch_rows<T, 4>(a, stream);
   if (vectors<2>(C, a.dy, a.w, a.h, a.dx, a.dres))
-    return launch_rows<T, 2>(a, dweight, dbias, stream);
-  return launch_rows<T, 1>(a, dweight, dbias, stream);
+    return launch_rows<T, 2>(a, stream);
+  return launch_rows<T, 1>(a, stream);
 }
 
 }  // namespace
@@ -386,8 +416,8 @@ pe_status run(const void* dy, const void* h, const void* w, const void* dres, in
 
 using namespace pe;
 
-extern "C" size_t pe_layernorm_bwd_workspace_size(int32_t C) {
-  if (C < 1 || C > kMaxChannels) return 0;
+extern "C" size_t pe_layernorm_bwd_workspace_size(int64_t N, int32_t C) {
+  if (N < 1 || C < 1 || C > kMaxChannels || N <= few_rows(C)) return 0;
   return (size_t)(C > kWide ? kMaxWideBlocks : kMaxBlocks) * 2 * (size_t)C * sizeof(float);
 }
 
@@ -402,8 +432,8 @@ extern "C" pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void
   if (C > kMaxChannels) return PE_ERR_UNSUPPORTED;
   if (N > 0) {
     if (!dy || !h || !weight || !dx) return PE_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < pe_layernorm_bwd_workspace_size(C))
+    const size_t need = pe_layernorm_bwd_workspace_size(N, C);
+    if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
       return PE_ERR_WORKSPACE;
   }
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;

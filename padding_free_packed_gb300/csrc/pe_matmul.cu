@@ -191,6 +191,13 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
   return plan;
 }
 
+// Parts of slices, then parts of fp32 operands.
+size_t workspace_bytes_of(const LinearPlan& plan, bool fp32, int64_t m, int64_t n, int64_t k,
+                          bool a_t, bool b_t) {
+  return matmul_tiles_workspace(tile_count(m, n), plan.slices) +
+         (fp32 ? (size_t)split_bytes(m, n, k, a_t, b_t) : 0);
+}
+
 // A matrix of bf16 that TMA can read.
 bool operand_ok(const void* x, int64_t ld) { return aligned(x, 16) && ld % 8 == 0; }
 
@@ -211,8 +218,7 @@ extern "C" size_t pe_matmul_workspace_size(pe_dtype dtype, int a_transposed, int
   const bool fp32 = dtype == PE_FP32;
   const LinearPlan plan =
       linear_plan(m, n, k, fp32, activation == PE_ACT_GEGLU, a_transposed != 0);
-  return matmul_tiles_workspace(tile_count(m, n), plan.slices) +
-         (fp32 ? (size_t)split_bytes(m, n, k, a_transposed != 0, b_transposed != 0) : 0);
+  return workspace_bytes_of(plan, fp32, m, n, k, a_transposed != 0, b_transposed != 0);
 }
 
 extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int a_transposed,
@@ -248,8 +254,10 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
   if (!aligned(out, size) || !aligned(bias, size) || !aligned(residual, size) ||
       !aligned(pre, size))
     return PE_ERR_UNSUPPORTED;
+  const LinearPlan plan = k == 0 ? LinearPlan{0, 1, 1, 1}
+                                 : linear_plan(m, n, k, fp32, geglu, a_transposed != 0);
   const size_t need =
-      pe_matmul_workspace_size(dtype, a_transposed, b_transposed, m, n, k, activation);
+      k == 0 ? 0 : workspace_bytes_of(plan, fp32, m, n, k, a_transposed != 0, b_transposed != 0);
   if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return PE_ERR_WORKSPACE;
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
@@ -274,7 +282,6 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
          out_dtype == PE_FP32 ? 1 : 0,
          four(out, out_ld) && four(residual, residual_ld) && four(pre, pre_ld) ? 1 : 0};
   if (k == 0) return matmul_no_sum(p, stream);
-  const LinearPlan plan = linear_plan(m, n, k, fp32, geglu, p.a.transposed);
   DeviceStatus* status = nullptr;
   PE_TRY(matmul_status_word(&status));
   if (fp32)

@@ -50,25 +50,6 @@ pe_status matmul_status_word(DeviceStatus** out);
 
 namespace sm103 {
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Every thread of the cluster; the .aligned form needs whole warps, so threads that a
-// branch before the barrier has parted come together first.
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// Address, in the cluster's shared window, of the same variable in CTA `rank`.
-__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-
 // mbar_wait for the waits of every block of k: a few attempts (each suspends the
 // thread for a while) before the clock and the abort flag are looked at. Not with a
 // short limit, which is kept by polling.

@@ -340,8 +340,8 @@ pe_status launch(const Matmul& q, int32_t split, DeviceStatus* status, cudaStrea
   const size_t smem = sizeof(Smem<kT>) + 1024;
   static_assert(2 * (sizeof(Smem<kT>) + 2048) <= 227 * 1024, "two CTAs share an SM");
   const auto kernel = matmul_narrow_kernel<kT, kAct>;
-  PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(smem)));
+  static std::atomic<uint64_t> done{0};
+  PE_TRY(allow_shared_memory(kernel, static_cast<int>(smem), done));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ceil_div(q.e.n, kGeglu ? 64 : 128) * split),
                      (unsigned)ceil_div(q.m, kT));

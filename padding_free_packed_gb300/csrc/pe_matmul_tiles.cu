@@ -954,12 +954,14 @@ template <int kOut, bool kGeglu, int kPairs>
 pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) {
   const auto kernel = matmul_tiles_kernel<kOut, kGeglu, kPairs>;
   const size_t smem = sizeof(Smem) + 1024;
-  PE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(smem)));
-  if (is_fp32(kOut)) {
-    cudaFuncAttributes attr;
-    PE_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
-    if (static_cast<uint32_t>(attr.numRegs) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
+  static std::atomic<uint64_t> done{0};
+  PE_TRY(allow_shared_memory(kernel, static_cast<int>(smem), done));
+  if (is_fp32(kOut)) {                     // the register split needs its registers
+    static const int registers = [&] {
+      cudaFuncAttributes attr;
+      return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (static_cast<uint32_t>(registers) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
       return PE_ERR_UNSUPPORTED;
   }
   // Clusters that fit at a time: each takes as many of one GPC's SMs as it has CTAs.

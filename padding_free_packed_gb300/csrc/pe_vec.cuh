@@ -8,6 +8,7 @@
 namespace pe {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kClusterLines = 8;               // blocks of a cluster that add their sums
 
 // V consecutive elements of a row, kept as loaded: bf16 pairs stay in one register
 // until they are used.
@@ -118,6 +119,30 @@ __device__ __forceinline__ void group_sync(int group) {
 // after the kernel before it in the stream.
 pe_status launch_sum_parts(const float* part, int32_t blocks, int32_t c0, float* out0, int32_t c1,
                            float* out1, cudaStream_t stream);
+
+// Few rows need no second kernel: the blocks form a cluster and add their lines in shared
+// memory. `line` is this block's, at the same place in every block; the blocks deal the
+// columns among them and add them in the order of the blocks.
+__device__ __forceinline__ void sum_lines_of_cluster(const float* line, int32_t blocks, int32_t c0,
+                                                     float* out0, int32_t c1, float* out1) {
+  using namespace sm103;
+  cluster_sync();                              // every block's line is complete
+  const uint32_t here = smem_u32(line);
+  const int32_t step = blocks * (int32_t)blockDim.x;
+  for (int32_t c = (int32_t)(cluster_rank() * blockDim.x + threadIdx.x); c < c0 + c1; c += step) {
+    float v[kClusterLines], s = 0.f;
+#pragma unroll
+    for (int b = 0; b < kClusterLines; ++b)
+      v[b] = b < blocks ? load_cluster_f32(peer_address(here + 4 * c, b)) : 0.f;
+#pragma unroll
+    for (int b = 0; b < kClusterLines; ++b) s += v[b];
+    if (c < c0)
+      out0[c] = s;
+    else if (out1)
+      out1[c - c0] = s;
+  }
+  cluster_sync();                              // the lines have been read
+}
 
 // Whether rows of C channels and their tensors allow accesses of V channels.
 template <int V, typename T, typename... P>

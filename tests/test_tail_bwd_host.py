@@ -66,13 +66,16 @@ def test_layernorm_bwd_refusals(lib):
     for name in ("dy", "h", "w", "dx", "dw"):
         assert _ln(lib, **{name: None}) == INVALID
     assert _ln(lib, c=16385) == UNSUPPORTED
-    need = lib.pe_layernorm_bwd_workspace_size(64)
+    need = lib.pe_layernorm_bwd_workspace_size(5000, 64)
     assert need > 0
-    assert _ln(lib, size=need - 1) == WORKSPACE
-    assert _ln(lib, ws=None) == WORKSPACE
-    assert _ln(lib, ws=24) == WORKSPACE
-    assert lib.pe_layernorm_bwd_workspace_size(0) == 0
-    assert lib.pe_layernorm_bwd_workspace_size(16385) == 0
+    assert _ln(lib, n=5000, size=need - 1) == WORKSPACE
+    assert _ln(lib, n=5000, ws=None) == WORKSPACE
+    assert _ln(lib, n=5000, ws=24) == WORKSPACE
+    assert lib.pe_layernorm_bwd_workspace_size(4, 64) == 0     # few rows need none
+    assert lib.pe_layernorm_bwd_workspace_size(1, 5000) > 0
+    assert lib.pe_layernorm_bwd_workspace_size(0, 64) == 0
+    assert lib.pe_layernorm_bwd_workspace_size(5000, 0) == 0
+    assert lib.pe_layernorm_bwd_workspace_size(5000, 16385) == 0
 
 
 def test_activation_bwd_refusals(lib):
@@ -89,12 +92,13 @@ def test_activation_bwd_refusals(lib):
     assert _act(lib, act=NONE, dz=None) == INVALID
     assert _act(lib, act=NONE, z=None, dz=None, db=None) == INVALID
     for act, wide in ((GELU, 1), (GEGLU, 2)):
-        need = lib.pe_activation_bwd_workspace_size(act, 64)
-        assert need == wide * lib.pe_activation_bwd_workspace_size(RELU, 64)
-        assert _act(lib, act=act, size=need - 1) == WORKSPACE
-    assert _act(lib, ws=None) == WORKSPACE
-    assert lib.pe_activation_bwd_workspace_size(7, 64) == 0
-    assert lib.pe_activation_bwd_workspace_size(GELU, 0) == 0
+        need = lib.pe_activation_bwd_workspace_size(act, 9000, 64)
+        assert need == wide * lib.pe_activation_bwd_workspace_size(RELU, 9000, 64) > 0
+        assert _act(lib, act=act, n=9000, size=need - 1) == WORKSPACE
+    assert _act(lib, n=9000, ws=None) == WORKSPACE
+    assert lib.pe_activation_bwd_workspace_size(GELU, 4, 64) == 0      # few rows need none
+    assert lib.pe_activation_bwd_workspace_size(7, 9000, 64) == 0
+    assert lib.pe_activation_bwd_workspace_size(GELU, 9000, 0) == 0
 
 
 def test_dropout_refusals(lib):
