@@ -241,6 +241,16 @@ pe_status allow_shared_memory(K* kernel, int bytes, std::atomic<uint64_t>& done)
   return PE_OK;
 }
 
+// Blocks of a kernel that an SM holds at a time (0: the question failed). A grid of as many
+// on every SM has no last, partly filled turn.
+template <typename K>
+int resident_blocks(K* kernel, int threads, size_t smem) {
+  int blocks = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) != cudaSuccess)
+    return 0;
+  return blocks;
+}
+
 // Launches `grid` in clusters (of eight blocks at most, the portable size).
 template <typename... KArgs, typename... Args>
 pe_status launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 cluster, unsigned threads,

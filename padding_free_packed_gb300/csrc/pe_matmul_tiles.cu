@@ -7,22 +7,17 @@
 // epilogue of a tile runs under the next tile's MMAs. An operand stored with k as its rows is
 // loaded in boxes of 64 columns by 64 rows and read by the MMA as it lies there.
 //
-// With every SM loading, L2 gives each 55 bytes a cycle (measured: a block of 64 takes 600
-// cycles, 512 without loads, 519 with a's alone), 32 KiB of which would be due in the 512
-// cycles of a block's MMAs. So two pairs with neighbouring row tiles form a cluster and share
-// their rows of b: each CTA loads half of what it needs of b and multicasts it to the CTA
-// that needs the same, 24 KiB a block.
+// Two pairs with neighbouring row tiles can form a cluster and share their rows of b: each CTA
+// loads half of what it needs of b and multicasts it to the CTA that needs the same, 24 KiB a
+// block instead of 32. Clusters of four leave 8 of the 152 SMs idle, and the two ways are
+// close (32299 x 2304 x 768 for a second on end: 82.0 us, pairs alone 84.7); the plan goes by
+// which has fewer turns.
 //
 //   warps 0, 2   loads of a and of b (every CTA), a ring of kStages blocks
 //   warp 1       MMA issue (first CTA of each pair)
 //   warps 4-11   epilogue; warps 4-7 the tile's left half, 8-11 its right half: bias, z into
 //                pre, activation, residual (loaded by TMA into the box that the result then
 //                leaves from), rounding, TMA stores of 32 rows x 128 bytes
-//
-// The loads and the MMAs are issued by one thread each, whose instructions take 10 to 20
-// cycles apiece while the epilogue's warps keep the schedulers busy. Their loops over blocks
-// are kept short for that reason, and a and b have a warp each: one thread for both took 530
-// cycles a block without an epilogue, 770 beside geglu's and 960 beside gelu's.
 //
 // With geglu the tile is 128 columns of out: the first CTA loads their gate rows of b, the
 // second their up rows, so that a thread finds both in its row of tensor memory.
@@ -34,6 +29,25 @@
 // slice before the next (so that the pairs read the same blocks of k at about the same
 // time); the slices' fp32 sums are then added, in the order of k, by a second kernel, which
 // also does the epilogue.
+//
+// What bounds it: a block of 64 is 512 cycles of MMAs, and every other cycle is one in which
+// the tensor cores wait for an instruction. Measured, in cycles a block (32299 x 2304 x 768;
+// the same with geglu; with gelu; 19456 x 2304 x 8192):
+//   loads and MMAs by one thread each, in branches of one thread   767  767  1040   608
+//   loads of a and of b by a warp each                             655  827  1020   546
+//   MMAs issued by a whole warp, one elected lane                  569  708   917   518
+//   loads likewise, gelu in paired arithmetic                      548  542   690   519
+// A branch of one thread keeps its operands out of the uniform registers that these
+// instructions read, and the epilogue's warps, whose independent multiply-adds never stall,
+// take the issue slots of the scheduler that the MMA warp is on (one such warp beside it
+// made 589 cycles 982; on another scheduler it changed nothing). With gelu that is what is
+// left: its own instructions are some 500 cycles a block on each scheduler.
+//
+// Measured (GB300, device time of a burst): 32299 x 2304 x 768 bf16 in 66.6 us (1.72 PFLOP/s,
+// 0.89 of the measured dense bf16 rate), with geglu and pre 81 (1.41), 169151 x 1024 x 1024
+// with bias and residual 214 to 221 us (1.65; the tensor cores are busy for 0.905 of the
+// cycles), 2304 x 768 x 32299 to fp32 80 us (1.42). For seconds on end the power cap rules:
+// 77 us for the first, 238 for 169151 x 1024 x 1024, at 1.6 to 1.8 GHz.
 #include <type_traits>
 
 #include "pe_matmul.cuh"
@@ -65,7 +79,8 @@ static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
 // Blocks of k that one accumulator sums: all of them for results rounded to bf16; for fp32
 // results a few, whose sums are then added in fp32 registers. The tensor cores cut the sum
 // off after every 16 products (1.7e-8 of it a time, always towards zero, measured), which a
-// chain of 11500 products turned into 1.2e-5 of the result; this way it stays at 3e-7.
+// chain of 11500 products turned into 1.2e-5 of the result. Eight blocks leave 5e-7, for 532
+// cycles a block where all of them take 516; four leave 3e-7, for 560.
 constexpr int32_t kChunk = 8;
 constexpr int32_t chunk_of(int out) { return is_fp32(out) ? kChunk : 0x7fffffff; }
 constexpr size_t kPartFloats = (size_t)kTile * kTile;

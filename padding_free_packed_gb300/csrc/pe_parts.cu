@@ -17,15 +17,14 @@ sum_parts_kernel(const float* part, int32_t blocks, int32_t c0, float* out0, int
   griddep_wait();
   float s = 0.f;
   if (c < cols) {
-    int32_t b = y;
-    for (; b + 96 < blocks; b += 128) {                  // four lines in flight
-      float v[4];
+    for (int32_t b = y; b < blocks; b += 320) {                       // ten lines in flight
+      float v[10];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = part[(int64_t)(b + 32 * j) * cols + c];
+      for (int j = 0; j < 10; ++j)
+        v[j] = b + 32 * j < blocks ? part[(int64_t)(b + 32 * j) * cols + c] : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s += v[j];
+      for (int j = 0; j < 10; ++j) s += v[j];
     }
-    for (; b < blocks; b += 32) s += part[(int64_t)b * cols + c];
   }
   sum[y][x] = s;
   __syncthreads();

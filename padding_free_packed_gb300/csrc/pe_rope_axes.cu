@@ -8,6 +8,8 @@
 // halves of a head. Angles are counted in turns modulo one, in 64-bit fixed point: a position
 // times the frequency as a fraction of 2^64, which wraps as turns do, so far positions lose
 // nothing and no double-precision arithmetic runs on the GPU.
+// Measured (GB300, device time): q and k of 169151 tokens, 16 heads x 64 bf16, out of one
+// buffer of q, k and v, in 203 us (6.8 TB/s, the measured copy rate).
 #include <math.h>
 
 #include "pe_vec.cuh"
@@ -17,6 +19,7 @@ namespace pe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 32;               // 16: 208 us in the case above, 3: 246
 constexpr int kMaxHalf = 128;                  // head_dim <= 256
 constexpr int kMaxAxes = 4;
 
@@ -119,7 +122,7 @@ template <typename T, int V>
 pe_status launch(const Tensor& q, const Tensor& k, const int32_t* pos, int64_t N, int32_t D,
                  const Plan& plan, float sign, cudaStream_t stream) {
   int64_t blocks = ceil_div(N, kThreads / 32);
-  const int64_t most = (int64_t)device_sm_count() * 16;
+  const int64_t most = (int64_t)device_sm_count() * kBlocksPerSm;
   if (blocks > most) blocks = most;
   rope_axes_kernel<T, V, 4>
       <<<(unsigned)blocks, kThreads, 0, stream>>>(q, k, pos, N, D, plan, sign);
