@@ -935,7 +935,8 @@ def pe_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
         dresidual = _input(dresidual, "dresidual", h, h.shape)
     dev = h.device
     dx = _like(out, "out", h)
-    dweight, dbias = torch.empty((2, c), dtype=torch.float32, device=dev).unbind()
+    dweight = torch.empty(c, dtype=torch.float32, device=dev)
+    dbias = torch.empty(c, dtype=torch.float32, device=dev)
     need = lib.pe_layernorm_bwd_workspace_size(n, c)
     ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
     _call("pe_layernorm_bwd", dev, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
