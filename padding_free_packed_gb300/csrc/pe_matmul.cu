@@ -9,8 +9,8 @@ namespace pe {
 namespace {
 
 // The kernels hold row, column and k coordinates of whole tiles in int32, and count blocks of
-// 256 x 128 (columns of out with geglu) x 64 in int32, six times with fp32 operands; sixteen
-// thread blocks a tile stay below 2^31.
+// 256 x 128 (columns of out with geglu) x 64 in int32, six times with fp32 operands; 32 thread
+// blocks a tile of 256 columns stay below 2^31, since three blocks of 128 make two tiles.
 constexpr int64_t kMaxSize = (1LL << 31) - 1024;
 bool sizes_ok(int64_t m, int64_t n, int64_t k) {
   constexpr int64_t kMaxBlocks = 1LL << 29;

@@ -46,7 +46,7 @@
 // Measured (GB300, device time of a burst): 32299 x 2304 x 768 bf16 in 66.6 us (1.72 PFLOP/s,
 // 0.89 of the measured dense bf16 rate), with geglu and pre 81 (1.41), 169151 x 1024 x 1024
 // with bias and residual 214 to 221 us (1.65; the tensor cores are busy for 0.905 of the
-// cycles), 2304 x 768 x 32299 to fp32 80 us (1.42). For seconds on end the power cap rules:
+// cycles), 2304 x 768 x 32299 to fp32 78 us (1.46). For seconds on end the power cap rules:
 // 77 us for the first, 238 for 169151 x 1024 x 1024, at 1.6 to 1.8 GHz.
 #include <type_traits>
 
@@ -84,6 +84,7 @@ static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
 constexpr int32_t kChunk = 8;
 constexpr int32_t chunk_of(int out) { return is_fp32(out) ? kChunk : 0x7fffffff; }
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
+constexpr int kPartsAhead = 5, kPartBlocks = 4;          // parts in flight; blocks an SM
 
 struct alignas(1024) Smem {
   uint8_t a[kStages][kOperandBytes];
@@ -856,43 +857,49 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
 }
 
 // Adds the slices' sums of every tile, in the order of k, and finishes them; without slices,
-// finishes zeros. One block per 32 rows x 128 columns of the accumulator (64 of the gate, 64
-// of the up part with geglu); parts are column-group-major.
+// finishes zeros. One block per 32 rows x 64 columns of the accumulator (32 of the gate, 32
+// of the up part with geglu); parts are column-group-major. Small blocks with few sums a
+// thread, since what it waits for is L2: 27 tiles of 5 slices in 7 us, in blocks of 128
+// columns 9.7.
 template <int kAct>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kPartBlocks)
 matmul_parts_kernel(const __grid_constant__ Params p) {
   constexpr bool kGeglu = kAct == PE_ACT_GEGLU;
   constexpr int32_t kOutCols = kGeglu ? kTile / 2 : kTile;
-  __shared__ float tile[32][132];
+  __shared__ float tile[32][68];
   griddep_wait();                                        // before any block may leave
-  const int piece = blockIdx.x & 15;                     // 2 CTAs x 4 row quarters x 2 halves
-  const int32_t t = blockIdx.x >> 4;
-  const int rank = piece >> 3, quad = (piece >> 1) & 3, half = piece & 1;
+  const int piece = blockIdx.x & 31;       // 2 CTAs x 4 row quarters x 2 halves x 2 parts
+  const int32_t t = blockIdx.x >> 5;
+  const int rank = piece >> 4, quad = (piece >> 2) & 3, half = (piece >> 1) & 1;
+  const int sub = piece & 1;
   int32_t rt, ct;
   place(p, t, rt, ct);
   const int32_t row0 = rt * kTile + rank * kRows + quad * 32;
-  const int32_t col0 = ct * kOutCols + half * (kOutCols / 2);
+  const int32_t col0 = ct * kOutCols + half * (kOutCols / 2) + sub * (kOutCols / 4);
   if (row0 >= p.e.m || col0 >= p.e.n) return;
   const int row = threadIdx.x & 31, g0 = threadIdx.x >> 5;
-  float4 sum[4] = {};
+  // Two groups of four columns: neighbours by 32 columns, or the gate's and the up part's.
+  constexpr int kApart = kGeglu ? 16 : 8;
+  float4 sum[2] = {};
   const float4* parts = reinterpret_cast<const float4*>(p.parts + (int64_t)t * kPartFloats) +
-                        (rank * 64 + half * 32) * 128 + quad * 32 + row + g0 * 128;
-  constexpr int kAhead = 4;                              // parts in flight
-  for (int32_t q = 0; q < p.slices; q += kAhead) {
-    float4 v[kAhead][4];
+                        (rank * 64 + half * 32 + sub * (kGeglu ? 8 : 16) + g0) * 128 +
+                        quad * 32 + row;
+  for (int32_t q = 0; q < p.slices; q += kPartsAhead) {
+    float4 v[kPartsAhead][2];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < kPartsAhead; ++j) {
       if (q + j < p.slices) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[j][i] = parts[(int64_t)(q + j) * p.tiles * (int64_t)(kPartFloats / 4) + 8 * i * 128];
+        for (int i = 0; i < 2; ++i)
+          v[j][i] = parts[(int64_t)(q + j) * p.tiles * (int64_t)(kPartFloats / 4) +
+                          i * kApart * 128];
       }
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < kPartsAhead; ++j) {
       if (q + j < p.slices) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           sum[i].x += v[j][i].x;
           sum[i].y += v[j][i].y;
           sum[i].z += v[j][i].z;
@@ -902,29 +909,25 @@ matmul_parts_kernel(const __grid_constant__ Params p) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(&tile[row][4 * (g0 + 8 * i)]) = sum[i];
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(&tile[row][4 * (g0 + 8 * i)]) = sum[i];
   __syncthreads();
   // Four columns of out a thread, the same in all of its rows.
-  constexpr int kGroups = kGeglu ? 16 : 32, kStep = 256 / kGroups;
-  const int c = 4 * (threadIdx.x % kGroups);
+  constexpr int kGroups = kGeglu ? 8 : 16, kStep = 256 / kGroups, kFlight = 32 / kStep;
+  const int c = 4 * (threadIdx.x % kGroups), r0 = threadIdx.x / kGroups;
   if (col0 + c >= p.e.n) return;
   const Finish4<kAct> finish(p.e, col0 + c);
-  constexpr int kFlight = 4;
-  for (int r0 = threadIdx.x / kGroups; r0 < 32; r0 += kFlight * kStep) {
-    float residual[kFlight][4];
-    if (p.e.residual) {
+  float residual[kFlight][4];
+  if (p.e.residual) {
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i)
-        if (r0 + i * kStep < 32 && row0 + r0 + i * kStep < p.e.m)
-          finish.residual(row0 + r0 + i * kStep, residual[i]);
-    }
+    for (int i = 0; i < kFlight; ++i)
+      if (row0 + r0 + i * kStep < p.e.m) finish.residual(row0 + r0 + i * kStep, residual[i]);
+  }
 #pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int r = r0 + i * kStep;
-      if (r < 32 && row0 + r < p.e.m)
-        finish.row(row0 + r, *reinterpret_cast<const float4*>(&tile[r][c]),
-                   *reinterpret_cast<const float4*>(&tile[r][kGeglu ? c + 64 : c]), residual[i]);
-    }
+  for (int i = 0; i < kFlight; ++i) {
+    const int r = r0 + i * kStep;
+    if (row0 + r < p.e.m)
+      finish.row(row0 + r, *reinterpret_cast<const float4*>(&tile[r][c]),
+                 *reinterpret_cast<const float4*>(&tile[r][kGeglu ? c + 32 : c]), residual[i]);
   }
 }
 
@@ -954,7 +957,7 @@ pe_status launch_parts(const Params& p, cudaStream_t stream) {
                       : p.e.act == PE_ACT_GELU ? matmul_parts_kernel<PE_ACT_GELU>
                       : p.e.act == PE_ACT_RELU ? matmul_parts_kernel<PE_ACT_RELU>
                                                : matmul_parts_kernel<PE_ACT_NONE>;
-  return launch_after_previous(kernel, dim3((unsigned)(16 * p.tiles)), dim3(256), 0, stream, p);
+  return launch_after_previous(kernel, dim3((unsigned)(32 * p.tiles)), dim3(256), 0, stream, p);
 }
 
 pe_status operand_map(CUtensorMap* map, const MatmulOperand& x, int32_t rows, int32_t k,
