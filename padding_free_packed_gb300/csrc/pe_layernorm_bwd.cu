@@ -7,15 +7,15 @@
 // large mean costs no precision), and dx is written once. The weight's and bias's sums of a
 // thread's own channels stay in fp32 registers until the block's last row; a second kernel
 // adds the blocks' lines in a fixed order. The next row's loads are in flight while a row is
-// worked on. Rows wider than 4096 channels take a block each and keep those sums in shared
-// memory.
-// Measured (GB300, device time, with the residual's gradient): 32299 x 768 bf16 in 41 us (4.8
-// TB/s, 0.71 of the measured copy rate; some 5 us are the start, the last rows and the second
-// kernel), 169151 x 1024 bf16 220 us (0.93), 32299 x 2304 bf16 125 us (0.70), 90487 x 512
-// fp32 114 us (0.96). What bounds it is bytes in flight: the sums a thread keeps (two for
-// each of its channels) leave 16 to 24 warps an SM. In paired arithmetic 768 channels took 42
-// us where single fp32 operations took 45. bf16 rows of odd width move two bytes at a time
-// (20000 x 777 51 us, 0.36).
+// worked on, in registers or, for wider rows, in a ring in shared memory. Rows wider than 4096
+// channels take a block each and keep those sums in shared memory.
+// Measured (GB300, device time, with the residual's gradient): 32299 x 768 bf16 in 36 us (5.5
+// TB/s, 0.81 of the measured copy rate; some 5 us are the start, the last rows and the second
+// kernel), 169151 x 1024 bf16 207 us (0.99), 32299 x 2304 bf16 94 us (0.93), 90487 x 512
+// fp32 113 us (0.97). What bounds the narrower ones is a row's chain of two joint sums, with
+// the 8 to 24 warps an SM that the registers of a thread's own sums (two for each of its
+// channels) leave. In paired arithmetic 768 channels took 42 us where single fp32 operations
+// took 45. bf16 rows of odd width move two bytes at a time (20000 x 777 51 us, 0.36).
 #include <math.h>
 
 #include "pe_vec.cuh"
@@ -73,17 +73,45 @@ __device__ __forceinline__ void group_sum(float (&x)[kSums], float* red, int gro
 // 495; 90487 x 512 fp32, 8 channels: 2 blocks 116 us, 3 blocks 184).
 template <int V, int kIter, int kGroup>
 constexpr int kMinBlocks =
-    V == 8 ? (kIter > 1 ? 2 : kGroup == 96 ? 4 : 3) : V * kIter > 8 ? 1 : 2;
+    V == 8 ? (kIter > 1 ? 2 : 3) : V * kIter > 8 ? 1 : 2;
+
+// With a ring of rows in shared memory no registers wait for loads, so a thread can have 24
+// channels of bf16 (or 12 of fp32) and a row fewer threads, whose sums take fewer steps: 768
+// channels of one warp, without a barrier, 36 us, of two 38, of three with 8 each 39. One
+// block an SM, of as many threads as the registers allow.
+constexpr int kRing = 3;                       // the row at work and two more
+template <int V, int kIter>
+constexpr int kRingThreads = V * kIter > 8 ? 384 : 512;
+template <int V, int kIter, int kGroup, bool kByRing>
+constexpr int kGroupsOf = kGroup > kThreads ? 1
+                          : kByRing         ? kRingThreads<V, kIter> / kGroup
+                                            : kThreads / kGroup;
+
+// 16 bytes into shared memory, in the thread's open group of copies.
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits for this thread's copies but those of its last kLeft groups.
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 // kGroup threads a row, each with kIter vectors of V channels, the same for all of its rows.
-template <typename T, int V, int kIter, int kGroup>
-__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads / kGroup * kGroup,
-                                  kGroup > kThreads ? 1 : kMinBlocks<V, kIter, kGroup>)
+// kByRing: every thread copies into the ring what it will read itself, so that its own wait is
+// enough.
+template <typename T, int V, int kIter, int kGroup, bool kByRing>
+__global__ void __launch_bounds__(kGroup * kGroupsOf<V, kIter, kGroup, kByRing>,
+                                  kGroup > kThreads || kByRing ? 1 : kMinBlocks<V, kIter, kGroup>)
 layernorm_bwd_kernel(const Args<T> a) {
   constexpr bool kIsWide = kGroup > kThreads;
-  constexpr int kGroups = kIsWide ? 1 : kThreads / kGroup;
+  constexpr int kGroups = kGroupsOf<V, kIter, kGroup, kByRing>;
   constexpr int kBlock = kGroup * kGroups;
-  extern __shared__ float sums[];            // wide: [2][C]; else every group's, at the end
+  // wide: [2][C]; else the ring, then every group's at the end
+  extern __shared__ __align__(16) float sums[];
   __shared__ float red[2][4 * 32];           // two sets: a row's writes miss the last's reads
   const int g = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
   const int64_t step = (int64_t)gridDim.x * kGroups;
@@ -127,22 +155,63 @@ layernorm_bwd_kernel(const Args<T> a) {
       }
     }
   };
-  load(t);
+  // The ring: [row][dy, h, dres][vector][thread], 16 bytes each.
+  static_assert(!kByRing || (kPaired && sizeof(T) * V == 16), "the ring holds 16 bytes a vector");
+  constexpr uint32_t kPlane = kBlock * 16, kSlot = 3 * kIter * kPlane;
+  [[maybe_unused]] char* const mine_in_ring = reinterpret_cast<char*>(sums) + threadIdx.x * 16;
+  [[maybe_unused]] uint32_t slot = 0;          // of the row at work
+  [[maybe_unused]] auto fetch = [&](int64_t row, uint32_t into) {
+    const uint32_t at = sm103::smem_u32(mine_in_ring) + into * kSlot;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int32_t c = (it * kGroup + g) * V;
+      if (c < a.C && row < a.N) {
+        copy_16(at + it * kPlane, a.dy + row * a.C + c);
+        copy_16(at + (kIter + it) * kPlane, a.h + row * a.C + c);
+        if (a.dres) copy_16(at + (2 * kIter + it) * kPlane, a.dres + row * a.C + c);
+      }
+    }
+    copy_commit();                             // a group for every row, copied or not
+  };
+  [[maybe_unused]] auto fetched = [&](int plane) {
+    return load_vec<T, V>(
+        reinterpret_cast<const T*>(mine_in_ring + slot * kSlot + plane * kPlane));
+  };
+  if constexpr (kByRing) {
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(t + i * step, i);
+  } else {
+    load(t);
+  }
   int phase = 0;
   for (; t < a.N; t += step) {
     if constexpr (kPaired) {
       using namespace sm103;
       Vec<T, V> dyn[kIter], hn[kIter], rn[kIter];
       uint64_t total = 0ull;
+      if constexpr (kByRing) {
+        // Over the row before, whose numbers have all been used.
+        fetch(t + (kRing - 1) * step, slot == 0 ? kRing - 1 : slot - 1);
+        copy_wait<kRing - 1>();
+      }
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
-        dyn[it] = dyv[it];
-        hn[it] = hv[it];
-        rn[it] = rv[it];
+        if constexpr (kByRing) {
+          dyn[it].zero();
+          hn[it].zero();
+          if ((it * kGroup + g) * V < a.C) {
+            dyn[it] = fetched(it);
+            hn[it] = fetched(kIter + it);
+          }
+        } else {
+          dyn[it] = dyv[it];
+          hn[it] = hv[it];
+          rn[it] = rv[it];
+        }
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) total = fadd2(total, hn[it].pair(j));
       }
-      load(t + step);
+      if constexpr (!kByRing) load(t + step);
       float first[1], other;
       f2_split(total, first[0], other);
       first[0] += other;
@@ -182,6 +251,9 @@ layernorm_bwd_kernel(const Args<T> a) {
         const int32_t c = (it * kGroup + g) * V;
         if (c < a.C) {
           Vec<T, V> o;
+          if constexpr (kByRing) {
+            if (a.dres) rn[it] = fetched(2 * kIter + it);
+          }
 #pragma unroll
           for (int j = 0; j < V / 2; ++j) {
             const int e = it * (V / 2) + j;
@@ -195,6 +267,7 @@ layernorm_bwd_kernel(const Args<T> a) {
           store_vec<T, V>(a.dx + t * a.C + c, o);
         }
       }
+      if constexpr (kByRing) slot = slot + 1 == kRing ? 0 : slot + 1;
     } else {
       Vec<T, V> dyn[kIter], hn[kIter], rn[kIter];
 #pragma unroll
@@ -324,15 +397,41 @@ int64_t few_rows(int32_t C) {
   return C > kWide ? 0 : 6 * kClusterLines * (kThreads / few_threads(C));
 }
 
+// `resident` blocks an SM (or as many as there are rows for), and the sum of their lines.
+template <typename T, typename K>
+pe_status launch_blocks(K* kernel, const Args<T>& a, int groups, int threads, size_t smem,
+                        int resident, int most_blocks, cudaStream_t stream) {
+  if (resident < 1) return PE_ERR_CUDA;
+  int64_t blocks = ceil_div(a.N, groups), most = (int64_t)resident * device_sm_count();
+  if (most > most_blocks) most = most_blocks;
+  if (blocks > most) blocks = most;
+  kernel<<<(unsigned)blocks, threads, smem, stream>>>(a);
+  PE_CUDA_TRY(cudaGetLastError());
+  return launch_sum_parts(a.part, (int32_t)blocks, a.C, a.dweight, a.C, a.dbias, stream);
+}
+
+template <typename T, int V, int kIter, int kGroup>
+pe_status launch_ring(const Args<T>& a, cudaStream_t stream) {
+  constexpr int kGroups = kGroupsOf<V, kIter, kGroup, true>, kBlock = kGroup * kGroups;
+  constexpr size_t join = (size_t)kGroups * kIter * V * (kGroup + 1) * sizeof(float);
+  constexpr size_t ring = (size_t)kRing * 3 * kIter * 16 * kBlock;
+  constexpr size_t smem = join > ring ? join : ring;
+  static_assert(smem <= 226 << 10, "the ring fits an SM's shared memory");
+  const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup, true>;
+  static std::atomic<uint64_t> done{0};
+  PE_TRY(allow_shared_memory(kernel, (int)smem, done));
+  return launch_blocks(kernel, a, kGroups, kBlock, smem, 1, kMaxBlocks, stream);
+}
+
 template <typename T, int V, int kIter, int kGroup>
 pe_status launch(const Args<T>& a, cudaStream_t stream) {
   constexpr bool wide = kGroup > kThreads;
-  constexpr int kGroups = wide ? 1 : kThreads / kGroup;
+  constexpr int kGroups = kGroupsOf<V, kIter, kGroup, false>;
   static_assert(!wide || kIter * kGroup * V >= kMaxChannels, "a block holds the widest row");
   size_t smem = wide ? 2 * (size_t)a.C * sizeof(float)
                 : kGroups > 1 ? (size_t)kGroups * kIter * V * (kGroup + 1) * sizeof(float)
                               : 0;
-  const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup>;
+  const auto kernel = layernorm_bwd_kernel<T, V, kIter, kGroup, false>;
   if (a.N <= few_rows(a.C)) {
     smem += 2 * (size_t)a.C * sizeof(float);
     static_assert(wide || kGroups * kIter * V * (kGroup + 1) + 2 * kWide <= 56 * 256,
@@ -351,20 +450,23 @@ pe_status launch(const Args<T>& a, cudaStream_t stream) {
   }
   static const int resident =
       resident_blocks(kernel, kGroup * kGroups, wide ? 2 * kMaxChannels * sizeof(float) : smem);
-  if (resident < 1) return PE_ERR_CUDA;
-  int64_t blocks = ceil_div(a.N, kGroups), most = (int64_t)resident * device_sm_count();
-  if (most > (wide ? kMaxWideBlocks : kMaxBlocks)) most = wide ? kMaxWideBlocks : kMaxBlocks;
-  if (blocks > most) blocks = most;
-  kernel<<<(unsigned)blocks, kGroup * kGroups, smem, stream>>>(a);
-  PE_CUDA_TRY(cudaGetLastError());
-  return launch_sum_parts(a.part, (int32_t)blocks, a.C, a.dweight, a.C, a.dbias, stream);
+  return launch_blocks(kernel, a, kGroups, kGroup * kGroups, smem, resident,
+                       wide ? kMaxWideBlocks : kMaxBlocks, stream);
 }
 
 // The form for V neighbouring channels per access: vectors a thread and threads a row, by the
-// row's width. 16 channels a thread of bf16, 8 of fp32 (which take twice the registers); with
-// the residual's gradient:
-//   bf16 32299 x 768    16 channels of 64 threads 43.2 us, 8 of 96 41.6, 24 of 32 51
-//   bf16 169151 x 1024  16 of 64 220 us, 8 of 128 236;   90487 x 512  16 of 32 64, 8 of 64 68
+// row's width. With the residual's gradient, channels of threads by registers / by the ring:
+//   bf16 90487 x 512    16 of 32 61 us, 8 of 64 68       / 24 of 32 59, 16 of 32 61
+//        20000 x 256    8 of 32 12.8                     / 24 of 32 14.6, 8 of 32 12.8
+//        32299 x 768    8 of 96 41, 16 of 64 43          / 24 of 32 36, 16 of 64 38
+//        169151 x 1024  16 of 64 218, 8 of 128 236       / 24 of 64 207, 16 of 64 209
+//        20000 x 1536   16 of 128 52                     / 24 of 64 43
+//        32299 x 2304   16 of 256 124                    / 24 of 96 94
+//        20000 x 4096   16 of 256 112                    / 24 of 192 100
+//   fp32 90487 x 512    8 of 64 113                      / 8 of 96 110
+//        20000 x 768    8 of 128 45                      / 8 of 128 40, 12 of 64 42
+//        20000 x 1140   8 of 256 73                      / 12 of 192 70, 8 of 160 66
+//        20000 x 2304   16 of 256 147                    / 12 of 192 111
 template <typename T, int V>
 pe_status launch_rows(const Args<T>& a, cudaStream_t stream) {
   const int32_t C = a.C;
@@ -378,16 +480,21 @@ pe_status launch_rows(const Args<T>& a, cudaStream_t stream) {
   if constexpr (V == 8) {
     if (C <= 256) return launch<T, V, 1, 32>(a, stream);
     if (C <= 512) return launch<T, V, 2, 32>(a, stream);
-    if (C <= 768) return launch<T, V, 1, 96>(a, stream);
-    if (C <= 1024) return launch<T, V, 2, 64>(a, stream);
-    if (C <= 2048) return launch<T, V, 2, 128>(a, stream);
-    return launch<T, V, 2, 256>(a, stream);
+    if (C <= 768) return launch_ring<T, V, 3, 32>(a, stream);
+    if (C <= 1536) return launch_ring<T, V, 3, 64>(a, stream);
+    if (C <= 2304) return launch_ring<T, V, 3, 96>(a, stream);
+    return launch_ring<T, V, 3, 192>(a, stream);
   } else {
     constexpr int kIter = 8 / V;               // eight channels a thread
     if (C <= 256) return launch<T, V, kIter, 32>(a, stream);
     if (C <= 512) return launch<T, V, kIter, 64>(a, stream);
-    if (C <= 1024) return launch<T, V, kIter, 128>(a, stream);
-    if (C <= 2048) return launch<T, V, kIter, 256>(a, stream);
+    if constexpr (V * sizeof(T) == 16) {
+      if (C <= 1024) return launch_ring<T, V, 2, 128>(a, stream);
+      if (C <= 2304) return launch_ring<T, V, 3, 192>(a, stream);
+    } else {
+      if (C <= 1024) return launch<T, V, kIter, 128>(a, stream);
+      if (C <= 2048) return launch<T, V, kIter, 256>(a, stream);
+    }
     return launch<T, V, 2 * kIter, 256>(a, stream);
   }
 }

@@ -70,6 +70,26 @@ def test_layernorm_bwd_of_many_rows(n, c, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,c", [(193, 520), (300, 768), (193, 776), (2000, 1024), (97, 1028),
+                                 (700, 1040), (700, 1536), (700, 1544), (49, 2304), (700, 2304),
+                                 (700, 2312), (49, 4096), (461, 4096)])
+def test_layernorm_bwd_of_rows_in_shared_memory(n, c, dtype):
+    """Rows wide enough to wait in shared memory, from one more than one launch takes to
+    several a group of threads, with and without the residual's gradient, and in place."""
+    _check_layernorm_bwd(n, c, dtype, False, seed=7)
+    want = _check_layernorm_bwd(n, c, dtype, True, seed=8)
+    gen = _gen(8)
+    h = (_randn(gen, n, c) * torch.exp(0.5 * _randn(gen, c))).to(dtype)
+    dy = _randn(gen, n, c).to(dtype)
+    w = (1 + 0.3 * _randn(gen, c)).to(dtype)
+    r = _randn(gen, n, c).to(dtype)
+    for which in range(3):
+        t = [dy.clone(), h.clone(), r.clone()]
+        got = pe.pe_layernorm_bwd(t[0], t[1], w, 1e-5, dresidual=t[2], out=t[which])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_layernorm_bwd_with_a_large_mean(dtype):
     _check_layernorm_bwd(300, 768, dtype, False, seed=3, mean=100.0)
 
