@@ -450,7 +450,8 @@ pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int a_transpose
  *     dweight[c] = sum over tokens of dy n, dbias[c] = sum over tokens of dy.
  * dx is the gradient of x and of residual alike, in the I/O dtype; it may be the
  * buffer dy, h or dresidual. dweight and dbias (nullable) are fp32 [channels],
- * zeros when num_tokens is 0. A row of dx does not depend on the other rows.
+ * zeros when num_tokens is 0. A row of dx does not depend on what the other rows hold
+ * (the order of its sums goes by the width and by whether there are many rows).
  * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
  * finite and > 0, NULL required pointers; PE_ERR_UNSUPPORTED for other dtypes or
  * devices and more than 16384 channels. */

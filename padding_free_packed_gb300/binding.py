@@ -1027,7 +1027,10 @@ def _rope_target(out: torch.Tensor | None, name: str, src: torch.Tensor) -> torc
 
 @functools.lru_cache(maxsize=256)
 def _int32_array(numbers: tuple):
-    return (ctypes.c_int32 * len(numbers))(*(int(x) for x in numbers))
+    numbers = [int(x) for x in numbers]
+    if any(abs(x) >= 2 ** 31 for x in numbers):      # ctypes would cut them off
+        raise ValueError(f"numbers of 32 bits, got {numbers}")
+    return (ctypes.c_int32 * len(numbers))(*numbers)
 
 
 def pe_rope_axes(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, sections,

@@ -380,3 +380,26 @@ def test_training_step_of_a_feed_forward_block(dtype):
                                (y, dx, dw, db, dw1, db1, dw2, db2), (yd.detach(), *grads)):
         err = float((got.double() - want).abs().max() / want.abs().max())
         assert err <= tol, f"{name}: {err:.2e}"
+
+
+@pytest.mark.parametrize("ld", [32768, 32770])
+def test_matrices_past_2_to_the_31_elements(ld):
+    """Rows that lie far apart: the same numbers as the same matrices without gaps."""
+    far, small = 70001, 64
+    gen = _gen(61)
+    a = torch.empty(far, 32768, dtype=BF16, device=DEV)[:, :small]
+    a.copy_(_randn(gen, far, small))
+    out = torch.empty(far, ld, dtype=BF16, device=DEV)[:, :small]
+    pre = torch.empty(far, ld, dtype=BF16, device=DEV)[:, :small]
+    out.copy_(_randn(gen, far, small))
+    b = _randn(gen, small, small).bfloat16()
+    tight, tight_pre, near = a.contiguous(), torch.empty(far, small, dtype=BF16, device=DEV), \
+        out.contiguous()
+    want = pe.pe_matmul(tight, b, activation="relu", residual=near, pre=tight_pre)
+    pe.pe_matmul(a, b, activation="relu", residual=out, pre=pre, out=out)
+    assert torch.equal(out, want) and torch.equal(pre, tight_pre)
+    # The same rows as b of a product with few rows, and as both operands of a long sum.
+    x = _randn(gen, 3, small).bfloat16()
+    assert torch.equal(pe.pe_matmul(x, a), pe.pe_matmul(x, tight))
+    both = dict(dtype=FP32, a_transposed=True, b_transposed=True)
+    assert torch.equal(pe.pe_matmul(a, a, **both), pe.pe_matmul(tight, tight, **both))

@@ -446,3 +446,72 @@ def test_runs_are_bitwise_equal_on_any_stream_and_in_graphs(which):
     torch.cuda.synchronize()
     for out in outs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_layernorm_bwd_by_two_launches_in_two_graphs_at_a_time():
+    gen = _gen(41)
+    h, dy, r = (_randn(gen, 2000, 1024).bfloat16() for _ in range(3))
+    w = _randn(gen, 1024).bfloat16()
+    want = [t.clone() for t in pe.pe_layernorm_bwd(dy, h, w, dresidual=r)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(pe.pe_layernorm_bwd(dy, h, w, dresidual=r))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+
+def test_rows_past_2_to_the_31_elements():
+    """The last rows are those that a call on them alone gives: dx, dz and a dropout's elements
+    depend on nothing else (a dropout's on their index, which the definition counts in 64
+    bits)."""
+    c, n, tail = 1024, (1 << 21) + 300, 300
+    gen = _gen(42)
+    dy, h = (torch.empty(n, c, dtype=BF16, device=DEV).normal_(generator=gen) for _ in range(2))
+    w = _randn(gen, c).bfloat16()
+    dx = pe.pe_layernorm_bwd(dy, h, w)[0]
+    want = pe.pe_layernorm_bwd(dy[-tail:], h[-tail:], w)[0]
+    assert torch.equal(dx[-tail:], want)
+    del dx
+    dz, _ = pe.pe_activation_bwd(dy, h, "gelu")
+    assert torch.equal(dz[-tail:], pe.pe_activation_bwd(dy[-tail:], h[-tail:], "gelu")[0])
+    del dz
+    y = pe.pe_dropout(h, 0.3, 5, 6)
+    words = [w for block in range((n - 1) * c // 4, n * c // 4)
+             for w in ref.philox_words(block, 5, 6)]
+    kept = torch.tensor([word >= 0.3 * 2 ** 32 for word in words], device=DEV)
+    x = h[-1].double()
+    want = torch.where(kept, x / 0.7, 0.0)
+    ref.assert_within(y[-1], want, ref.rounded(2 * U * want.abs(), want, BF16), "dropout")
+
+
+def test_rope_of_tokens_past_2_to_the_31_elements():
+    n, step, tail = 70001, 32768, 50
+    store = torch.empty(n, step, dtype=BF16, device=DEV).normal_(generator=_gen(43))
+    q, k = store[:, :512].view(n, 8, 64), store[:, 1024:1280].view(n, 4, 64)
+    pos = torch.randint(0, 1 << 20, (2, n), dtype=torch.int32, device=DEV, generator=_gen(44))
+    want = pe.pe_rope_axes(q[-tail:].contiguous(), k[-tail:].contiguous(), pos[:, -tail:],
+                           (12, 20), 1e4)
+    untouched = store[-tail:, 512:1024].clone()
+    got = pe.pe_rope_axes(q, k, pos, (12, 20), 1e4, out_q=q, out_k=k)
+    for a, b in zip(got, want):
+        assert torch.equal(a[-tail:], b)
+    assert torch.equal(store[-tail:, 512:1024], untouched)
+
+
+def test_rope_refuses_sections_that_32_bits_do_not_hold():
+    q = torch.zeros(2, 1, 64, device=DEV)
+    pos = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        pe.pe_rope_axes(q, None, pos, (2 ** 32 + 32,), 1e4)
