@@ -814,7 +814,9 @@ def pe_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
     a_scales, b_scales = a_scales.contiguous(), b_scales.contiguous()
     out = _output(out, "out", (m, n), dtype if out is None else out.dtype, dev)
     need = lib.pe_matmul_fp8_workspace_size(m, n, k)
-    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
+    ws, ws_bytes = None, 0
+    if need or workspace is not None:
+        ws, ws_bytes = _workspace_for(workspace, need, dev)
     _call("pe_matmul_fp8", dev, a_code, a.data_ptr(), _fp8_ld(a), a_scales.data_ptr(), b_code,
           b.data_ptr(), _fp8_ld(b), b_scales.data_ptr(), m, n, k, _dtype_code(out.dtype),
           out.data_ptr(), _ptr(ws), ws_bytes)
@@ -913,7 +915,9 @@ def pe_matmul(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None
     if pre is not None:
         pre_ld = _row_tensor(pre, "pre", (m, n), out.dtype, dev)
     need = _matmul_workspace(code, bool(a_transposed), bool(b_transposed), m, n, k, act)
-    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
+    ws, ws_bytes = None, 0
+    if need or workspace is not None:
+        ws, ws_bytes = _workspace_for(workspace, need, dev)
     _call("pe_matmul", dev, code, a.data_ptr(), a_ld, a_transposed, b.data_ptr(), b_ld,
           b_transposed, m, n, k, _ptr(bias), act, _ptr(residual), residual_ld, out_code,
           out.data_ptr(), out_ld, _ptr(pre), pre_ld, _ptr(ws), ws_bytes)
@@ -938,7 +942,9 @@ def pe_layernorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
     dweight = torch.empty(c, dtype=torch.float32, device=dev)
     dbias = torch.empty(c, dtype=torch.float32, device=dev)
     need = lib.pe_layernorm_bwd_workspace_size(n, c)
-    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
+    ws, ws_bytes = None, 0
+    if need or workspace is not None:
+        ws, ws_bytes = _workspace_for(workspace, need, dev)
     _call("pe_layernorm_bwd", dev, _dtype_code(h.dtype), dy.data_ptr(), h.data_ptr(),
           weight.data_ptr(), _ptr(dresidual), n, c, float(eps), dx.data_ptr(),
           dweight.data_ptr(), dbias.data_ptr(), _ptr(ws), ws_bytes)
@@ -971,7 +977,7 @@ def pe_activation_bwd(dy: torch.Tensor, pre: torch.Tensor | None, activation="no
     if need_dbias:
         dbias = torch.empty(wide, dtype=torch.float32, device=dev)
         need = lib.pe_activation_bwd_workspace_size(act, n, f)
-        if need:
+        if need or workspace is not None:
             ws, ws_bytes = _workspace_for(workspace, need, dev)
     _call("pe_activation_bwd", dev, _dtype_code(dy.dtype), act, dy.data_ptr(), _ptr(pre), n,
           f, _ptr(dz), _ptr(dbias), _ptr(ws), ws_bytes)

@@ -191,6 +191,16 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
   return plan;
 }
 
+// Products of fp32 operands that are not worth their parts (m x n x k, us as they lie; by
+// parts): 4 x 8192 x 8192 111; 213, 8 x 2304 x 768 6.9; 12.0, 16 x 768 x 768 6.6; 9.8, 33 x 333
+// x 1001 10.9; 10.8, 64 x 64 x 64 2.4; 6.7, but 16 x 8192 x 8192 309; 214, 33 x 2304 x 768 21;
+// 13, 56 x 333 x 1001 12.7; 10.8, 5000 x 64 x 100 31; 11.8. By parts costs a launch and a
+// workspace more: 22 us a call from Python for 11.
+bool few(bool fp32, int64_t m, int64_t n, int64_t k, bool a_t, bool b_t) {
+  return fp32 && !a_t && !b_t &&
+         (m <= 4 || (m <= 64 && (double)m * (double)n * (double)k <= (double)(1 << 24)));
+}
+
 // Parts of slices, then parts of fp32 operands.
 size_t workspace_bytes_of(const LinearPlan& plan, bool fp32, int64_t m, int64_t n, int64_t k,
                           bool a_t, bool b_t) {
@@ -216,6 +226,7 @@ extern "C" size_t pe_matmul_workspace_size(pe_dtype dtype, int a_transposed, int
       !sizes_ok(m, n, k))
     return 0;
   const bool fp32 = dtype == PE_FP32;
+  if (few(fp32, m, n, k, a_transposed != 0, b_transposed != 0)) return 0;
   const LinearPlan plan =
       linear_plan(m, n, k, fp32, activation == PE_ACT_GEGLU, a_transposed != 0);
   return workspace_bytes_of(plan, fp32, m, n, k, a_transposed != 0, b_transposed != 0);
@@ -254,10 +265,11 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
   if (!aligned(out, size) || !aligned(bias, size) || !aligned(residual, size) ||
       !aligned(pre, size))
     return PE_ERR_UNSUPPORTED;
-  const LinearPlan plan = k == 0 ? LinearPlan{0, 1, 1, 1}
+  const bool direct = k == 0 || few(fp32, m, n, k, a_transposed != 0, b_transposed != 0);
+  const LinearPlan plan = direct ? LinearPlan{0, 1, 1, 1}
                                  : linear_plan(m, n, k, fp32, geglu, a_transposed != 0);
   const size_t need =
-      k == 0 ? 0 : workspace_bytes_of(plan, fp32, m, n, k, a_transposed != 0, b_transposed != 0);
+      direct ? 0 : workspace_bytes_of(plan, fp32, m, n, k, a_transposed != 0, b_transposed != 0);
   if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return PE_ERR_WORKSPACE;
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
@@ -282,6 +294,7 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
          out_dtype == PE_FP32 ? 1 : 0,
          four(out, out_ld) && four(residual, residual_ld) && four(pre, pre_ld) ? 1 : 0};
   if (k == 0) return matmul_no_sum(p, stream);
+  if (direct) return matmul_few(p, stream);
   DeviceStatus* status = nullptr;
   PE_TRY(matmul_status_word(&status));
   if (fp32)

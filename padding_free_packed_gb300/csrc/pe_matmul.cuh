@@ -70,6 +70,8 @@ pe_status matmul_no_sum(const Matmul& p, cudaStream_t stream);
 // cluster.
 pe_status matmul_narrow(const Matmul& p, int32_t rows, int32_t split, DeviceStatus* status,
                         cudaStream_t stream);
+// fp32 operands as they are, neither transposed, few products.
+pe_status matmul_few(const Matmul& p, cudaStream_t stream);
 
 namespace sm103 {
 

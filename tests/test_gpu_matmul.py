@@ -403,3 +403,26 @@ def test_matrices_past_2_to_the_31_elements(ld):
     assert torch.equal(pe.pe_matmul(x, a), pe.pe_matmul(x, tight))
     both = dict(dtype=FP32, a_transposed=True, b_transposed=True)
     assert torch.equal(pe.pe_matmul(a, a, **both), pe.pe_matmul(tight, tight, **both))
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 9, 64])
+@pytest.mark.parametrize("n,k", [(1, 3), (7, 130), (96, 768), (33, 1001), (64, 4100)])
+@pytest.mark.parametrize("act", ["none", "geglu"])
+def test_few_products_of_fp32(m, n, k, act):
+    """Rows by fours and what is left of them, one to eight warps a column, a last piece of k
+    of one to three elements; results in both types, inside wider matrices."""
+    n += n % 2 if act == "geglu" else 0
+    for out_dtype in (FP32, BF16):
+        _check(m, n, k, dtype=FP32, out_dtype=out_dtype, bias=True, act=act, residual=True,
+               pre=True, out_ld=(n // 2 if act == "geglu" else n) + 5)
+
+
+def test_few_products_of_rows_that_start_anywhere():
+    gen = _gen(67)
+    a, b = _randn(gen, 3, 66), _randn(gen, 40, 71)
+    want = pe.pe_matmul(a[:, 1:65].contiguous(), b[:, 3:67].contiguous())
+    got = pe.pe_matmul(a[:, 1:65], b[:, 3:67])
+    z = a[:, 1:65].double() @ b[:, 3:67].double().t()
+    bound = sum_error(64, a[:, 1:65].double().abs() @ b[:, 3:67].double().abs().t(), FP32)
+    ref.assert_within(got, z, ref.rounded(bound, z, FP32), "odd rows")
+    ref.assert_within(want, z, ref.rounded(bound, z, FP32), "the same, aligned")

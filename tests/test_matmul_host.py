@@ -83,12 +83,16 @@ def test_workspace(lib):
     assert size(0, 0, 0, 4, 8, 64, 9) == 0
     assert size(0, 0, 0, 4, -8, 64, NONE) == 0
     # Three parts of two bytes an element, rows rounded up to eight elements.
-    assert size(1, 0, 0, 5, 7, 9, NONE) == 6 * 16 * (5 + 7)
+    assert size(1, 0, 1, 5, 7, 9, NONE) == 6 * (5 * 16 + 9 * 8)
     assert size(1, 1, 0, 5, 7, 9, NONE) == 6 * (9 * 8 + 7 * 16)
-    need = size(1, 0, 0, 4, 8, 64, NONE)
-    assert _mm(lib, dtype=1, size=need - 1) == WORKSPACE
-    assert _mm(lib, dtype=1, ws=None) == WORKSPACE
-    assert _mm(lib, dtype=1, ws=24) == WORKSPACE
+    need = size(1, 0, 1, 4, 8, 64, NONE)
+    assert _mm(lib, dtype=1, tb=1, size=need - 1) == WORKSPACE
+    assert _mm(lib, dtype=1, tb=1, ws=None) == WORKSPACE
+    assert _mm(lib, dtype=1, tb=1, ws=24) == WORKSPACE
+    # Few products, neither operand transposed: multiplied as they lie.
+    assert size(1, 0, 0, 4, 100000, 4096, NONE) == 0
+    assert size(1, 0, 0, 64, 100, 1000, NONE) == 0
+    assert size(1, 0, 0, 320, 1000, 1000, NONE) == 6 * (320 + 1000) * 1000
 
 
 def test_binding_refuses_before_any_call(lib):
