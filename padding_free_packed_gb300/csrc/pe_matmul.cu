@@ -195,7 +195,7 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
 // parts): 4 x 8192 x 8192 111; 213, 8 x 2304 x 768 6.9; 12.0, 16 x 768 x 768 6.6; 9.8, 33 x 333
 // x 1001 10.9; 10.8, 64 x 64 x 64 2.4; 6.7, but 16 x 8192 x 8192 309; 214, 33 x 2304 x 768 21;
 // 13, 56 x 333 x 1001 12.7; 10.8, 5000 x 64 x 100 31; 11.8. By parts costs a launch and a
-// workspace more: 22 us a call from Python for 11.
+// workspace more: 20 us a call from Python for 12.
 bool few(bool fp32, int64_t m, int64_t n, int64_t k, bool a_t, bool b_t) {
   return fp32 && !a_t && !b_t &&
          (m <= 4 || (m <= 64 && (double)m * (double)n * (double)k <= (double)(1 << 24)));
