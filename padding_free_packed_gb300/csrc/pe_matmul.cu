@@ -124,7 +124,7 @@ pe_status split(Matmul& p, void* parts, cudaStream_t stream) {
 int64_t tile_count(int64_t m, int64_t n) { return ceil_div(m, 256) * ceil_div(n, 256); }
 
 // Estimated microseconds of every way, from times measured on a GB300 (m x n x k, bf16; T:
-// rows of a per CTA, S: split; tiles: on pairs, on clusters of two pairs):
+// rows of a per CTA, S: split; tiles: on pairs of CTAs):
 //   1 x 2304 x 768     T16 S1 6.8, S2 5.9, S4 5.2, S8 5.7   T64 S4 5.4      tiles 8.4
 //   1 x 768 x 2304     T16 S1 13.6, S4 6.9, S8 6.5          T64 S8 6.5      tiles 14.7
 //   64 x 768 x 768     T16 S4 5.7   T32 S4 5.9              T64 S2 6.9      tiles 8.9
@@ -133,11 +133,11 @@ int64_t tile_count(int64_t m, int64_t n) { return ceil_div(m, 256) * ceil_div(n,
 //   320 x 2304 x 768   T16 S1 14.1  T32 S1 8.1, S2 12.7     T64 S1 8.6      tiles 9.3
 //   640 x 2304 x 768                T32 S1 14.5             T64 S1 9.4      tiles 9.5
 //   2500 x 768 x 768                T32 S1 15.7             T64 S1 9.8      tiles 9.5
-//   20000 x 64 x 768                T32 S1 24.9             T64 S1 18.3     tiles 13.3, 17.6
+//   20000 x 64 x 768                T32 S1 24.9             T64 S1 18.3     tiles 13.3
 // A narrow CTA takes 0.28 for each block of k beside its start and its rows, half as much
-// again where two share an SM, and what is left over after 304 takes a second turn. A tile takes 0.26 for each block
-// with up to 136 SMs at work or with two pairs a cluster (which hold 144), 0.27 with all, and
-// 0.5 between two. Slices pay for parts that are written and read:
+// again where two share an SM, and what is left over after 304 takes a second turn. A tile
+// takes 0.26 for each block with up to 136 SMs at work, 0.27 with all, and 0.5 between two.
+// Slices pay for parts that are written and read:
 //   2304 x 768 x 32299 to fp32, 27 tiles   1: 142, 2: 84, 4: 92, 5: 82, 8: 85, 12: 101
 //   768 x 768 x 32299, 9 tiles             1: 142, 2: 79, 4: 47, 6: 39, 8: 37, 9: 52, 16: 43
 //   1024 x 1024 x 169151, 16 tiles         2: 361, 4: 212, 5: 331, 8: 220, 9: 208, 12: 230
@@ -146,16 +146,9 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
   constexpr int64_t kSms = 152, kPairs = kSms / 2;
   const int64_t blocks = ceil_div(k, kMatmulBlock) * (fp32 ? kMaxMatmulTerms : 1);
   const int64_t tiles = tile_count(m, n);
-  LinearPlan plan = {0, 1, 1, 1};
+  LinearPlan plan = {0, 1, 1};
   double best = 5.5 + (double)ceil_div(tiles, kPairs) *
                           ((tiles <= 68 ? 0.26 : 0.27) * (double)blocks + 0.5);
-  const int64_t doubles = ceil_div(m, 512) * ceil_div(n, 256);
-  const double two =
-      5.5 + (double)ceil_div(doubles, kMatmulClusters) * (0.26 * (double)blocks + 0.5);
-  if (two < best) {
-    best = two;
-    plan.pairs = 2;
-  }
   // Slices of eight blocks at least.
   for (int32_t slices = 2; slices <= 16 && slices * 8 <= blocks && tiles <= 4 * kPairs; ++slices) {
     const int64_t units = tiles * slices;
@@ -164,7 +157,6 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
                      0.1 * (double)units;
     if (t < best) {
       best = t;
-      plan.pairs = 1;
       plan.slices = slices;
     }
   }
@@ -184,7 +176,7 @@ LinearPlan linear_plan(int64_t m, int64_t n, int64_t k, bool fp32, bool geglu,
       t += (double)(ceil_div(units, 2 * kSms) - 1) * (t - 2);
       if (t < best) {
         best = t;
-        plan = {kRows[i], split, 1, 1};
+        plan = {kRows[i], split, 1};
       }
     }
   }
@@ -266,7 +258,7 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
       !aligned(pre, size))
     return PE_ERR_UNSUPPORTED;
   const bool direct = k == 0 || few(fp32, m, n, k, a_transposed != 0, b_transposed != 0);
-  const LinearPlan plan = direct ? LinearPlan{0, 1, 1, 1}
+  const LinearPlan plan = direct ? LinearPlan{0, 1, 1}
                                  : linear_plan(m, n, k, fp32, geglu, a_transposed != 0);
   const size_t need =
       direct ? 0 : workspace_bytes_of(plan, fp32, m, n, k, a_transposed != 0, b_transposed != 0);
@@ -303,5 +295,5 @@ extern "C" pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int 
                      matmul_tiles_workspace(tile_count(m, n), plan.slices),
                  stream));
   if (plan.rows) return matmul_narrow(p, plan.rows, plan.split, status, stream);
-  return matmul_tiles(p, plan.pairs, plan.slices, workspace, status, stream);
+  return matmul_tiles(p, plan.slices, workspace, status, stream);
 }

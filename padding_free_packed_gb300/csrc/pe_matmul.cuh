@@ -43,12 +43,8 @@ struct Matmul {
 struct LinearPlan {
   int32_t rows;            // of a per CTA of the narrow kernel: 16, 32 or 64; 0: tiles
   int32_t split;           // narrow: CTAs of a cluster that share a tile's sum
-  int32_t pairs;           // tiles: pairs of CTAs in a cluster, 1 or 2
   int32_t slices;          // tiles: of k, their sums added by a second kernel (1: none)
 };
-// Clusters of four CTAs that a GB300 holds at a time, one CTA an SM (its GPCs' SMs in fours:
-// 144 of the 152).
-constexpr int32_t kMatmulClusters = 36;
 
 constexpr int kMaxMatmulTerms = 6;
 // Products of parts of x = h + m + l, the smallest first: l h, h l, m m, m h, h m, h h. A part
@@ -62,8 +58,8 @@ __host__ __device__ __forceinline__ int32_t term_b(int32_t term, int32_t terms) 
 
 // Tiles of 256 x 256 (or slices of their sums) on pairs of CTAs.
 size_t matmul_tiles_workspace(int64_t tiles, int32_t slices);
-pe_status matmul_tiles(const Matmul& p, int32_t pairs, int32_t slices, void* workspace,
-                       DeviceStatus* status, cudaStream_t stream);
+pe_status matmul_tiles(const Matmul& p, int32_t slices, void* workspace, DeviceStatus* status,
+                       cudaStream_t stream);
 // What is left of a product without a sum: z = bias.
 pe_status matmul_no_sum(const Matmul& p, cudaStream_t stream);
 // Few rows: 128 rows of b by 16, 32 or 64 rows of a per CTA, the sum over k split over a

@@ -7,11 +7,8 @@
 // epilogue of a tile runs under the next tile's MMAs. An operand stored with k as its rows is
 // loaded in boxes of 64 columns by 64 rows and read by the MMA as it lies there.
 //
-// Two pairs with neighbouring row tiles can form a cluster and share their rows of b: each CTA
-// loads half of what it needs of b and multicasts it to the CTA that needs the same, 24 KiB a
-// block instead of 32. Clusters of four leave 8 of the 152 SMs idle, and the two ways are
-// close (32299 x 2304 x 768 for a second on end: 82.0 us, pairs alone 84.7); the plan goes by
-// which has fewer turns.
+// Every CTA loads its own rows by itself: no load writes into another CTA's shared memory, so
+// that the kernel can run in any process, one of several GPUs' among them.
 //
 //   warps 0, 2   loads of a and of b (every CTA), a ring of kStages blocks
 //   warp 1       MMA issue (first CTA of each pair)
@@ -96,8 +93,8 @@ struct alignas(1024) Smem {
   uint64_t residual[8];                        // the box's residual has arrived
   uint64_t drain;
   int32_t loaded[2];                           // blocks of a, of b that this CTA loaded
-  int32_t issued[2][4];                        // the same of every CTA of the cluster, and
-  int32_t aborted[4];                          // whether one of its waits gave up
+  int32_t issued[2][2];                        // the same of both CTAs, and whether one of
+  int32_t aborted[2];                          // their waits gave up
   uint32_t tmem_base;
   WaitGuard guard;
 };
@@ -128,9 +125,9 @@ struct Params {
   int32_t terms;
   int32_t a_transposed, b_transposed;
   int32_t up_row;            // geglu: b's first up row
-  int32_t row_units;         // rows of tiles, a cluster's pairs together
+  int32_t row_tiles;
   int32_t col_tiles;
-  int32_t tiles;             // row_units * col_tiles
+  int32_t tiles;             // row_tiles * col_tiles
   int32_t slices;            // of k; more than one: sums through `parts`
   int32_t slice_blocks;      // blocks of a slice; the first slices
   int32_t slice_more;        // have one more
@@ -169,18 +166,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-// The same into the CTAs of `mask`, at the same place in each, counted on the barrier of each
-// one's pair.
-__device__ __forceinline__ void tma_load_shared(uint32_t dst, const CUtensorMap* map,
-                                                uint32_t bar, int32_t x, int32_t y, int32_t z,
-                                                uint16_t mask) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(mask)
       : "memory");
 }
 // The same box into the L2 cache only.
@@ -223,25 +208,25 @@ __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_low, uint3
 #undef PE_MMA
 #undef PE_NEXT
 }
-// Arrives once on this barrier in the CTAs of `mask` when the MMAs issued so far complete.
-__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
+// Arrives once on this barrier of both CTAs when the MMAs issued so far complete.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;\n\t}" ::"r"(bar),
-      "h"(mask)
+      "h"(uint16_t{3})
       : "memory");
 }
-// Tiles are dealt in bands of four rows, down the rows first, so that the clusters at work
+// Tiles are dealt in bands of four rows, down the rows first, so that the pairs at work
 // share operands in L2 both ways.
 constexpr int32_t kBand = 4;
 __device__ __forceinline__ void place(const Params& p, int32_t tile, int32_t& row, int32_t& col) {
   const int32_t band = p.by_band.quotient(tile), rest = tile - band * (int32_t)p.by_band.d;
-  const int32_t left = p.row_units - band * kBand;
+  const int32_t left = p.row_tiles - band * kBand;
   col = left >= kBand ? rest / kBand : left == 1 ? rest : left == 2 ? rest / 2 : rest / 3;
   row = band * kBand + rest - col * (left < kBand ? left : kBand);
 }
 
-// The work of a cluster: units, of a tile and a slice of its blocks of k, slice by slice.
+// The work of a pair: units, of a tile and a slice of its blocks of k, slice by slice.
 struct Walk {
   int32_t unit, tile;
   int32_t first, last;            // last: one past the unit's last block
@@ -409,30 +394,28 @@ __device__ __forceinline__ void apply_gelu(float (&z)[32]) {
   }
 }
 
-template <int kOut, bool kGeglu, int kPairs>
+template <int kOut, bool kGeglu>
 __global__ void __launch_bounds__(kThreads, 1)
 matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int32_t cta = (int32_t)cluster_rank();            // in the cluster
-  const int32_t rank = cta & 1, pair = cta >> 1;          // in the pair; of the cluster's pairs
-  const int32_t cluster = blockIdx.x / (2 * kPairs), clusters = gridDim.x / (2 * kPairs);
-  constexpr uint16_t kAll = (1 << 2 * kPairs) - 1;
+  const int32_t rank = (int32_t)cluster_rank();           // in the pair
+  const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   volatile WaitGuard* guard = &s.guard;
   constexpr int32_t kOutCols = kGeglu ? kTile / 2 : kTile;   // of a tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), kPairs);
+      mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.acc_full[i]), 1);
       mbar_init(smem_u32(&s.acc_empty[i]), 16);
     }
     for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&s.residual[i]), 1);
-    mbar_init(smem_u32(&s.drain), kPairs);
+    mbar_init(smem_u32(&s.drain), 1);
     s.guard.abort = 0;
     s.guard.limit_ns = p.wait_limit_ns;
     fence_mbarrier_init();
@@ -460,47 +443,39 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
     auto load = [&](auto of_b, auto is_transposed) {
       constexpr bool kB = decltype(of_b)::value, kTransposed = decltype(is_transposed)::value;
       const CUtensorMap* map = kB ? &maps.b : &maps.a;
-      const uint32_t to0 = smem_u32(kB ? s.b[0] : s.a[0]) +
-                           (kB && kPairs == 2 ? pair * (kOperandBytes / 2) : 0);
-      const uint32_t full0 = peer_address(smem_u32(&s.full[0]), (uint32_t)(cta & ~1));
+      const uint32_t to0 = smem_u32(kB ? s.b[0] : s.a[0]);
+      const uint32_t full0 = peer_address(smem_u32(&s.full[0]), 0);
       const uint32_t full_own = smem_u32(&s.full[0]), empty0 = smem_u32(&s.empty[0]);
-      // This CTA's place in a tile's rows of the operand, and the CTAs that need the same
-      // rows of b.
-      const int32_t in_tile = kB && kPairs == 2 ? pair * 64 : 0;
-      const uint16_t sharers = (uint16_t)(5 << rank);
       const int32_t x_end = p.term_blocks * kMatmulBlock;
       int32_t issued = 0;
       uint32_t stage = 0, parity = 1;
       bool ok = true;
       Walk w;
       int32_t next_row, next_col;                      // of tiles
-      bool more = w.at(p, cluster);
+      bool more = w.at(p, pair);
       place(p, w.tile, next_row, next_col);
-      for (; more && ok; more = w.at(p, w.unit + clusters)) {
-        const int32_t at = in_tile + (!kB      ? (next_row * kPairs + pair) * kTile + rank * kRows
-                                      : kGeglu ? next_col * kOutCols + (rank ? p.up_row : 0)
-                                               : next_col * kTile + rank * kRows);
+      for (; more && ok; more = w.at(p, w.unit + pairs)) {
+        const int32_t at = !kB      ? next_row * kTile + rank * kRows
+                           : kGeglu ? next_col * kOutCols + (rank ? p.up_row : 0)
+                                    : next_col * kTile + rank * kRows;
         int32_t term = p.terms == 1 ? 0 : w.first / p.term_blocks;
         int32_t x = (w.first - term * p.term_blocks) * kMatmulBlock;
         int32_t z = kB ? term_b(term, p.terms) : term_a(term, p.terms);
-        // The rows of a that this CTA's next tile reads, which the clusters on its row of
+        // The rows of a that this CTA's next tile reads, which the pairs on its row of
         // tiles share out, go to L2 under this tile: from HBM a block takes longer than
         // the ring is deep (169151 x 1024 x 1024 222 us without, 217 with; with residual
         // 253, 243).
         Walk next;
-        const bool ahead = next.at(p, w.unit + clusters) && p.slices == 1;
+        const bool ahead = next.at(p, w.unit + pairs) && p.slices == 1;
         place(p, next.tile, next_row, next_col);
-        const int32_t ahead_at = (next_row * kPairs + pair) * kTile + rank * kRows;
+        const int32_t ahead_at = next_row * kTile + rank * kRows;
         int32_t until = !kB && !kTransposed && ahead ? next_col : 0x7fffffff;
         for (int32_t left = w.last - w.first; left > 0; --left) {
           ok = eager_warp_wait(empty0 + stage * 8, parity, guard, p.status, kSiteProducer);
           if (!ok) break;
           const uint32_t bar = full0 + stage * 8, to = to0 + stage * kOperandBytes;
           if (!kB && rank == 0) expect_pair(full_own + stage * 8);
-          if constexpr (kB && kPairs == 2) {           // one of two boxes, for two pairs
-            tma_load_shared(to, map, bar, kTransposed ? at : x, kTransposed ? x : at, z,
-                            sharers);
-          } else if constexpr (kTransposed) {          // 64 columns by 64 rows a box
+          if constexpr (kTransposed) {                 // 64 columns by 64 rows a box
             tma_load_pair(to, map, bar, at, x, z);
             tma_load_pair(to + kOperandBytes / 2, map, bar, at + 64, x, z);
           } else {
@@ -547,13 +522,12 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       constexpr bool kBT = decltype(b_is_transposed)::value;
       const uint64_t desc_a = smem_desc_sw128(smem_u32(s.a[0]), kAT ? 8192 : 16, 1024);
       const uint64_t desc_b = smem_desc_sw128(smem_u32(s.b[0]), kBT ? 8192 : 16, 1024);
-      const uint16_t both = (uint16_t)(3 << (cta & ~1));   // this pair's CTAs
       const uint32_t full0 = smem_u32(&s.full[0]), empty0 = smem_u32(&s.empty[0]);
       uint32_t stage = 0, parity = 0;
       int32_t turn = 0;                  // of the accumulators
       bool ok = true;
       Walk w;
-      for (bool more = w.at(p, cluster); more && ok; more = w.at(p, w.unit + clusters)) {
+      for (bool more = w.at(p, pair); more && ok; more = w.at(p, w.unit + pairs)) {
         for (int32_t block = w.first; block < w.last && ok; ++turn) {
           const uint32_t buf = turn & 1, d = tmem + buf * kTile;
           const int32_t end = w.last - block < chunk_of(kOut) ? w.last : block + chunk_of(kOut);
@@ -568,14 +542,14 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
                 d, (uint32_t)desc_a + stage * (kOperandBytes / 16), (uint32_t)(desc_a >> 32),
                 (uint32_t)desc_b + stage * (kOperandBytes / 16), (uint32_t)(desc_b >> 32),
                 p.idesc, accumulate);
-            commit_pair(empty0 + stage * 8, kAll);
+            commit_pair(empty0 + stage * 8);
             accumulate = 1;
             if (++stage == kStages) {
               stage = 0;
               parity ^= 1;
             }
           }
-          if (ok) commit_pair(smem_u32(&s.acc_full[buf]), both);
+          if (ok) commit_pair(smem_u32(&s.acc_full[buf]));
         }
       }
     };
@@ -590,14 +564,14 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       else
         issue(std::false_type(), std::false_type());
     }
-    commit_pair(smem_u32(&s.drain), kAll);   // waited for below: no MMA in flight past that
+    commit_pair(smem_u32(&s.drain));         // waited for below: no MMA in flight past that
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     if constexpr (is_fp32(kOut)) regs_claim<kRegsHigh>();
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const int32_t row_in = rank * kRows + quad * 32;            // this warp's rows in the tile
-    const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[0]), (uint32_t)(cta & ~1));
+    const uint32_t acc_empty = peer_address(smem_u32(&s.acc_empty[0]), 0);
     // This warp's box, this thread's row of it, and the barrier that counts its residuals.
     const uint32_t box = smem_u32(s.box[warp - 4]);
     const uint32_t box_row = box + lane * 128 + ((lane & 7) << 4);
@@ -609,12 +583,12 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
     int32_t turn = 0;                      // of the accumulators
     bool ok = true;
     Walk w;
-    for (bool more = w.at(p, cluster); more; more = w.at(p, w.unit + clusters)) {
+    for (bool more = w.at(p, pair); more; more = w.at(p, w.unit + pairs)) {
       int32_t tile_row, tile_col;
       place(p, w.tile, tile_row, tile_col);
-      const int32_t row0 = (tile_row * kPairs + pair) * kTile + row_in;
+      const int32_t row0 = tile_row * kTile + row_in;
       const int32_t col0 = tile_col * kOutCols + half * (kOutCols / 2);
-      const bool whole = kPairs == 2 || p.slices == 1;
+      const bool whole = p.slices == 1;
       const bool stored = whole && row0 < p.e.m && col0 < p.e.n;
       bool loading = false;                // the box's residual is on its way
       auto load_residual = [&](int32_t col) {
@@ -806,21 +780,21 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (uint32_t to = 0; to < 2 * kPairs; ++to) {
+    for (uint32_t to = 0; to < 2; ++to) {
       for (int i = 0; i < 2; ++i)
-        store_cluster_i32(peer_address(smem_u32(&s.issued[i][cta]), to), s.loaded[i]);
-      store_cluster_i32(peer_address(smem_u32(&s.aborted[cta]), to), s.guard.abort);
+        store_cluster_i32(peer_address(smem_u32(&s.issued[i][rank]), to), s.loaded[i]);
+      store_cluster_i32(peer_address(smem_u32(&s.aborted[rank]), to), s.guard.abort);
     }
   }
   __syncthreads();
   cluster_sync();
   if (threadIdx.x == 0) {
-    // The issuing warps' last commits arrive in every CTA, which stays until they, and so
-    // every arrival before them, have reached its barriers.
+    // The issuing warp's last commit arrives in both CTAs, which stay until it, and so every
+    // arrival before it, has reached their barriers.
     mbar_drain_wait(smem_u32(&s.drain), 0);
     bool aborted = false;
     int32_t fewest = s.loaded[0], most = s.loaded[0];
-    for (int i = 0; i < 2 * kPairs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       aborted |= s.aborted[i] != 0;
       for (int j = 0; j < 2; ++j) {
         fewest = s.issued[j][i] < fewest ? s.issued[j][i] : fewest;
@@ -832,9 +806,9 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       // on this pair's barrier, then every load that may be in flight is waited for.
       for (int32_t i = fewest; i < most; ++i) {
         uint32_t bytes = 0;                // into the pair's CTAs
-        for (int j = 0; j < 2 * kPairs; ++j) {
-          if (j >> 1 == pair && s.issued[0][j] > i) bytes += kOperandBytes;
-          if (s.issued[1][j] > i) bytes += kOperandBytes / kPairs;
+        for (int j = 0; j < 2; ++j) {
+          if (s.issued[0][j] > i) bytes += kOperandBytes;
+          if (s.issued[1][j] > i) bytes += kOperandBytes;
         }
         const uint32_t bar = smem_u32(&s.full[i % kStages]);
         if (s.loaded[0] <= i)              // nothing was expected yet
@@ -932,7 +906,7 @@ matmul_parts_kernel(const __grid_constant__ Params p) {
 }
 
 // ---------------------------------------------------------------- host side
-Params base_params(const Matmul& q, int pairs) {
+Params base_params(const Matmul& q) {
   Params p = {};
   p.e = q.e;
   p.term_blocks = (int32_t)ceil_div(q.k, kMatmulBlock);
@@ -942,9 +916,9 @@ Params base_params(const Matmul& q, int pairs) {
   p.b_transposed = q.b.transposed ? 1 : 0;
   const bool geglu = q.e.act == PE_ACT_GEGLU;
   p.up_row = geglu ? q.e.n : 0;
-  p.row_units = (int32_t)ceil_div(q.m, kTile * pairs);
+  p.row_tiles = (int32_t)ceil_div(q.m, kTile);
   p.col_tiles = (int32_t)ceil_div(q.e.n, geglu ? kTile / 2 : kTile);
-  p.tiles = p.row_units * p.col_tiles;
+  p.tiles = p.row_tiles * p.col_tiles;
   p.by_band = Divisor::of(kBand * p.col_tiles);
   p.by_tiles = Divisor::of(p.tiles);
   p.idesc = idesc_bf16(256, 256, q.a.transposed, q.b.transposed);
@@ -961,16 +935,16 @@ pe_status launch_parts(const Params& p, cudaStream_t stream) {
 }
 
 pe_status operand_map(CUtensorMap* map, const MatmulOperand& x, int32_t rows, int32_t k,
-                      int32_t planes, uint32_t box_rows) {
+                      int32_t planes) {
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return x.transposed
              ? matmul_map_planes(map, bf16, 2, x.base, k, rows, x.ld * 2, 64, planes)
-             : matmul_map_planes(map, bf16, 2, x.base, rows, k, x.ld * 2, box_rows, planes);
+             : matmul_map_planes(map, bf16, 2, x.base, rows, k, x.ld * 2, kRows, planes);
 }
 
-template <int kOut, bool kGeglu, int kPairs>
+template <int kOut, bool kGeglu>
 pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) {
-  const auto kernel = matmul_tiles_kernel<kOut, kGeglu, kPairs>;
+  const auto kernel = matmul_tiles_kernel<kOut, kGeglu>;
   const size_t smem = sizeof(Smem) + 1024;
   static std::atomic<uint64_t> done{0};
   PE_TRY(allow_shared_memory(kernel, static_cast<int>(smem), done));
@@ -982,17 +956,15 @@ pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) 
     if (static_cast<uint32_t>(registers) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
       return PE_ERR_UNSUPPORTED;
   }
-  // Clusters that fit at a time: each takes as many of one GPC's SMs as it has CTAs.
-  const int64_t work = (int64_t)p.tiles * p.slices;
-  const int64_t fit = kPairs == 2 ? kMatmulClusters : device_sm_count() / 2;
+  const int64_t work = (int64_t)p.tiles * p.slices, fit = device_sm_count() / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * kPairs * (work < fit ? work : fit)));
+  cfg.gridDim = dim3((unsigned)(2 * (work < fit ? work : fit)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * kPairs;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1003,13 +975,13 @@ pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) 
   return PE_OK;
 }
 
-template <bool kGeglu, int kPairs>
+template <bool kGeglu>
 pe_status launch_out(bool boxes, const Maps& maps, const Params& p, cudaStream_t stream) {
   if (p.e.out_fp32)
-    return boxes ? launch_kernel<kOutFp32, kGeglu, kPairs>(maps, p, stream)
-                 : launch_kernel<kOutFp32Anywhere, kGeglu, kPairs>(maps, p, stream);
-  return boxes ? launch_kernel<kOutBf16, kGeglu, kPairs>(maps, p, stream)
-               : launch_kernel<kOutBf16Anywhere, kGeglu, kPairs>(maps, p, stream);
+    return boxes ? launch_kernel<kOutFp32, kGeglu>(maps, p, stream)
+                 : launch_kernel<kOutFp32Anywhere, kGeglu>(maps, p, stream);
+  return boxes ? launch_kernel<kOutBf16, kGeglu>(maps, p, stream)
+               : launch_kernel<kOutBf16Anywhere, kGeglu>(maps, p, stream);
 }
 
 }  // namespace
@@ -1019,14 +991,14 @@ size_t matmul_tiles_workspace(int64_t tiles, int32_t slices) {
 }
 
 pe_status matmul_no_sum(const Matmul& q, cudaStream_t stream) {
-  return launch_parts(base_params(q, 1), stream);
+  return launch_parts(base_params(q), stream);
 }
 
-pe_status matmul_tiles(const Matmul& q, int32_t pairs, int32_t slices, void* workspace,
+pe_status matmul_tiles(const Matmul& q, int32_t slices, void* workspace,
                        DeviceStatus* status, cudaStream_t stream) {
   Maps maps;
-  PE_TRY(operand_map(&maps.a, q.a, q.m, q.k, q.planes, kRows));
-  PE_TRY(operand_map(&maps.b, q.b, q.n, q.k, q.planes, kRows / pairs));
+  PE_TRY(operand_map(&maps.a, q.a, q.m, q.k, q.planes));
+  PE_TRY(operand_map(&maps.b, q.b, q.n, q.k, q.planes));
   const MatmulEpilogue& e = q.e;
   const bool geglu = e.act == PE_ACT_GEGLU;
   const int size = e.out_fp32 ? 4 : 2;
@@ -1048,17 +1020,14 @@ pe_status matmul_tiles(const Matmul& q, int32_t pairs, int32_t slices, void* wor
     PE_TRY(map(&maps.pre, e.pre, e.pre_ld));
     PE_TRY(map(&maps.pre_up, e.pre ? pre_up : nullptr, e.pre_ld));
   }
-  Params p = base_params(q, pairs);
+  Params p = base_params(q);
   p.slices = slices;
   p.slice_blocks = p.blocks / slices;
   p.slice_more = p.blocks % slices;
   p.status = status;
   p.parts = static_cast<float*>(workspace);
-  if (pairs == 2)
-    return geglu ? launch_out<true, 2>(tma, maps, p, stream)
-                 : launch_out<false, 2>(tma, maps, p, stream);
-  PE_TRY((geglu ? launch_out<true, 1>(tma, maps, p, stream)
-                : launch_out<false, 1>(tma, maps, p, stream)));
+  PE_TRY(geglu ? launch_out<true>(tma, maps, p, stream)
+               : launch_out<false>(tma, maps, p, stream));
   return slices == 1 ? PE_OK : launch_parts(p, stream);
 }
 
