@@ -3,7 +3,7 @@
 //
 // A pair of CTAs (tcgen05 cta_group::2) works on a 256 x 256 tile: each CTA loads 128 rows of
 // a and 128 rows of b, 64 elements of k at a time, and the pair's MMAs (M = 256, N = 256, K =
-// 16) sum a tile over the whole of k in tensor memory. Two accumulators take turns, so the
+// 16) sum a tile in tensor memory, over the whole of k or a chain of its blocks. Two accumulators take turns, so the
 // epilogue of a tile runs under the next tile's MMAs. An operand stored with k as its rows is
 // loaded in boxes of 64 columns by 64 rows and read by the MMA as it lies there.
 //
@@ -65,21 +65,33 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBoxBytes = 32 * 128;                 // 32 rows of 128 bytes
 // How rows of out, residual and pre move between a warp's box and memory: by TMA or, where
 // rows start anywhere, by the warp's lanes.
-enum Out { kOutBf16 = 0, kOutFp32 = 1, kOutBf16Anywhere = 2, kOutFp32Anywhere = 3 };
+enum Out {
+  kOutBf16 = 0,
+  kOutFp32 = 1,
+  kOutBf16Anywhere = 2,
+  kOutFp32Anywhere = 3,
+  kOutBf16Long = 4,                    // sums of more than kLongest blocks
+  kOutBf16AnywhereLong = 6
+};
 constexpr bool is_fp32(int out) { return out & 1; }
-constexpr bool by_tma(int out) { return out < 2; }
+constexpr bool by_tma(int out) { return !(out & 2); }
 
 constexpr uint32_t kRegsLaunch = 168;
 constexpr uint32_t kRegsLow = 40, kRegsHigh = 232;
 static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
-// Blocks of k that one accumulator sums: all of them for results rounded to bf16; for fp32
-// results a few, whose sums are then added in fp32 registers. The tensor cores cut the sum
-// off after every 16 products (1.7e-8 of it a time, always towards zero, measured), which a
-// chain of 11500 products turned into 1.2e-5 of the result. Eight blocks leave 5e-7, for 532
-// cycles a block where all of them take 516; four leave 3e-7, for 560.
+// Blocks of k that one accumulator sums. The tensor cores align 16 products and the sum so far
+// to the largest of them and cut them off towards zero, so a chain of additions of numbers of
+// one sign loses a share that grows with its length: k = 4096 1.1e-5 of the sum, 8192 3.2e-5,
+// 2^17 8e-4, 2^19 3.3e-3, which a result rounded to bf16 (2e-3 to 4e-3) shows. So results
+// rounded to bf16 have chains of kLongest blocks at most; fp32 results, and longer sums, add chains of kChunk in fp32
+// registers: 1.1e-7 of the sum of magnitudes lost in the mean, 3.5e-7 at most, whatever k
+// (elementary fp32 operations: 1.1e-5 at most over 32299). Of one accumulator a block takes
+// 516 cycles, of chains of eight 532 (32299 x 768 x 2304 to fp32), of four 560.
+constexpr int32_t kLongest = 128;
 constexpr int32_t kChunk = 8;
-constexpr int32_t chunk_of(int out) { return is_fp32(out) ? kChunk : 0x7fffffff; }
+constexpr bool by_chunks(int out) { return is_fp32(out) || (out & kOutBf16Long); }
+constexpr int32_t chunk_of(int out) { return by_chunks(out) ? kChunk : 0x7fffffff; }
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 constexpr int kPartsAhead = 5, kPartBlocks = 4;          // parts in flight; blocks an SM
 
@@ -437,7 +449,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
-  if (is_fp32(kOut) && warp < 4) regs_release<kRegsLow>();
+  if (by_chunks(kOut) && warp < 4) regs_release<kRegsLow>();
   if (warp == 0 || warp == 2) {
     // ---------------------------------------------------------- loads
     auto load = [&](auto of_b, auto is_transposed) {
@@ -567,7 +579,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
     commit_pair(smem_u32(&s.drain));         // waited for below: no MMA in flight past that
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    if constexpr (is_fp32(kOut)) regs_claim<kRegsHigh>();
+    if constexpr (by_chunks(kOut)) regs_claim<kRegsHigh>();
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const int32_t row_in = rank * kRows + quad * 32;            // this warp's rows in the tile
@@ -633,9 +645,9 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc_empty + buf * 8);
       };
-      float sum[is_fp32(kOut) ? kRows : 1];
+      float sum[by_chunks(kOut) ? kRows : 1];
       uint32_t buf = turn & 1;
-      if constexpr (is_fp32(kOut)) {
+      if constexpr (by_chunks(kOut)) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
         for (int32_t block = w.first; block < w.last; block += kChunk, ++turn) {
@@ -665,7 +677,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
         continue;
       }
       auto load = [&](int u, float (&z)[32]) {
-        if constexpr (is_fp32(kOut)) {
+        if constexpr (by_chunks(kOut)) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) z[i] = sum[32 * u + i];
         } else {
@@ -687,7 +699,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
                   make_float4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]);
           }
         }
-        if (!is_fp32(kOut)) hand_back(buf);
+        if (!by_chunks(kOut)) hand_back(buf);
         continue;
       }
       // The box to columns `col` .. of a tensor (its map; its address and rows, of p.e.n
@@ -708,9 +720,9 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       // Loops over the accumulator's columns stay loops where the sums are not in registers:
       // unrolled, their code pushed the MMA warp's out of the instruction cache.
       if (p.e.pre) {                       // z, before anything else
-#pragma unroll(is_fp32(kOut) ? 2 : 1)
+#pragma unroll(by_chunks(kOut) ? 2 : 1)
         for (int part = 0; part < (kGeglu ? 2 : 1); ++part) {
-#pragma unroll(is_fp32(kOut) ? 4 : 1)
+#pragma unroll(by_chunks(kOut) ? 4 : 1)
           for (int u = 0; u < kUnits; ++u) {
             float z[32];
             load(part * 2 + u, z);
@@ -724,7 +736,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
           }
         }
       }
-#pragma unroll(is_fp32(kOut) ? 4 : 1)
+#pragma unroll(by_chunks(kOut) ? 4 : 1)
       for (int u = 0; u < kUnits; ++u) {
         const int32_t col = col0 + u * 32;
         float y[32];
@@ -738,7 +750,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] *= up[i];
         }
-        if (!is_fp32(kOut) && u == kUnits - 1) hand_back(buf);
+        if (!by_chunks(kOut) && u == kUnits - 1) hand_back(buf);
         if constexpr (!kGeglu) {
           if (p.e.act == PE_ACT_GELU) {
             apply_gelu<kOut>(y);
@@ -948,7 +960,7 @@ pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) 
   const size_t smem = sizeof(Smem) + 1024;
   static std::atomic<uint64_t> done{0};
   PE_TRY(allow_shared_memory(kernel, static_cast<int>(smem), done));
-  if (is_fp32(kOut)) {                     // the register split needs its registers
+  if (by_chunks(kOut)) {                     // the register split needs its registers
     static const int registers = [&] {
       cudaFuncAttributes attr;
       return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
@@ -980,6 +992,9 @@ pe_status launch_out(bool boxes, const Maps& maps, const Params& p, cudaStream_t
   if (p.e.out_fp32)
     return boxes ? launch_kernel<kOutFp32, kGeglu>(maps, p, stream)
                  : launch_kernel<kOutFp32Anywhere, kGeglu>(maps, p, stream);
+  if (p.slice_blocks + (p.slice_more ? 1 : 0) > kLongest)
+    return boxes ? launch_kernel<kOutBf16Long, kGeglu>(maps, p, stream)
+                 : launch_kernel<kOutBf16AnywhereLong, kGeglu>(maps, p, stream);
   return boxes ? launch_kernel<kOutBf16, kGeglu>(maps, p, stream)
                : launch_kernel<kOutBf16Anywhere, kGeglu>(maps, p, stream);
 }
