@@ -413,12 +413,15 @@ pe_status pe_geglu(pe_dtype dtype, const void* x, int64_t num_tokens, int32_t fe
  *     dW = dZ^T X    a = dZ transposed,  b = X transposed (residual: a sum so far).
  * PE_ACT_GEGLU: z has n = 2F columns, out [m, F] = gelu(z[:, :F]) * z[:, F:].
  * dtype is that of a and b: PE_BF16, or PE_FP32, whose numbers are split into three
- * bf16 parts and multiplied part by part on the tensor cores (six products; what is
- * left out is below 2^-23 of |a| |b|) or, where there are few, multiplied in fp32.
+ * bf16 parts (exactly from 2^-124 up, smaller ones to within 2^-148) and multiplied part by
+ * part on the tensor cores (six products; what is left out is below 2^-23 of |a| |b|) or,
+ * where there are few, multiplied in fp32.
  * Sums are fp32, in an order that depends on the sizes alone: the result is bitwise the same
- * in every run on a device. The tensor cores cut them off towards zero: an fp32 result loses
- * up to 5e-7 of the sum of its |a| |b|, a bf16 result up to 4e-5 before it is rounded. An infinity or
- * a NaN among fp32 operands makes every sum it enters NaN; bf16 operands follow IEEE.
+ * in every run on a device. The tensor cores cut them off towards zero: beside the rounding
+ * of its additions an fp32 result loses up to 5e-7 of the sum of its |a| |b|, a bf16 result up
+ * to 4e-5 before it is rounded. An infinity or a NaN among fp32 operands makes every sum it
+ * enters NaN, and a sum of fp32 operands whose |a| |b| leave fp32's range is infinite or NaN;
+ * bf16 operands follow IEEE.
  * Bias (n numbers), residual, out and pre are in out_dtype, out rounded once; bias,
  * residual and pre are nullable. Every *_ld is the number of elements from a stored row
  * to the next, at least the row's length (not looked at for a NULL tensor). bf16

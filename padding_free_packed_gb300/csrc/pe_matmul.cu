@@ -21,15 +21,18 @@ bool sizes_ok(int64_t m, int64_t n, int64_t k) {
 }
 
 // ---------------------------------------------------------------- parts of fp32 operands
-// x = h + m + l with h, m and l in bf16: h is x rounded to bf16 (cut off where that would
-// leave the range), m the rest rounded, l what is left of that. All differences are exact, and
-// l holds the last of x's 24 bits. An infinity or a NaN has NaN for all three, since the
-// products of an infinite h with another operand's parts of zero would be NaN in any case.
+// x = h + m / 2^7 + l / 2^14 with h, m and l in bf16: h is x rounded to bf16 (cut off where that
+// would leave the range), m the rest rounded, l what is left of that. All differences are exact,
+// and l holds the last of x's 24 bits. The rest is up to 2^-8 of x, and what is left up to 2^-17,
+// so held as they are they would lose bits below 2^-133, the last bit of bf16, from |x| = 2^-110
+// on; held that much larger none is above |x|, an |x| of 2^-124 or more loses nothing, and a
+// smaller one at most 2^-148. An infinity or a NaN has NaN for all three, since the products of
+// an infinite h with another operand's parts of zero would be NaN in any case.
 __device__ __forceinline__ void parts_of(float x, float& h, float& m, float& l) {
   const float r = __bfloat162float(__float2bfloat16_rn(x));
   h = fabsf(r) <= 3.3895314e38f ? r : __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-  m = __bfloat162float(__float2bfloat16_rn(x - h));
-  l = (x - h) - m;
+  m = __bfloat162float(__float2bfloat16_rn((x - h) * 0x1p7f));
+  l = ((x - h) - m * 0x1p-7f) * 0x1p14f;
   if (!(fabsf(x) <= 3.402823466e38f)) h = m = l = __uint_as_float(0x7fc00000u);
 }
 

@@ -47,14 +47,34 @@ struct LinearPlan {
 };
 
 constexpr int kMaxMatmulTerms = 6;
-// Products of parts of x = h + m + l, the smallest first: l h, h l, m m, m h, h m, h h. A part
-// is at most 2^-8 of the one before it, so what is left out is below 2^-23 of |a| |b|.
+// Products of parts of x = h + m / 2^7 + l / 2^14, the smallest first: l h, h l, m m, m h, h m,
+// h h. What a part stands for is at most 2^-8 of the one before it, so what is left out is below
+// 2^-23 of |a| |b|.
 __host__ __device__ __forceinline__ int32_t term_a(int32_t term, int32_t terms) {
   return (0x001102 >> (4 * (terms == 1 ? 5 : term))) & 3;
 }
 __host__ __device__ __forceinline__ int32_t term_b(int32_t term, int32_t terms) {
   return (0x010120 >> (4 * (terms == 1 ? 5 : term))) & 3;
 }
+
+// The blocks of k that one accumulator sums, a chain: `most` of them, and products of parts that
+// count for 2^-14, for 2^-7 and for 1 in chains of their own.
+struct Chains {
+  int32_t small_end, middle_end;     // one past the blocks that count for 2^-14, for 2^-7
+
+  __host__ static Chains of(int32_t term_blocks, int32_t terms) {
+    return terms == 1 ? Chains{0, 0} : Chains{3 * term_blocks, 5 * term_blocks};
+  }
+  // One past the last block of the chain from `block` on, in a sum that ends before `last`.
+  __device__ __forceinline__ int32_t end(int32_t block, int32_t last, int32_t most) const {
+    const int32_t end = last - block < most ? last : block + most;
+    const int32_t kind = block < small_end ? small_end : block < middle_end ? middle_end : end;
+    return kind < end ? kind : end;
+  }
+  __device__ __forceinline__ float weight(int32_t block) const {
+    return block < small_end ? 0x1p-14f : block < middle_end ? 0x1p-7f : 1.f;
+  }
+};
 
 // Tiles of 256 x 256 (or slices of their sums) on pairs of CTAs.
 size_t matmul_tiles_workspace(int64_t tiles, int32_t slices);

@@ -5,10 +5,10 @@
 // is narrow (128 rows of b, which is the MMA's M, by kT = 16, 32 or 64 rows of a, its N),
 // several blocks of k are in flight in a CTA, and a cluster of up to 8 CTAs shares the sum
 // over k, joined through distributed shared memory in the order of k (no workspace, no
-// second launch). An accumulator sums four blocks of k, which four warps then add to fp32
-// sums in registers (the tensor cores cut a sum off after every 16 products); at the end they
-// copy them to shared memory, and the cluster's CTAs deal out the rows among them: a lane
-// adds four neighbouring columns, finishes them and writes them. That part is one warp a
+// second launch). An accumulator sums four blocks of k (of fp32 operands' parts of one size),
+// which four warps then add to fp32 sums in registers (the tensor cores cut a sum off after
+// every 16 products); at the end they copy them to shared memory, and the cluster's CTAs deal
+// out the rows among them: a lane adds four neighbouring columns, finishes and writes them. That part is one warp a
 // scheduler or two, so it is bound by its instructions, not by memory: the activation is a
 // template's, and all eight warps take part.
 // With geglu the tile's rows of b are 64 of the gate's and the same 64 of the up part's.
@@ -60,6 +60,7 @@ struct Params {
   int32_t term_blocks;       // of one term
   int32_t terms;
   int32_t split;
+  Chains chains;
   int32_t a_transposed, b_transposed;
   int32_t up_row;            // geglu: b's first up row
   uint32_t idesc;
@@ -178,12 +179,15 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
     // ------------------------------------------------------------ MMA issue
     const uint32_t step_a = p.a_transposed ? 128 : 2, step_b = p.b_transposed ? 128 : 2;
     bool ok = true;
+    int32_t turn = -1, end = 0, buf = 0;
     for (int32_t i = 0; i < count; ++i) {
       const int stage = i % S;
       ok = warp_wait(smem_u32(&s.full[stage]), (i / S) & 1, guard, p.status, kSiteMma);
       if (!ok) break;
-      const int32_t turn = i / kChunk, buf = turn & 1;
-      if (i % kChunk == 0) {
+      const bool fresh = i == end;         // a chain begins
+      if (fresh) {
+        end = p.chains.end(lo + i, lo + count, kChunk) - lo;
+        buf = ++turn & 1;
         ok = warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
                        kSiteMma);
         if (!ok) break;
@@ -195,9 +199,9 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
 #pragma unroll
       for (int k = 0; k < 4; ++k)          // 16 elements of k each
         mma_ss_warp(tmem + buf * kT, db + k * step_b, da + k * step_a, p.idesc,
-                    i % kChunk > 0 || k > 0);
+                    !fresh || k > 0);
       tc_commit_warp(smem_u32(&s.empty[stage]));
-      if (i % kChunk == kChunk - 1 || i == count - 1) tc_commit_warp(smem_u32(&s.acc_full[buf]));
+      if (i == end - 1) tc_commit_warp(smem_u32(&s.acc_full[buf]));
     }
     tc_commit_warp(smem_u32(&s.drain));    // no MMA is in flight past this
     mbar_drain_wait(smem_u32(&s.drain), 0);
@@ -207,8 +211,11 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
 #pragma unroll
     for (int c = 0; c < kT; ++c) sum[c] = 0.f;
     bool ok = true;
-    for (int32_t turn = 0; turn * kChunk < count; ++turn) {
+    int32_t turn = 0;
+    for (int32_t block = lo; block < lo + count;
+         block = p.chains.end(block, lo + count, kChunk), ++turn) {
       const int buf = turn & 1;
+      const float weight = p.chains.weight(block);
       ok = warp_wait(smem_u32(&s.acc_full[buf]), (turn >> 1) & 1, guard, p.status,
                      kSiteEpilogue);
       if (!ok) break;
@@ -224,7 +231,7 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
         tmem_ld16(src, d);
         hand_back();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) sum[c] += __uint_as_float(d[c]);
+        for (int c = 0; c < 16; ++c) sum[c] = fmaf(__uint_as_float(d[c]), weight, sum[c]);
       } else {
 #pragma unroll
         for (int h = 0; h < kT; h += 32) {
@@ -233,7 +240,8 @@ matmul_narrow_kernel(const __grid_constant__ CUtensorMap tm_a,
           tmem_wait_ld(d);
           if (h + 32 == kT) hand_back();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sum[h + c] += __uint_as_float(d[c]);
+          for (int c = 0; c < 32; ++c)
+            sum[h + c] = fmaf(__uint_as_float(d[c]), weight, sum[h + c]);
         }
       }
     }
@@ -334,6 +342,7 @@ pe_status launch(const Matmul& q, int32_t split, DeviceStatus* status, cudaStrea
   p.term_blocks = (int32_t)ceil_div(q.k, kMatmulBlock);
   p.terms = q.planes == 3 ? kMaxMatmulTerms : 1;
   p.blocks = p.term_blocks * p.terms;
+  p.chains = Chains::of(p.term_blocks, p.terms);
   p.split = split;
   p.a_transposed = q.a.transposed ? 1 : 0;
   p.b_transposed = q.b.transposed ? 1 : 0;

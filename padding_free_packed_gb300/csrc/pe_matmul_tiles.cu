@@ -20,7 +20,8 @@
 // second their up rows, so that a thread finds both in its row of tensor memory.
 //
 // fp32 operands come as three bf16 parts each, and six products of parts, the smallest
-// first, are summed in the same accumulator, as six times as many blocks of k.
+// first, are summed like six times as many blocks of k, what parts of one size give in chains of
+// its own.
 //
 // Work: whole tiles in turn, or, where few tiles have long sums, slices of k, all tiles of a
 // slice before the next (so that the pairs read the same blocks of k at about the same
@@ -70,7 +71,7 @@ enum Out {
   kOutFp32 = 1,
   kOutBf16Anywhere = 2,
   kOutFp32Anywhere = 3,
-  kOutBf16Long = 4,                    // sums of more than kLongest blocks
+  kOutBf16Long = 4,                    // sums of more than kLongest blocks, or of parts
   kOutBf16AnywhereLong = 6
 };
 constexpr bool is_fp32(int out) { return out & 1; }
@@ -91,7 +92,6 @@ static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
 constexpr int32_t kLongest = 128;
 constexpr int32_t kChunk = 8;
 constexpr bool by_chunks(int out) { return is_fp32(out) || (out & kOutBf16Long); }
-constexpr int32_t chunk_of(int out) { return by_chunks(out) ? kChunk : 0x7fffffff; }
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 constexpr int kPartsAhead = 5, kPartBlocks = 4;          // parts in flight; blocks an SM
 
@@ -135,6 +135,7 @@ struct Params {
   int32_t blocks;            // of k, of all terms
   int32_t term_blocks;       // of one term
   int32_t terms;
+  Chains chains;
   int32_t a_transposed, b_transposed;
   int32_t up_row;            // geglu: b's first up row
   int32_t row_tiles;
@@ -542,7 +543,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       for (bool more = w.at(p, pair); more && ok; more = w.at(p, w.unit + pairs)) {
         for (int32_t block = w.first; block < w.last && ok; ++turn) {
           const uint32_t buf = turn & 1, d = tmem + buf * kTile;
-          const int32_t end = w.last - block < chunk_of(kOut) ? w.last : block + chunk_of(kOut);
+          const int32_t end = by_chunks(kOut) ? p.chains.end(block, w.last, kChunk) : w.last;
           uint32_t accumulate = 0;
           ok = eager_warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
                           kSiteMma);
@@ -650,8 +651,10 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       if constexpr (by_chunks(kOut)) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
-        for (int32_t block = w.first; block < w.last; block += kChunk, ++turn) {
+        for (int32_t block = w.first; block < w.last;
+             block = p.chains.end(block, w.last, kChunk), ++turn) {
           buf = turn & 1;
+          const float weight = p.chains.weight(block);
           ok = eager_warp_wait(smem_u32(&s.acc_full[buf]), (turn >> 1) & 1, guard, p.status,
                                kSiteEpilogue);
           if (!ok) break;
@@ -662,7 +665,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
             load_acc(columns(buf, u), z);
             if (u == 3) hand_back(buf);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[32 * u + i] += z[i];
+            for (int i = 0; i < 32; ++i) sum[32 * u + i] = fmaf(z[i], weight, sum[32 * u + i]);
           }
         }
       } else {
@@ -924,6 +927,7 @@ Params base_params(const Matmul& q) {
   p.term_blocks = (int32_t)ceil_div(q.k, kMatmulBlock);
   p.terms = q.planes == 3 ? kMaxMatmulTerms : 1;
   p.blocks = p.term_blocks * p.terms;
+  p.chains = Chains::of(p.term_blocks, p.terms);
   p.a_transposed = q.a.transposed ? 1 : 0;
   p.b_transposed = q.b.transposed ? 1 : 0;
   const bool geglu = q.e.act == PE_ACT_GEGLU;
@@ -992,7 +996,7 @@ pe_status launch_out(bool boxes, const Maps& maps, const Params& p, cudaStream_t
   if (p.e.out_fp32)
     return boxes ? launch_kernel<kOutFp32, kGeglu>(maps, p, stream)
                  : launch_kernel<kOutFp32Anywhere, kGeglu>(maps, p, stream);
-  if (p.slice_blocks + (p.slice_more ? 1 : 0) > kLongest)
+  if (p.terms > 1 || p.slice_blocks + (p.slice_more ? 1 : 0) > kLongest)
     return boxes ? launch_kernel<kOutBf16Long, kGeglu>(maps, p, stream)
                  : launch_kernel<kOutBf16AnywhereLong, kGeglu>(maps, p, stream);
   return boxes ? launch_kernel<kOutBf16, kGeglu>(maps, p, stream)
