@@ -172,8 +172,9 @@ pe_status launch(const Args<T>& a, cudaStream_t stream) {
                            dim3((unsigned)strips, (unsigned)lines), dim3(1, (unsigned)lines),
                            kThreads, 0, stream, few);
   }
-  static const int resident =
-      resident_blocks(activation_bwd_kernel<T, V, kAct, kRows>, kThreads, 0);
+  static DeviceNumber known;
+  const int resident =
+      resident_blocks(activation_bwd_kernel<T, V, kAct, kRows>, kThreads, 0, known);
   if (resident < 1) return PE_ERR_CUDA;
   int64_t most = (int64_t)device_sm_count() * resident / strips;
   if (most < 1) most = 1;

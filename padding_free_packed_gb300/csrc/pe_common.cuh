@@ -241,14 +241,43 @@ pe_status allow_shared_memory(K* kernel, int bytes, std::atomic<uint64_t>& done)
   return PE_OK;
 }
 
+// A positive number of every device, one object for each question. An answer of 0 (the question
+// failed, as any runtime call does after an asynchronous error) is not kept: the next call asks
+// again.
+class DeviceNumber {
+ public:
+  template <typename Ask>
+  int of(int device, Ask ask) {
+    if (device < 0 || device >= kDevices) return ask();
+    int number = known_[device].load();
+    if (number <= 0) {
+      number = ask();
+      if (number > 0) known_[device].store(number);
+    }
+    return number;
+  }
+  template <typename Ask>
+  int of_current(Ask ask) {
+    int device = 0;
+    return cudaGetDevice(&device) == cudaSuccess ? of(device, ask) : 0;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> known_[kDevices] = {};
+};
+
 // Blocks of a kernel that an SM holds at a time (0: the question failed). A grid of as many
 // on every SM has no last, partly filled turn.
 template <typename K>
-int resident_blocks(K* kernel, int threads, size_t smem) {
-  int blocks = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) != cudaSuccess)
-    return 0;
-  return blocks;
+int resident_blocks(K* kernel, int threads, size_t smem, DeviceNumber& known) {
+  return known.of_current([&] {
+    int blocks = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) ==
+                   cudaSuccess
+               ? blocks
+               : 0;
+  });
 }
 
 // Launches `grid` in clusters (of eight blocks at most, the portable size).

@@ -448,8 +448,9 @@ pe_status launch(const Args<T>& a, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     PE_TRY(allow_shared_memory(kernel, 2 * kMaxChannels * (int)sizeof(float), done));
   }
-  static const int resident =
-      resident_blocks(kernel, kGroup * kGroups, wide ? 2 * kMaxChannels * sizeof(float) : smem);
+  static DeviceNumber known;
+  const int resident = resident_blocks(
+      kernel, kGroup * kGroups, wide ? 2 * kMaxChannels * sizeof(float) : smem, known);
   return launch_blocks(kernel, a, kGroups, kGroup * kGroups, smem, resident,
                        wide ? kMaxWideBlocks : kMaxBlocks, stream);
 }

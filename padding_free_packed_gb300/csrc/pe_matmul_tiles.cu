@@ -965,10 +965,12 @@ pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) 
   static std::atomic<uint64_t> done{0};
   PE_TRY(allow_shared_memory(kernel, static_cast<int>(smem), done));
   if (by_chunks(kOut)) {                     // the register split needs its registers
-    static const int registers = [&] {
+    static DeviceNumber known;
+    const int registers = known.of_current([&] {
       cudaFuncAttributes attr;
       return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
-    }();
+    });
+    if (registers < 1) return PE_ERR_CUDA;
     if (static_cast<uint32_t>(registers) * kThreads < 128u * (kRegsLow + 2 * kRegsHigh))
       return PE_ERR_UNSUPPORTED;
   }
