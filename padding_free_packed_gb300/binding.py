@@ -814,9 +814,7 @@ def pe_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
     a_scales, b_scales = a_scales.contiguous(), b_scales.contiguous()
     out = _output(out, "out", (m, n), dtype if out is None else out.dtype, dev)
     need = lib.pe_matmul_fp8_workspace_size(m, n, k)
-    ws, ws_bytes = None, 0
-    if need or workspace is not None:
-        ws, ws_bytes = _workspace_for(workspace, need, dev)
+    ws, ws_bytes = _workspace_for(workspace, need, dev) if need else (None, 0)
     _call("pe_matmul_fp8", dev, a_code, a.data_ptr(), _fp8_ld(a), a_scales.data_ptr(), b_code,
           b.data_ptr(), _fp8_ld(b), b_scales.data_ptr(), m, n, k, _dtype_code(out.dtype),
           out.data_ptr(), _ptr(ws), ws_bytes)
