@@ -459,7 +459,7 @@ pe_status pe_matmul(pe_dtype dtype, const void* a, int64_t a_ld, int a_transpose
  * (the order of its sums goes by the width and by whether there are many rows).
  * Errors: PE_ERR_INVALID_ARG for negative sizes, channels < 1, eps that is not
  * finite and > 0, NULL required pointers; PE_ERR_UNSUPPORTED for other dtypes or
- * devices and more than 16384 channels. */
+ * devices, more than 16384 channels and tensors not aligned to their elements. */
 size_t pe_layernorm_bwd_workspace_size(int64_t num_tokens, int32_t channels);
 pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void* h, const void* weight,
                            const void* dresidual, int64_t num_tokens, int32_t channels, float eps,
@@ -477,8 +477,9 @@ pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void* h, const 
  * and dbias is the result.
  * Errors: PE_ERR_INVALID_ARG for negative rows, features < 1, another
  * activation, NULL required pointers or ones that have to be NULL, dz = dy with
- * PE_ACT_GEGLU; PE_ERR_OVERFLOW for 2^30 - 1024 features or more;
- * PE_ERR_UNSUPPORTED for other dtypes or devices. */
+ * PE_ACT_GEGLU; PE_ERR_OVERFLOW for more than 2^30 - 1024 features;
+ * PE_ERR_UNSUPPORTED for other dtypes or devices and tensors not aligned to their
+ * elements. */
 size_t pe_activation_bwd_workspace_size(pe_activation activation, int64_t rows, int32_t features);
 pe_status pe_activation_bwd(pe_dtype dtype, pe_activation activation, const void* dy,
                             const void* pre, int64_t rows, int32_t features, void* dz,
@@ -498,7 +499,8 @@ pe_status pe_activation_bwd(pe_dtype dtype, pe_activation activation, const void
  * launches. y may be x or residual.
  * Errors: PE_ERR_INVALID_ARG for a negative count, p outside [0, 1), NULL required
  * pointers; PE_ERR_OVERFLOW for more than 2^60 elements; PE_ERR_UNSUPPORTED for
- * other dtypes, devices or a device_offset that is not aligned. */
+ * other dtypes or devices, a device_offset that is not aligned and tensors not aligned
+ * to their elements. */
 pe_status pe_dropout(pe_dtype dtype, const void* x, const void* residual, int64_t count, double p,
                      uint64_t seed, uint64_t offset, const uint64_t* device_offset, void* y,
                      pe_stream_t stream);
@@ -520,7 +522,7 @@ pe_status pe_dropout(pe_dtype dtype, const void* x, const void* residual, int64_
  * not finite and > 1, num_axes outside 1 .. 4, sections that are negative or do not add
  * up, strides below a token's size, in place with two strides, NULL required pointers;
  * PE_ERR_OVERFLOW for more than 2^28 elements a token; PE_ERR_UNSUPPORTED for other
- * dtypes or devices. */
+ * dtypes or devices and tensors not aligned to their elements. */
 pe_status pe_rope_axes(pe_dtype dtype, const void* q, int64_t q_stride, void* q_out,
                        int64_t q_out_stride, int32_t q_heads, const void* k, int64_t k_stride,
                        void* k_out, int64_t k_out_stride, int32_t k_heads,

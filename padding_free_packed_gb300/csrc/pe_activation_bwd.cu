@@ -241,9 +241,11 @@ extern "C" pe_status pe_activation_bwd(pe_dtype dtype, pe_activation activation,
   if (!activation_ok(activation) || rows < 0 || features < 1) return PE_ERR_INVALID_ARG;
   if (features > kMaxFeatures) return PE_ERR_OVERFLOW;
   if (activation == PE_ACT_NONE && (pre || dz || !dbias)) return PE_ERR_INVALID_ARG;
+  if (!by_elements(PE_FP32, dbias)) return PE_ERR_UNSUPPORTED;
   if (rows > 0) {
     if (!dy || (activation != PE_ACT_NONE && (!pre || !dz))) return PE_ERR_INVALID_ARG;
     if (activation == PE_ACT_GEGLU && dz == dy) return PE_ERR_INVALID_ARG;
+    if (!by_elements(dtype, dy, pre, dz)) return PE_ERR_UNSUPPORTED;
     const size_t need =
         dbias ? pe_activation_bwd_workspace_size(activation, rows, features) : 0;
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))

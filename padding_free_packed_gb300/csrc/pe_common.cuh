@@ -31,6 +31,12 @@ __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + 
 inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
+// Whether tensors of a type start at multiples of its elements' size; null ones do.
+template <typename... P>
+bool by_elements(pe_dtype dtype, P... p) {
+  const uintptr_t size = dtype == PE_FP32 ? 4 : 2;
+  return (aligned(p, size) && ...);
+}
 
 // Element conversions to and from the fp32 compute type.
 __device__ __forceinline__ float to_f32(float x) { return x; }

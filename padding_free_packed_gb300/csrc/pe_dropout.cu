@@ -178,7 +178,8 @@ extern "C" pe_status pe_dropout(pe_dtype dtype, const void* x, const void* resid
   if (count > (1LL << 60)) return PE_ERR_OVERFLOW;
   if (count == 0) return PE_OK;
   if (!x || !y) return PE_ERR_INVALID_ARG;
-  if (!aligned(device_offset, 8)) return PE_ERR_UNSUPPORTED;
+  if (!aligned(device_offset, 8) || !by_elements(dtype, x, residual, y))
+    return PE_ERR_UNSUPPORTED;
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
   Draw d;
   uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);

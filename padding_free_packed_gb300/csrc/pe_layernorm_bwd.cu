@@ -545,9 +545,10 @@ extern "C" pe_status pe_layernorm_bwd(pe_dtype dtype, const void* dy, const void
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (dtype != PE_BF16 && dtype != PE_FP32) return PE_ERR_UNSUPPORTED;
   if (N < 0 || C < 1 || !(eps > 0.f) || !isfinite(eps) || !dweight) return PE_ERR_INVALID_ARG;
-  if (C > kMaxChannels) return PE_ERR_UNSUPPORTED;
+  if (C > kMaxChannels || !by_elements(PE_FP32, dweight, dbias)) return PE_ERR_UNSUPPORTED;
   if (N > 0) {
     if (!dy || !h || !weight || !dx) return PE_ERR_INVALID_ARG;
+    if (!by_elements(dtype, dy, h, weight, dresidual, dx)) return PE_ERR_UNSUPPORTED;
     const size_t need = pe_layernorm_bwd_workspace_size(N, C);
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
       return PE_ERR_WORKSPACE;

@@ -194,6 +194,9 @@ extern "C" pe_status pe_rope_axes(pe_dtype dtype, const void* q, int64_t q_strid
   const Tensor tk = {k, k_out, k_stride, k_out_stride, k_heads};
   if (!positions || !tensor_ok(tq, N, head_dim) || !tensor_ok(tk, N, head_dim))
     return PE_ERR_INVALID_ARG;
+  if ((q_heads && !by_elements(dtype, q, q_out)) || (k_heads && !by_elements(dtype, k, k_out)) ||
+      !by_elements(PE_FP32, positions))
+    return PE_ERR_UNSUPPORTED;
   if (!device_is_sm103()) return PE_ERR_UNSUPPORTED;
   const float sign = inverse ? -1.f : 1.f;
   if (dtype == PE_FP32)
