@@ -72,7 +72,8 @@ enum Out {
   kOutBf16Anywhere = 2,
   kOutFp32Anywhere = 3,
   kOutBf16Long = 4,                    // sums of more than kLongest blocks, or of parts
-  kOutBf16AnywhereLong = 6
+  kOutBf16AnywhereLong = 6,
+  kOutSlices = 8                       // sums of slices, finished elsewhere to fp32
 };
 constexpr bool is_fp32(int out) { return out & 1; }
 constexpr bool by_tma(int out) { return !(out & 2); }
@@ -85,13 +86,16 @@ static_assert(128 * (kRegsLow + 2 * kRegsHigh) <= kThreads * kRegsLaunch,
 // to the largest of them and cut them off towards zero, so a chain of additions of numbers of
 // one sign loses a share that grows with its length: k = 4096 1.1e-5 of the sum, 8192 3.2e-5,
 // 2^17 8e-4, 2^19 3.3e-3, which a result rounded to bf16 (2e-3 to 4e-3) shows. So results
-// rounded to bf16 have chains of kLongest blocks at most; fp32 results, and longer sums, add chains of kChunk in fp32
-// registers: 1.1e-7 of the sum of magnitudes lost in the mean, 3.5e-7 at most, whatever k
-// (elementary fp32 operations: 1.1e-5 at most over 32299). Of one accumulator a block takes
-// 516 cycles, of chains of eight 532 (32299 x 768 x 2304 to fp32), of four 560.
+// rounded to bf16 have chains of kLongest blocks at most; fp32 results, and longer sums, add
+// chains of eight in fp32 registers: 1.1e-7 of the sum of magnitudes lost in the mean, 3.5e-7 at
+// most, whatever k (elementary fp32 operations: 1.1e-5 at most over 32299). Of one accumulator
+// a block takes 516 cycles, of chains of eight 532 (32299 x 768 x 2304 to fp32 82 us), of four
+// 560 (89). The slices of fp32 results, weights' gradients, have an epilogue short enough for
+// chains of four: 2304 x 768 x 32299 in 78.5 us for 77.7, off by 2.5e-7 of the result's size for
+// 4.7e-7 (elementary fp32 operations 2.7e-7).
 constexpr int32_t kLongest = 128;
-constexpr int32_t kChunk = 8;
-constexpr bool by_chunks(int out) { return is_fp32(out) || (out & kOutBf16Long); }
+constexpr bool by_chunks(int out) { return out & (kOutFp32 | kOutBf16Long | kOutSlices); }
+constexpr int32_t chunk_of(int out) { return out & kOutSlices ? 4 : 8; }
 constexpr size_t kPartFloats = (size_t)kTile * kTile;
 constexpr int kPartsAhead = 5, kPartBlocks = 4;          // parts in flight; blocks an SM
 
@@ -543,7 +547,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       for (bool more = w.at(p, pair); more && ok; more = w.at(p, w.unit + pairs)) {
         for (int32_t block = w.first; block < w.last && ok; ++turn) {
           const uint32_t buf = turn & 1, d = tmem + buf * kTile;
-          const int32_t end = by_chunks(kOut) ? p.chains.end(block, w.last, kChunk) : w.last;
+          const int32_t end = by_chunks(kOut) ? p.chains.end(block, w.last, chunk_of(kOut)) : w.last;
           uint32_t accumulate = 0;
           ok = eager_warp_wait(smem_u32(&s.acc_empty[buf]), ((turn >> 1) & 1) ^ 1, guard, p.status,
                           kSiteMma);
@@ -601,7 +605,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       place(p, w.tile, tile_row, tile_col);
       const int32_t row0 = tile_row * kTile + row_in;
       const int32_t col0 = tile_col * kOutCols + half * (kOutCols / 2);
-      const bool whole = p.slices == 1;
+      const bool whole = kOut != kOutSlices && p.slices == 1;
       const bool stored = whole && row0 < p.e.m && col0 < p.e.n;
       bool loading = false;                // the box's residual is on its way
       auto load_residual = [&](int32_t col) {
@@ -622,19 +626,21 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
       // The bias of this half's 128 columns of the accumulator: with geglu 64 of the gate's,
       // then 64 of the up part's. The half's warps meet here for every segment, after a wait
       // that gave up too.
-      float* bias = s.bias[half];
-      named_barrier(1 + half, 128);        // the segment before has read its own
-      {
-        const int i = quad * 32 + lane;
-        float v = 0.f;
-        if (p.e.bias) {
-          const int32_t c = kGeglu ? col0 + (i & 63) : col0 + i;
-          if (c < p.e.n)
-            v = io_get(p.e.bias, kGeglu && i >= 64 ? (int64_t)p.up_row + c : c, is_fp32(kOut));
+      [[maybe_unused]] float* bias = s.bias[half];
+      if constexpr (kOut != kOutSlices) {
+        named_barrier(1 + half, 128);        // the segment before has read its own
+        {
+          const int i = quad * 32 + lane;
+          float v = 0.f;
+          if (p.e.bias) {
+            const int32_t c = kGeglu ? col0 + (i & 63) : col0 + i;
+            if (c < p.e.n)
+              v = io_get(p.e.bias, kGeglu && i >= 64 ? (int64_t)p.up_row + c : c, is_fp32(kOut));
+          }
+          bias[i] = v;
         }
-        bias[i] = v;
+        named_barrier(1 + half, 128);
       }
-      named_barrier(1 + half, 128);
       if (!ok) continue;
       // Columns of accumulator `buf`: 32 u .. of this half (with geglu u = 2, 3 are up's).
       auto columns = [&](uint32_t buf, int u) {
@@ -652,7 +658,7 @@ matmul_tiles_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P
 #pragma unroll
         for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
         for (int32_t block = w.first; block < w.last;
-             block = p.chains.end(block, w.last, kChunk), ++turn) {
+             block = p.chains.end(block, w.last, chunk_of(kOut)), ++turn) {
           buf = turn & 1;
           const float weight = p.chains.weight(block);
           ok = eager_warp_wait(smem_u32(&s.acc_full[buf]), (turn >> 1) & 1, guard, p.status,
@@ -995,6 +1001,7 @@ pe_status launch_kernel(const Maps& maps, const Params& p, cudaStream_t stream) 
 
 template <bool kGeglu>
 pe_status launch_out(bool boxes, const Maps& maps, const Params& p, cudaStream_t stream) {
+  if (p.e.out_fp32 && p.slices > 1) return launch_kernel<kOutSlices, kGeglu>(maps, p, stream);
   if (p.e.out_fp32)
     return boxes ? launch_kernel<kOutFp32, kGeglu>(maps, p, stream)
                  : launch_kernel<kOutFp32Anywhere, kGeglu>(maps, p, stream);
