@@ -885,7 +885,8 @@ def pe_matmul(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None
     N / 2] with geglu) in `dtype` (a's by default), or in `out` and its dtype. With `pre` [M,
     N], a b^T + bias is also written there. bias, residual and pre are in out's dtype. out
     may be residual; out, residual and pre may be parts of wider matrices. bf16 operands
-    whose rows do not start at multiples of 16 bytes are copied first."""
+    whose rows do not start at multiples of 16 bytes are copied first. geglu with
+    b_transposed needs N / 2 to be a multiple of 8."""
     act = _activation_code(activation)
     a, a_ld = _operand(a, "a")
     b, b_ld = _operand(b, "b")

@@ -8,7 +8,9 @@
 // Measured (GB300, device time): 169151 x 1024 bf16 with residual in 158 us (6.6 TB/s, 0.97 of
 // the measured copy rate), without 146 us (0.70: the generator's integer products are the
 // bound), 90487 x 512 fp32 with residual 82 us (1.0). Four loads in flight a thread instead
-// of two took 3 % more; products and comparisons one element at a time 9 %.
+// of two took 3 % more; products and comparisons one element at a time 9 %. Tensors that do not
+// start at multiples of 16 bytes go one element a thread, each with a whole block of four
+// words: 169151 x 1024 bf16 without residual 610 us (0.17), 90487 x 512 fp32 163 (0.33).
 #include <math.h>
 
 #include "pe_vec.cuh"

@@ -15,7 +15,10 @@
 // fp32 113 us (0.97). What bounds the narrower ones is a row's chain of two joint sums, with
 // the 8 to 24 warps an SM that the registers of a thread's own sums (two for each of its
 // channels) leave. In paired arithmetic 768 channels took 42 us where single fp32 operations
-// took 45. bf16 rows of odd width move two bytes at a time (20000 x 777 51 us, 0.36).
+// took 45. Further from the bound: fp32 rows past 2304 channels, without the ring (20000 x 3000
+// 174 us, 0.81, x 4096 207, 0.93), bf16 rows of odd width, which move two bytes at a time (20000
+// x 777 50 us, 0.37), and rows past 4096 channels, a block each with nothing in flight beside its
+// joint sums (10000 x 5120 bf16 353 us, 0.17, x 8192 468, 0.21; 5000 x 8192 fp32 213, 0.45).
 #include <math.h>
 
 #include "pe_vec.cuh"
@@ -389,7 +392,7 @@ layernorm_bwd_kernel(const Args<T> a) {
 // Rows that one cluster takes: six for each group of threads of its eight blocks, 16 channels
 // a thread. That saves a launch and a workspace, which cost the host more than the rows in
 // turn cost the device (320 x 500 fp32: 7.8 us on the device, with two launches 4.6; calls
-// in a row from Python 15.4 us, four less than with two launches).
+// in a row from Python 16 us, four less than with two launches).
 int32_t few_threads(int32_t C) {
   return C <= 512 ? 32 : C <= 1024 ? 64 : C <= 2048 ? 128 : 256;
 }

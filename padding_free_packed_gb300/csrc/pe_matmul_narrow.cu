@@ -13,8 +13,8 @@
 // template's, and all eight warps take part.
 // With geglu the tile's rows of b are 64 of the gate's and the same 64 of the up part's.
 //
-// Measured (GB300, device time, K = 768, bf16): 1 x 2304 in 5.2 us, 64 x 768 in 5.7, 128 x 2304
-// in 6.6, 320 x 1001 (K = 1140) in 8.0, of which a launch that does nothing is 2.3. A block
+// Measured (GB300, device time, K = 768, bf16): 1 x 2304 in 5.6 us, 64 x 768 in 5.8, 128 x 2304
+// in 6.6, 320 x 2304 in 8.4, 320 x 1001 (K = 1140) in 8.0, of which a launch that does nothing is 2.3. A block
 // of k takes 0.28 us in turn, the latency of its load through six stages.
 //
 //   warps 0-3   sums to shared memory

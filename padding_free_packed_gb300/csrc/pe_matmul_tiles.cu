@@ -44,7 +44,10 @@
 // Measured (GB300, device time of a burst): 32299 x 2304 x 768 bf16 in 66.6 us (1.72 PFLOP/s,
 // 0.89 of the measured dense bf16 rate), with geglu and pre 81 (1.41), 169151 x 1024 x 1024
 // with bias and residual 214 to 221 us (1.65; the tensor cores are busy for 0.905 of the
-// cycles), 2304 x 768 x 32299 to fp32 78 us (1.46). For seconds on end the power cap rules:
+// cycles), the input gradient 32299 x 768 x 2304 71 to 73 (1.6), 2304 x 768 x 32299 to fp32 78.5
+// (1.46), 90487 x 512 x 512 of fp32 180 beside the 73 that cut its operands into parts; with
+// results in fp32 gelu is 32 calls out of line for a thread and unit, 90487 x 1024 x 512 637 us
+// for 400. For seconds on end the power cap rules:
 // 77 us for the first, 238 for 169151 x 1024 x 1024, at 1.6 to 1.8 GHz.
 #include <type_traits>
 
